@@ -425,6 +425,143 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
                               float* a_scale_ws, int8_t* w_i8_ws, int out_dt, void* y, void* workspace,
                               int64_t workspace_bytes, void* stream);
 
+/*
+ * Attention over the projections' outputs, and the paged cache of keys and
+ * values that decode and verify steps read.  [FP8 card, "Model overview"]:
+ * 24 query heads sharing 4 key / value heads of width 256; ["Supported"]: BF16
+ * and 8-bit caches, speculative decoding.
+ *
+ * Conventions, beyond those above
+ *   - Queries, keys and values are BF16 rows [token][head][D], D = 64, 128 or
+ *     256, heads of a token back to back; `stride` is the distance in elements
+ *     between tokens (at least heads * D, a multiple of 8, below 2^24), so
+ *     that slices of a fused projection's output can be passed.  Query head h
+ *     reads KV head h / (Hq / Hkv).
+ *   - Sequences are packed one after another: sequence b owns the rows
+ *     cu[b] .. cu[b + 1] - 1 (int32 [B + 1], ascending).  These offsets, and
+ *     all lengths, tables and masks, are read on the device, when the work
+ *     runs; offsets outside the arrays are cut back to them.
+ *   - o [Tq][Hq][D] is FP32 or BF16 (out_dt); lse [Tq][Hq] FP32, or NULL:
+ *     the natural logarithm of the sum of exp(logits) (it joins this result
+ *     with attention over other keys).  A row that sees no key gets o = 0 and
+ *     lse = -infinity.  Keys and values that a row does not see do not touch
+ *     its result, whatever they hold, infinities and NaN included.
+ *   - Logits, softmax statistics and sums are FP32.  The weights of the
+ *     softmax are rounded to BF16 for a BF16 output, and to three BF16 terms
+ *     (22 bits) for an FP32 output.
+ *   - `scale` multiplies the logits; it must be finite and positive
+ *     (NQ_ERR_RANGE).
+ */
+
+/*
+ * Causal attention over packed prompts: query i of a sequence with n_q queries
+ * and n_k keys sees its keys j <= i + n_k - n_q (the queries are the last
+ * n_q of the n_k tokens, so a chunk of a prompt passes the keys of the chunks
+ * before it too; with n_q > n_k the first rows see nothing).
+ *   q [Tq][Hq][D], k / v [Tk][Hkv][D], cu_q / cu_k [B + 1]
+ * Query rows outside every sequence are not written.
+ * Errors: D, Hq % Hkv, strides -> NQ_ERR_SHAPE.
+ */
+nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                         const uint16_t* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                         int64_t B, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D, float scale,
+                         int out_dt, void* o, float* lse, void* stream);
+
+typedef enum {
+    NQ_KV_BF16 = 0,  /* BF16 rows */
+    NQ_KV_E4M3 = 1   /* E4M3 codes; a KV head's values are code * scale[head] (FP32 [Hkv], for K and for V) */
+} nq_kv_fmt;
+
+/*
+ * The cache.  A plane holds the keys, or the values, of one layer:
+ * [pages][Hkv][page_size][D], page_size a power of two from 16 to 4096 tokens.
+ * Token i of sequence b is row i % page_size of page
+ * page_table[b][i / page_size] (int32 [B][width], -1 where there is no page;
+ * width * page_size at most 2^30).  All planes share the page numbers.  A page
+ * number outside [0, pages) is never followed: its rows read as zeros and are
+ * not written.
+ *
+ * A step gives each sequence b the drafted tokens cu_q[b] .. cu_q[b + 1] - 1
+ * (one token in plain decoding); they follow its lens[b] committed tokens in
+ * the cache.
+ */
+
+/*
+ * The step's keys and values into the cache: token t of sequence b to position
+ * lens[b] + (t - cu[b]).  E4M3: e4m3_rne_sat(fp32(x / scale[head])).  Tokens
+ * past the table or without a page are dropped.
+ */
+nq_status nq_kv_append(int kv_fmt, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                       const float* k_scale, const float* v_scale, const int32_t* page_table, int64_t width,
+                       const int32_t* lens, const int32_t* cu, int64_t B, int64_t T, int64_t Hkv, int64_t D,
+                       int64_t page_size, int64_t pages, void* k_pages, void* v_pages, void* stream);
+
+/*
+ * Attention of the drafted tokens, which form a tree: token i of a sequence
+ * sees all committed tokens, and drafted token j (0 .. 63, counted from the
+ * sequence's first) where bit j of tree_mask[i] is set (uint64 [T]; bit i
+ * itself included or not, as given; bits past the sequence's drafted tokens
+ * are ignored).  The drafted tokens' keys and values are in the cache already.
+ *   max_q    the most drafted tokens of a sequence, 1 .. 64; later ones are
+ *            neither computed nor written
+ *   max_len  about the longest lens[b] + drafted tokens; it only shapes the
+ *            launch, every length gives the same result up to rounding
+ *   workspace, workspace_bytes   optional (nq_attn_tree_workspace_bytes): lets
+ *            a sequence's keys be split over workgroups.  It needs no
+ *            preparation and holds nothing between calls; calls that share it
+ *            must be ordered (the same stream)
+ * The result does not depend on timing: parts are joined in the order of
+ * their keys.
+ */
+int64_t nq_attn_tree_workspace_bytes(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
+nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                       const float* k_scale, const float* v_scale, const int32_t* page_table, int64_t width,
+                       const int32_t* lens, const int32_t* cu_q, const uint64_t* tree_mask, int64_t B,
+                       int64_t max_q, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size,
+                       int64_t pages, int64_t max_len, float scale, int out_dt, void* o, float* lse,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Accounting of pages, on the device, so that a step's launches can be queued
+ * (or captured) without waiting for it.  refs (int32 [pages]) counts the table
+ * entries that name each page; a page with count 0 is free.  Free pages are
+ * handed out lowest first, rows in order.  `shortfall` (int32) receives how
+ * many pages were wanted but not there; those entries stay -1.  `free_list`
+ * (int32 [pages]) is scratch.
+ *
+ * reserve: entries lens[b] / page_size .. ceil(new_lens[b] / page_size) - 1 of
+ *   row b that are negative get a page (count 1).  B at most 8192.
+ * release: entries from ceil(keep_lens[b] / page_size) on are given back and
+ *   become -1 (keep_lens[b] = 0: the whole row).
+ * fork: child c becomes a copy of row parents[c] up to lens[parents[c]]
+ *   tokens: whole pages are shared (counted), a last page that is partly
+ *   filled is replaced by a page of the child's own, and copies[c] = (parent's
+ *   page, child's page), or (-1, -1) where nothing is to be copied; the other
+ *   entries become -1.  What the child's row held before is not given back.
+ *   The child's rows may not overlap the parents'.
+ * copy_pages: page copies[i][0] to page copies[i][1] in each of `planes`
+ *   planes, plane_bytes apart; pairs with a number outside [0, pages) are
+ *   skipped.  No page may be written by one pair and named by another.
+ * compact: the end of a verify step.  accept (int32, the drafted tokens that
+ *   sequence b keeps, in order: accept[cu_accept[b]] ..) are moved together:
+ *   row lens[b] + accept[i] to row lens[b] + i, in every plane, for i below 64.
+ *   `accepted` is accept's length; rows without a page are skipped.
+ */
+nq_status nq_kv_reserve(int32_t* refs, int64_t pages, int32_t* page_table, int64_t width, const int32_t* lens,
+                        const int32_t* new_lens, int64_t B, int64_t page_size, int32_t* free_list,
+                        int32_t* shortfall, void* stream);
+nq_status nq_kv_release(int32_t* refs, int64_t pages, int32_t* page_table, int64_t width,
+                        const int32_t* keep_lens, int64_t B, int64_t page_size, void* stream);
+nq_status nq_kv_fork(int32_t* refs, int64_t pages, const int32_t* page_table, int64_t width, const int32_t* lens,
+                     int64_t B, const int32_t* parents, int64_t children, int64_t page_size, int32_t* child_table,
+                     int32_t* copies, int32_t* free_list, int32_t* shortfall, void* stream);
+nq_status nq_kv_copy_pages(void* pool, int64_t planes, int64_t plane_bytes, int64_t page_bytes, int64_t pages,
+                           const int32_t* copies, int64_t n, void* stream);
+nq_status nq_kv_compact(void* pool, int64_t planes, int64_t plane_bytes, int64_t Hkv, int64_t page_size,
+                        int64_t row_bytes, int64_t pages, const int32_t* page_table, int64_t width,
+                        const int32_t* lens, const int32_t* accept, const int32_t* cu_accept, int64_t B,
+                        int64_t accepted, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

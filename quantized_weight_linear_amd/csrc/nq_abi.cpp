@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "nq.h"
@@ -585,6 +586,166 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
         return from_hip(nq::launch_gemv_a8(nq::W_Q8G64, w_i8_ws, w_scale, a_q_ws, a_scale_ws, T, N, K, bf16, y,
                                            workspace, workspace ? workspace_bytes : 0, s, false));
     return from_hip(nq::launch_gemm_w8a8(a_q_ws, a_scale_ws, w_i8_ws, w_scale, T, N, K, bf16, y, nullptr, s));
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t I31 = (int64_t)1 << 31;
+constexpr int64_t MOST_BLOCKS = (int64_t)1 << 24;       // 256 threads each: below 2^32 threads a launch
+
+bool heads_ok(int64_t Hq, int64_t Hkv, int64_t D) {
+    return Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq < 65536 && (D == 64 || D == 128 || D == 256);
+}
+bool stride_ok(int64_t stride, int64_t heads, int64_t D) {
+    return stride >= heads * D && stride % 8 == 0 && stride < ((int64_t)1 << 24);
+}
+bool page_ok(int64_t page_size) { return page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0; }
+bool table_ok(int64_t B, int64_t width, int64_t page_size, int64_t pages) {
+    return B >= 0 && B < MOST_BLOCKS && width >= 0 && pages >= 0 && pages < I31 && page_ok(page_size) &&
+           width * page_size <= ((int64_t)1 << 30);
+}
+bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
+
+template <class... P>
+nq_status all_there(P... p) {
+    for (const void* x : {(const void*)p...})
+        if (x == nullptr) return NQ_ERR_NULL;
+    for (const void* x : {(const void*)p...})
+        if (!aligned16(x)) return NQ_ERR_ALIGN;
+    return NQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                         int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk,
+                         int64_t Hq, int64_t Hkv, int64_t D, float scale, int out_dt, void* o, float* lse, void* stream) {
+    if (B < 0 || Tq < 0 || Tk < 0 || B >= I31 || Tq >= I31 || Tk >= I31 || !heads_ok(Hq, Hkv, D)) return NQ_ERR_SHAPE;
+    if (!stride_ok(q_stride, Hq, D) || !stride_ok(k_stride, Hkv, D) || !stride_ok(v_stride, Hkv, D)) return NQ_ERR_SHAPE;
+    if ((Tq / 64 + (B < Tq ? B : Tq)) * Hq >= MOST_BLOCKS) return NQ_ERR_SHAPE;
+    if (!out_ok(out_dt)) return NQ_ERR_FORMAT;
+    if (!scale_ok(scale)) return NQ_ERR_RANGE;
+    if (B == 0 || Tq == 0) return NQ_OK;
+    NQ_TRY(all_there(q, cu_q, cu_k, o));
+    NQ_TRY(need(k, Tk));
+    NQ_TRY(need(v, Tk));
+    NQ_TRY(align_ok(k));
+    NQ_TRY(align_ok(v));
+    NQ_TRY(align_ok(lse));
+    return from_hip(nq::launch_attn_prompt(q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, scale,
+                                           out_dt == NQ_OUT_BF16, o, lse, as_stream(stream)));
+}
+
+nq_status nq_kv_append(int kv_fmt, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                       const float* k_scale, const float* v_scale, const int32_t* page_table, int64_t width,
+                       const int32_t* lens, const int32_t* cu, int64_t B, int64_t T, int64_t Hkv, int64_t D,
+                       int64_t page_size, int64_t pages, void* k_pages, void* v_pages, void* stream) {
+    if (kv_fmt != NQ_KV_BF16 && kv_fmt != NQ_KV_E4M3) return NQ_ERR_FORMAT;
+    if (T < 0 || T >= I31 || !heads_ok(Hkv, Hkv, D) || !table_ok(B, width, page_size, pages)) return NQ_ERR_SHAPE;
+    if (!stride_ok(k_stride, Hkv, D) || !stride_ok(v_stride, Hkv, D)) return NQ_ERR_SHAPE;
+    if (T * Hkv * D / (8 * 256) >= MOST_BLOCKS) return NQ_ERR_SHAPE;
+    if (B == 0 || T == 0 || width == 0 || pages == 0) return NQ_OK;
+    NQ_TRY(all_there(k, v, page_table, lens, cu, k_pages, v_pages));
+    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_there(k_scale, v_scale));
+    return from_hip(nq::launch_kv_append(kv_fmt == NQ_KV_E4M3, k, k_stride, v, v_stride, k_scale, v_scale, page_table, width,
+                                         lens, cu, B, T, Hkv, D, page_size, pages, k_pages, v_pages, as_stream(stream)));
+}
+
+int64_t nq_attn_tree_workspace_bytes(int64_t B, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len) {
+    if (B <= 0 || B >= MOST_BLOCKS || max_q < 1 || max_q > 64 || !heads_ok(Hq, Hkv, D) || max_len < 0) return 0;
+    return nq::attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len);
+}
+
+nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                       const float* k_scale, const float* v_scale, const int32_t* page_table, int64_t width,
+                       const int32_t* lens, const int32_t* cu_q, const uint64_t* tree_mask, int64_t B, int64_t max_q,
+                       int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t pages, int64_t max_len,
+                       float scale, int out_dt, void* o, float* lse, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+    if (kv_fmt != NQ_KV_BF16 && kv_fmt != NQ_KV_E4M3) return NQ_ERR_FORMAT;
+    if (!out_ok(out_dt)) return NQ_ERR_FORMAT;
+    if (T < 0 || T >= I31 || max_q < 1 || max_q > 64 || max_len < 0 || workspace_bytes < 0 || !heads_ok(Hq, Hkv, D) ||
+        !table_ok(B, width, page_size, pages) || !stride_ok(q_stride, Hq, D))
+        return NQ_ERR_SHAPE;
+    if (B * Hq * max_q >= MOST_BLOCKS) return NQ_ERR_SHAPE;
+    if (!scale_ok(scale)) return NQ_ERR_RANGE;
+    if (B == 0 || T == 0) return NQ_OK;
+    NQ_TRY(all_there(q, lens, cu_q, tree_mask, o));
+    NQ_TRY(need(page_table, width));
+    NQ_TRY(need(k_pages, pages));
+    NQ_TRY(need(v_pages, pages));
+    NQ_TRY(align_ok(page_table));
+    NQ_TRY(align_ok(k_pages));
+    NQ_TRY(align_ok(v_pages));
+    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_there(k_scale, v_scale));
+    NQ_TRY(align_ok(lse));
+    NQ_TRY(align_ok(workspace));
+    return from_hip(nq::launch_attn_tree(kv_fmt == NQ_KV_E4M3, q, q_stride, k_pages, v_pages, k_scale, v_scale, page_table,
+                                         width, lens, cu_q, tree_mask, B, max_q, T, Hq, Hkv, D, page_size, pages, max_len,
+                                         scale, out_dt == NQ_OUT_BF16, o, lse, workspace, workspace ? workspace_bytes : 0,
+                                         as_stream(stream)));
+}
+
+nq_status nq_kv_reserve(int32_t* refs, int64_t pages, int32_t* page_table, int64_t width, const int32_t* lens,
+                        const int32_t* new_lens, int64_t B, int64_t page_size, int32_t* free_list, int32_t* shortfall,
+                        void* stream) {
+    if (!table_ok(B, width, page_size, pages) || B > 8192 || B * width >= I31) return NQ_ERR_SHAPE;
+    NQ_TRY(all_there(shortfall));
+    if (B > 0 && width > 0) NQ_TRY(all_there(page_table, lens, new_lens));
+    if (pages > 0) NQ_TRY(all_there(refs, free_list));
+    return from_hip(nq::launch_kv_reserve(refs, pages, page_table, width, lens, new_lens, width > 0 ? B : 0, page_size, free_list, shortfall,
+                                          as_stream(stream)));
+}
+
+nq_status nq_kv_release(int32_t* refs, int64_t pages, int32_t* page_table, int64_t width, const int32_t* keep_lens,
+                        int64_t B, int64_t page_size, void* stream) {
+    if (!table_ok(B, width, page_size, pages) || width / 256 >= 65535) return NQ_ERR_SHAPE;
+    if (B == 0 || width == 0) return NQ_OK;
+    NQ_TRY(all_there(page_table, keep_lens));
+    if (pages > 0) NQ_TRY(all_there(refs));
+    return from_hip(nq::launch_kv_release(refs, pages, page_table, width, keep_lens, B, page_size, as_stream(stream)));
+}
+
+nq_status nq_kv_fork(int32_t* refs, int64_t pages, const int32_t* page_table, int64_t width, const int32_t* lens, int64_t B,
+                     const int32_t* parents, int64_t children, int64_t page_size, int32_t* child_table, int32_t* copies,
+                     int32_t* free_list, int32_t* shortfall, void* stream) {
+    if (!table_ok(B, width, page_size, pages) || width / 256 >= 65535 || children < 0 || children >= MOST_BLOCKS) return NQ_ERR_SHAPE;
+    if (children == 0) return NQ_OK;
+    NQ_TRY(all_there(parents, copies, shortfall));
+    if (B > 0) NQ_TRY(all_there(lens));
+    if (width > 0) NQ_TRY(all_there(child_table));
+    if (B > 0 && width > 0) NQ_TRY(all_there(page_table));
+    if (pages > 0) NQ_TRY(all_there(refs, free_list));
+    return from_hip(nq::launch_kv_fork(refs, pages, page_table, width, lens, B, parents, children, page_size, child_table,
+                                       copies, free_list, shortfall, as_stream(stream)));
+}
+
+nq_status nq_kv_copy_pages(void* pool, int64_t planes, int64_t plane_bytes, int64_t page_bytes, int64_t pages,
+                           const int32_t* copies, int64_t n, void* stream) {
+    if (planes < 0 || planes > 65535 || page_bytes < 0 || page_bytes % 16 != 0 || page_bytes >= I31 || pages < 0 ||
+        pages >= I31 || plane_bytes % 16 != 0 || (pages > 0 && plane_bytes / pages < page_bytes) || n < 0 ||
+        n * ((page_bytes + 16383) / 16384) >= MOST_BLOCKS)
+        return NQ_ERR_SHAPE;
+    if (planes == 0 || page_bytes == 0 || pages == 0 || n == 0) return NQ_OK;
+    NQ_TRY(all_there(pool, copies));
+    return from_hip(nq::launch_kv_copy_pages(pool, planes, plane_bytes, page_bytes, pages, copies, n, as_stream(stream)));
+}
+
+nq_status nq_kv_compact(void* pool, int64_t planes, int64_t plane_bytes, int64_t Hkv, int64_t page_size, int64_t row_bytes,
+                        int64_t pages, const int32_t* page_table, int64_t width, const int32_t* lens, const int32_t* accept,
+                        const int32_t* cu_accept, int64_t B, int64_t accepted, void* stream) {
+    if (!table_ok(B, width, page_size, pages) || planes < 0 || planes > 65535 || Hkv < 1 || Hkv >= 65536 || row_bytes < 16 ||
+        row_bytes % 16 != 0 || row_bytes > 512 || accepted < 0 || accepted >= I31 || plane_bytes % 16 != 0 ||
+        (pages > 0 && plane_bytes / pages < Hkv * page_size * row_bytes) || B * Hkv >= MOST_BLOCKS)
+        return NQ_ERR_SHAPE;
+    if (B == 0 || accepted == 0 || planes == 0 || pages == 0 || width == 0) return NQ_OK;
+    NQ_TRY(all_there(pool, page_table, lens, accept, cu_accept));
+    return from_hip(nq::launch_kv_compact(pool, planes, plane_bytes, Hkv, page_size, row_bytes, pages, page_table, width, lens,
+                                          accept, cu_accept, B, accepted, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,438 @@
+// Attention of drafted tokens over a paged cache (nq_attn_tree).
+//
+// The rows of one (sequence, KV head) are its drafted tokens times the query
+// heads that share the head, so every cached byte is read once for all of
+// them.  Few rows (up to 32: one token, or a few): the waves of a workgroup
+// take different keys, each through LDS of its own without barriers, and join
+// at the end.  More rows: the waves take different rows of the same keys.
+// Either way a sequence's keys are split over workgroups and the parts are
+// joined by a second small kernel, so that one long context uses every CU.
+// Bound by HBM: the cache's bytes once.
+#include <hip/hip_runtime.h>
+
+#include "nq.h"
+#include "nq_attn_rows.h"
+#include "nq_launch.h"
+
+namespace nq {
+namespace attn {
+
+struct TreeArgs {
+    const uint16_t* q;
+    int64_t qs;                     // elements between tokens
+    const void *k_pages, *v_pages;
+    const float *k_scale, *v_scale; // per KV head (E4M3 caches), or NULL
+    const int32_t* table;
+    int width;
+    const int32_t *lens, *cu;
+    const uint64_t* masks;
+    int seqs, max_q;
+    int64_t t;
+    int hq, hkv, group;
+    int page_shift;
+    int64_t pages;
+    float scale;
+    void* o;
+    float* lse;
+    float* parts;                   // split outputs, then (m c, l) pairs
+    int splits, chunk;              // at most `splits` ranges of at least `chunk` keys
+    int row_tiles;
+};
+
+// One sequence as the call describes it, kept inside its arrays.
+struct Seq {
+    int64_t t0;
+    int n, len, total;
+    __device__ __forceinline__ Seq(const TreeArgs& a, int b) {
+        int64_t x0 = a.cu[b], x1 = a.cu[b + 1];
+        x0 = x0 < 0 ? 0 : x0 > a.t ? a.t : x0;
+        x1 = x1 < x0 ? x0 : x1 > a.t ? a.t : x1;
+        t0 = x0;
+        n = (int)(x1 - x0 < a.max_q ? x1 - x0 : a.max_q);
+        const int64_t cap = (int64_t)a.width << a.page_shift;
+        int64_t ln = a.lens[b];
+        ln = ln < 0 ? 0 : ln > cap ? cap : ln;
+        len = (int)ln;
+        total = (int)(ln + n < cap ? ln + n : cap);
+    }
+};
+
+// How a sequence's keys are split: ranges of `chunk` keys, as many as asked
+// for at most (longer ranges where the sequence is longer than the caller said).
+struct Ranges {
+    int chunk, count;
+    __device__ __forceinline__ Ranges(const TreeArgs& a, int total) {
+        const int least = ((total + a.splits - 1) / a.splits + KEYS - 1) / KEYS * KEYS;
+        chunk = a.chunk > least ? a.chunk : least;
+        count = (total + chunk - 1) / chunk;
+    }
+};
+
+// K or V rows of one sequence and KV head in pages of (1 << page_shift) rows.
+// A page number outside the pool gives rows of zeros.
+template <int D, bool FP8>
+struct PagedRows {
+    const char *k, *v;
+    const int32_t* table;           // this sequence's row
+    int64_t pages;
+    int64_t page_bytes, head_bytes; // bytes of a page; of the heads before this one
+    int page_shift, total;
+    static constexpr int k_stride = Tile<D, FP8>::ROW, v_stride = Tile<D, FP8>::ROW;
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const char* base, int key) const {
+        int rows = total - key < 16 ? total - key : 16;
+        const int64_t page = rows > 0 ? table[key >> page_shift] : -1;
+        if (page < 0 || page >= pages) rows = 0;
+        const int64_t at = rows > 0 ? page * page_bytes + head_bytes + (int64_t)(key & ((1 << page_shift) - 1)) * k_stride : 0;
+        return rows_rsrc(base + at, rows, k_stride, k_stride);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t k_rows(int key) const { return rows(k, key); }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t v_rows(int key) const { return rows(v, key); }
+};
+
+template <int QB>
+struct TreeSees {
+    int len;                        // committed keys: seen by every row
+    uint64_t mask[QB];              // drafted keys that this lane's rows see
+    __device__ __forceinline__ int all_before() const { return len; }
+    __device__ __forceinline__ uint64_t seen(int b, int key) const {
+        const int at = len - key;   // where the drafted keys start among these 64
+        const uint64_t drafted = at >= 64 ? 0ull : at >= 0 ? mask[b] << at : at > -64 ? mask[b] >> -at : 0ull;
+        return bits_below(at) | drafted;
+    }
+};
+
+__device__ __forceinline__ int64_t part_row(const TreeArgs& a, int b, int kvh, int split, int row) {
+    return (((int64_t)b * a.hkv + kvh) * a.splits + split) * ((int64_t)a.max_q * a.group) + row;
+}
+__device__ __forceinline__ float2* part_sums(const TreeArgs& a, int d) {
+    return reinterpret_cast<float2*>(a.parts + (int64_t)a.seqs * a.hkv * a.splits * a.max_q * a.group * d);
+}
+
+// Rows [0, n group) of (b, kvh): token row / group, query head kvh group + row % group.
+template <int D, int QB, bool FP8, bool BF16OUT>
+struct TreeRows {
+    static constexpr bool SPLITP = !BF16OUT;
+    __device__ static void load(Rows<D, QB, FP8, SPLITP>& R, TreeSees<QB>& sees, const TreeArgs& a, const Seq& s, int kvh,
+                                const int (&row)[QB]) {
+        sees.len = s.len;
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            const bool real = row[i] < s.n * a.group;
+            const int tok = real ? row[i] / a.group : 0, head = kvh * a.group + (real ? row[i] % a.group : 0);
+            sees.mask[i] = real ? a.masks[s.t0 + tok] & bits_below(s.total - s.len) : ~0ull;
+            R.load_q(i, real ? a.q + (s.t0 + tok) * a.qs + (int64_t)head * D : nullptr);
+        }
+    }
+    // Results of one row block: outputs, or a part of them.
+    __device__ static void store(const Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int b, int kvh, int split,
+                                 bool only, int i, int row) {
+        const float l = halves_sum(R.l[i]);
+        const float mc = R.m[i] == -INFINITY ? 0.f : R.m[i] * R.c;
+        if (row >= s.n * a.group) return;
+        const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
+        const int64_t out = (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
+        const int64_t part = part_row(a, b, kvh, split, row);
+        const float f = only ? inverse_sum(l) * vs : 1.0f;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = R.o[i][d][4 * e] * f, x1 = R.o[i][d][4 * e + 1] * f, x2 = R.o[i][d][4 * e + 2] * f,
+                            x3 = R.o[i][d][4 * e + 3] * f;
+                if (only) store4<BF16OUT>(a.o, out * D + R.column(d, e), x0, x1, x2, x3);
+                else store4<false>(a.parts, part * D + R.column(d, e), x0, x1, x2, x3);
+            }
+        if (R.lane < 32) {
+            if (!only) part_sums(a, D)[part] = make_float2(mc, l);
+            else if (a.lse) a.lse[out] = log_sum_exp(mc, l);
+        }
+    }
+};
+
+template <int D, bool FP8>
+__device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const Seq& s, int b, int kvh) {
+    PagedRows<D, FP8> src;
+    src.k = (const char*)a.k_pages;
+    src.v = (const char*)a.v_pages;
+    src.table = a.table + (int64_t)b * a.width;
+    src.pages = a.pages;
+    src.head_bytes = ((int64_t)kvh << a.page_shift) * Tile<D, FP8>::ROW;
+    src.page_bytes = ((int64_t)a.hkv << a.page_shift) * Tile<D, FP8>::ROW;
+    src.page_shift = a.page_shift;
+    src.total = s.total;
+    return src;
+}
+
+// More than 32 rows: NW waves of 32 QB rows.
+template <int D, int QB, int KB, int NW, bool FP8, bool BF16OUT>
+__global__ __launch_bounds__(NW * 64) void attn_tree_rows_kernel(TreeArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int split = blockIdx.x % a.splits, rt = blockIdx.x / a.splits % a.row_tiles;
+    const int kvh = blockIdx.x / (a.splits * a.row_tiles) % a.hkv, b = blockIdx.x / (a.splits * a.row_tiles) / a.hkv;
+    const Seq s(a, b);
+    const Ranges r(a, s.total);
+    if (rt * NW * QB * 32 >= s.n * a.group) return;
+    if (split >= r.count && split > 0) return;          // (range 0 of an empty sequence writes its zeros)
+    const int key0 = split * r.chunk, key1 = key0 + r.chunk < s.total ? key0 + r.chunk : s.total;
+    Rows<D, QB, FP8, !BF16OUT> R;
+    R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
+    TreeSees<QB> sees;
+    int row[QB];
+#pragma unroll
+    for (int i = 0; i < QB; ++i) row[i] = ((rt * NW + wave) * QB + i) * 32 + (lane & 31);
+    TreeRows<D, QB, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
+    const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, b, kvh);
+    attend_rows<D, QB, KB, FP8, !BF16OUT, NW>(R, (lds_ptr)smem, key0, key1, src, sees, wave, lane);
+#pragma unroll
+    for (int i = 0; i < QB; ++i)
+        TreeRows<D, QB, FP8, BF16OUT>::store(R, a, s, b, kvh, split, r.count <= 1, i, row[i]);
+}
+
+// Up to 32 rows: wave w takes every NW-th tile of 32 keys of the range, with a
+// ring of RING tiles of its own in LDS.  K and V of a tile are waited for
+// separately: each slot is loaded again as soon as it has been read.
+template <int D, bool FP8, int NW>
+struct KeysLds {
+    static constexpr int TILE = 32 * Tile<D, FP8>::ROW;
+    static constexpr int RING = TILE >= 16384 ? 1 : TILE >= 8192 ? 2 : 4;
+    static constexpr int WAVE = 2 * RING * TILE;                    // 32 KiB (D = 64, E4M3: 16 KiB)
+    static constexpr int JOIN = NW * 32 * (D + 4) * 4;              // the waves' results at the end
+    static constexpr int BYTES = NW * WAVE > JOIN ? NW * WAVE : JOIN;
+};
+
+template <int D, int NW, bool FP8, bool BF16OUT>
+__global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
+    using L = KeysLds<D, FP8, NW>;
+    constexpr int LOADS = 2 * Tile<D, FP8>::LOADS16, R1 = (2 * L::RING - 1) * LOADS;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int split = blockIdx.x % a.splits, kvh = blockIdx.x / a.splits % a.hkv, b = blockIdx.x / a.splits / a.hkv;
+    const Seq s(a, b);
+    const Ranges r(a, s.total);
+    if (s.n == 0 || (split >= r.count && split > 0)) return;
+    const int key0 = split * r.chunk, key1 = key0 + r.chunk < s.total ? key0 + r.chunk : s.total;
+    Rows<D, 1, FP8, !BF16OUT> R;
+    R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
+    TreeSees<1> sees;
+    const int row[1] = {lane & 31};
+    TreeRows<D, 1, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
+    PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, b, kvh);
+    src.total = key1;                                   // keys past the range: no rows, zeros
+    const Stager<D, FP8> st(lane);
+    const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
+    auto load_k = [&](int key, int slot) {
+        st.rows16(src.k_rows(key), src.k_stride, mine + slot * 2 * L::TILE);
+        st.rows16(src.k_rows(key + 16), src.k_stride, mine + slot * 2 * L::TILE + L::TILE / 2);
+    };
+    auto load_v = [&](int key, int slot) {
+        st.rows16(src.v_rows(key), src.v_stride, mine + slot * 2 * L::TILE + L::TILE);
+        st.rows16(src.v_rows(key + 16), src.v_stride, mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
+    };
+    constexpr int STEP = NW * 32;
+    const int from = key0 + wave * 32;
+#pragma unroll
+    for (int i = 0; i < L::RING; ++i) {
+        load_k(from + i * STEP, i);
+        load_v(from + i * STEP, i);
+    }
+    int slot = 0;
+    for (int key = from; key < key1; key += STEP) {
+        const lds_ptr k = mine + slot * 2 * L::TILE, v = k + L::TILE;
+        v16f x[1][1];
+        wait_vm<R1>();
+        R.template logits<1>(k, x);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
+        load_k(key + L::RING * STEP, slot);
+        uint64_t seen[1] = {~0ull};
+        const bool partly = key + 32 > sees.all_before();
+        if (partly) {
+            seen[0] = sees.seen(0, key);
+            R.template hide<1>(x[0], seen[0]);
+        }
+        R.template softmax<1>(0, x[0]);
+        wait_vm<R1>();
+        if (partly && (rows16_not_finite<D, FP8>(v, lane) || rows16_not_finite<D, FP8>(v + L::TILE / 2, lane)))
+            R.template values_one_by_one<1>(v, x, seen);
+        else
+            R.template values<1>(v, x);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        load_v(key + L::RING * STEP, slot);
+        slot = slot + 1 == L::RING ? 0 : slot + 1;
+    }
+    // The waves' rows, joined: wave w's results go to LDS and every wave
+    // finishes D / NW columns' worth of each row.
+    wait_vm<0>();
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(smem);
+    constexpr int PITCH = D + 4;                        // floats a row
+    const float l = halves_sum(R.l[0]);
+    float* at = join + (wave * 32 + (lane & 31)) * PITCH;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<v4f*>(at + R.column(d, e)) =
+                v4f{R.o[0][d][4 * e], R.o[0][d][4 * e + 1], R.o[0][d][4 * e + 2], R.o[0][d][4 * e + 3]};
+    if (lane < 32) {
+        at[D] = R.m[0] == -INFINITY ? -INFINITY : R.m[0] * R.c;
+        at[D + 1] = l;
+    }
+    __syncthreads();
+    const bool only = r.count <= 1;
+    const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
+    constexpr int LANES = D / 4;                        // threads a row
+    for (int i = threadIdx.x / LANES; i < s.n * a.group; i += NW * 64 / LANES) {
+        const int col = threadIdx.x % LANES * 4;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = max2(top, join[(w * 32 + i) * PITCH + D]);
+        v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float* p = join + (w * 32 + i) * PITCH;
+            const float lw = p[D + 1];
+            // a wave that saw nothing has neither sum nor outputs
+            const float f = lw == 0.f ? 0.f : __builtin_amdgcn_exp2f(p[D] == -INFINITY ? 0.f : p[D] - top);
+            const v4f y = *reinterpret_cast<const v4f*>(p + col);
+            sum += lw * f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] += y[j] * f;
+        }
+        const float mc = top == -INFINITY ? 0.f : top;
+        const int64_t out = (s.t0 + i / a.group) * a.hq + kvh * a.group + i % a.group;
+        const int64_t part = part_row(a, b, kvh, split, i);
+        const float f = only ? inverse_sum(sum) * vs : 1.0f;
+        if (only) store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        else store4<false>(a.parts, part * D + col, x[0], x[1], x[2], x[3]);
+        if (col == 0) {
+            if (!only) part_sums(a, D)[part] = make_float2(mc, sum);
+            else if (a.lse) a.lse[out] = log_sum_exp(mc, sum);
+        }
+    }
+}
+
+// The parts of a row, joined in the order of their keys (one result whatever
+// the order in which the parts were made).  One workgroup a row: wave w sums
+// every fourth part, then the waves are added.
+template <int D, bool BF16OUT>
+__global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a) {
+    __shared__ float top_s[4], sum_s[4];
+    __shared__ __align__(16) float o_s[4][D];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rows = a.max_q * a.group;
+    const int row = blockIdx.x % rows, kvh = blockIdx.x / rows % a.hkv, b = blockIdx.x / rows / a.hkv;
+    const Seq s(a, b);
+    const Ranges r(a, s.total);
+    if (row >= s.n * a.group || r.count <= 1) return;
+    const float2* ml = part_sums(a, D);
+    constexpr int W = D / 64;                           // columns a lane: 1, 2 or 4
+    float top = -INFINITY;
+    for (int i = lane; i < r.count; i += 64) {
+        const float2 p = ml[part_row(a, b, kvh, i, row)];
+        if (p.y != 0.f) top = max2(top, p.x);
+    }
+    top = wave_max(top);
+    float sum = 0.f, x[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) x[j] = 0.f;
+    for (int i = wave; i < r.count; i += 4) {
+        const int64_t at = part_row(a, b, kvh, i, row);
+        const float2 p = ml[at];
+        const float f = p.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(p.x - top);
+        sum += p.y * f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) x[j] += a.parts[at * D + lane * W + j] * f;
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) o_s[wave][lane * W + j] = x[j];
+    if (lane == 0) sum_s[wave] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+    sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+    const float f = inverse_sum(sum) * (a.v_scale ? a.v_scale[kvh] : 1.0f);
+    const int64_t out = (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const int col = lane * W + j;
+        const float y = (o_s[0][col] + o_s[1][col] + o_s[2][col] + o_s[3][col]) * f;
+        if constexpr (BF16OUT) reinterpret_cast<uint16_t*>(a.o)[out * D + col] = (uint16_t)f32_to_bf16_rne(y);
+        else reinterpret_cast<float*>(a.o)[out * D + col] = y;
+    }
+    if (lane == 0 && a.lse) a.lse[out] = log_sum_exp(top == -INFINITY ? 0.f : top, sum);
+}
+
+template <class K>
+hipError_t set_lds(K kernel, int bytes) {
+    return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int D, bool FP8, bool BF16OUT>
+hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
+    const unsigned units = (unsigned)a.seqs * a.hkv * a.splits;
+    if (a.max_q * a.group <= 32) {
+        constexpr int LDS = KeysLds<D, FP8, 4>::BYTES;
+        auto kernel = attn_tree_keys_kernel<D, 4, FP8, BF16OUT>;
+        if (hipError_t e = set_lds(kernel, LDS); e != hipSuccess) return e;
+        kernel<<<units, 256, LDS, stream>>>(a);
+    } else {
+        constexpr int LDS = RowsLds<D, FP8, 4>::BYTES;
+        auto kernel = attn_tree_rows_kernel<D, 1, 2, 4, FP8, BF16OUT>;
+        if (hipError_t e = set_lds(kernel, LDS); e != hipSuccess) return e;
+        kernel<<<units * a.row_tiles, 256, LDS, stream>>>(a);
+    }
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (a.splits > 1) {
+        attn_tree_join_kernel<D, BF16OUT><<<(unsigned)a.seqs * a.hkv * a.max_q * a.group, 256, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+}  // namespace attn
+
+// Ranges a sequence's keys are split into: enough workgroups for two rounds of
+// the CUs, none shorter than 256 keys.
+static int tree_splits(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t max_len) {
+    const int64_t rows = max_q * (hq / hkv), tiles = rows <= 32 ? 1 : (rows + 127) / 128;
+    const int64_t units = seqs * hkv * tiles, want = 2 * (int64_t)device_cu_count();
+    int64_t splits = (want + units - 1) / units;
+    const int64_t most = (max_len + 255) / 256;
+    if (splits > most) splits = most;
+    return (int)(splits < 1 ? 1 : splits > 1024 ? 1024 : splits);
+}
+
+int64_t attn_tree_workspace_bytes(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
+    const int64_t splits = tree_splits(seqs, max_q, hq, hkv, max_len);
+    return splits <= 1 ? 0 : seqs * hq * max_q * splits * (d * 4 + 8);
+}
+
+hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                            const float* k_scale, const float* v_scale, const int32_t* table, int64_t width,
+                            const int32_t* lens, const int32_t* cu_q, const uint64_t* masks, int64_t seqs, int64_t max_q,
+                            int64_t t, int64_t hq, int64_t hkv, int64_t d, int64_t page_size, int64_t pages,
+                            int64_t max_len, float scale, bool bf16_out, void* o, float* lse, void* workspace,
+                            int64_t workspace_bytes, hipStream_t stream) {
+    using namespace attn;
+    int splits = tree_splits(seqs, max_q, hq, hkv, max_len);
+    if (splits > 1 && workspace_bytes < attn_tree_workspace_bytes(seqs, max_q, hq, hkv, d, max_len)) splits = 1;
+    const int64_t rows = max_q * (hq / hkv);
+    const int chunk = (int)(((max_len + splits - 1) / splits + KEYS - 1) / KEYS * KEYS);
+    const TreeArgs a{q, q_stride, k_pages, v_pages, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, table, (int)width, lens,
+                     cu_q, masks, (int)seqs, (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size),
+                     pages, scale, o, lse, reinterpret_cast<float*>(workspace), splits, chunk < KEYS ? KEYS : chunk,
+                     rows <= 32 ? 1 : (int)((rows + 127) / 128)};
+    switch (d) {
+        case 64:
+            return fp8 ? (bf16_out ? go_tree<64, true, true>(a, stream) : go_tree<64, true, false>(a, stream))
+                       : (bf16_out ? go_tree<64, false, true>(a, stream) : go_tree<64, false, false>(a, stream));
+        case 128:
+            return fp8 ? (bf16_out ? go_tree<128, true, true>(a, stream) : go_tree<128, true, false>(a, stream))
+                       : (bf16_out ? go_tree<128, false, true>(a, stream) : go_tree<128, false, false>(a, stream));
+        default:
+            return fp8 ? (bf16_out ? go_tree<256, true, true>(a, stream) : go_tree<256, true, false>(a, stream))
+                       : (bf16_out ? go_tree<256, false, true>(a, stream) : go_tree<256, false, false>(a, stream));
+    }
+}
+
+}  // namespace nq

@@ -22,9 +22,10 @@ NQ_W_Q4G64_F16S, NQ_W_Q8G32_F16S, NQ_W_Q8G64_F16S, NQ_W_MXFP8_G32, NQ_W_BF16 = r
 NQ_W_Q3G64_F16S, NQ_W_Q5G64_F16S, NQ_W_Q6G64_F16S = 5, 6, 7
 NQ_ROUTE_BF16, NQ_ROUTE_A8, NQ_ROUTE_A8_DECODE = 0, 1, 2
 NQ_A8_PREFILL, NQ_A8_DECODE = 1, 2
+NQ_KV_BF16, NQ_KV_E4M3 = 0, 1
 
 # every entry point the header declares: name -> (restype, argtypes)
-_P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+_P, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
     "nq_abi_version": (ctypes.c_int, []),
     "nq_status_string": (ctypes.c_char_p, [_I]),
@@ -55,6 +56,16 @@ SIGNATURES = {
     "nq_linear_q8g64": (_I, [_P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _I, _P, _P, _I64, _P]),
     "nq_unpack_q4_to_int8": (_I, [_P, _I64, _I64, _P, _P]),
     "nq_linear_q4g64": (_I, [_P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _P, _I, _P, _P, _I64, _P]),
+    "nq_attn_prompt": (_I, [_P, _I64] * 3 + [_P, _P] + [_I64] * 6 + [_F, _I, _P, _P, _P]),
+    "nq_kv_append": (_I, [_I] + [_P, _I64] * 2 + [_P, _P, _P, _I64, _P, _P] + [_I64] * 6 + [_P, _P, _P]),
+    "nq_attn_tree_workspace_bytes": (_I64, [_I64] * 6),
+    "nq_attn_tree": (_I, [_I, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _P] + [_I64] * 9 +
+                     [_F, _I, _P, _P, _P, _I64, _P]),
+    "nq_kv_reserve": (_I, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P]),
+    "nq_kv_release": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _P]),
+    "nq_kv_fork": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P]),
+    "nq_kv_copy_pages": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _P]),
+    "nq_kv_compact": (_I, [_P] + [_I64] * 6 + [_P, _I64, _P, _P, _P, _I64, _I64, _P]),
 }
 
 _lib = None
@@ -345,3 +356,150 @@ def nq_linear_qbits_g64(fmt, x, T, w_codes, w_scale, N, K, a8, a_q_ws, a_scale_w
     _check(lib().nq_linear_qbits_g64(fmt, _ptr(x), T, _ptr(w_codes), _ptr(w_scale), N, K, _a8_flags(a8),
                                      _ptr(a_q_ws), _ptr(a_scale_ws), _ptr(w_i8_ws), _out_dt(y), _ptr(y), wp, wb,
                                      _stream(x, w_codes)), "nq_linear_qbits_g64")
+
+
+# ---------------------------------------------------------------------------
+# Attention and the paged cache.  Sizes come from the tensors' shapes: rows
+# [T][heads][D] (a slice of a wider row is fine: heads back to back, any
+# distance between tokens), planes [pages][Hkv][page_size][D], pools of planes
+# [planes][pages][Hkv][page_size][D], tables [B][width].
+# ---------------------------------------------------------------------------
+
+def _rows(t, what):
+    """Address and token stride of rows [T][heads][D]."""
+    if t.dim() != 3 or t.element_size() != 2:
+        raise ValueError(f"{what}: BF16 rows [T][heads][D] expected")
+    n, h, d = t.shape
+    if n == 0:
+        return None, h * d
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) < h * d):
+        raise ValueError(f"{what}: a token's heads must be back to back")
+    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+
+
+def _ints(t, n, what, size=4):
+    """Address of at least n integers of `size` bytes."""
+    if t is None or t.element_size() != size or t.is_floating_point():
+        raise ValueError(f"{what}: integers of {size} bytes expected")
+    _size(t, n * size, what)
+    return _ptr(t)
+
+
+def _floats(t, n, what):
+    if t is not None and t.dtype != torch.float32:
+        raise ValueError(f"{what}: float32 expected")
+    _size(t, 4 * n, what)
+    return _ptr(t)
+
+
+def _table(t):
+    if t.dim() != 2:
+        raise ValueError("page table: [B][width] expected")
+    return _ints(t, t.numel(), "page table"), t.shape[0], t.shape[1]
+
+
+def _planes(fmt, k_pages, v_pages, hkv, d):
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != hkv or k_pages.shape[3] != d:
+        raise ValueError("pages: [pages][Hkv][page_size][D] expected, the same for keys and values")
+    if k_pages.element_size() != v_pages.element_size() or k_pages.element_size() != (1 if fmt == NQ_KV_E4M3 else 2):
+        raise ValueError("pages: one byte an element for E4M3, two for BF16")
+    return _ptr(k_pages), _ptr(v_pages), k_pages.shape[2], k_pages.shape[0]
+
+
+def _same(o, q):
+    if o.shape != q.shape:
+        raise ValueError("o: the shape of q expected")
+    return _ptr(o)
+
+
+def nq_attn_prompt(q, k, v, cu_q, cu_k, scale, o, lse=None):
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    if k.shape != v.shape or k.shape[2] != q.shape[2] or cu_q.numel() != cu_k.numel():
+        raise ValueError("q, k and v must have the same D, k and v the same shape, cu_q and cu_k the same length")
+    (tq, hq, d), (tk, hkv, _), b = q.shape, k.shape, max(0, cu_q.numel() - 1)
+    _check(lib().nq_attn_prompt(qp, qs, kp, ks, vp, vs, _ints(cu_q, b + 1 if b else 0, "cu_q"), _ints(cu_k, b + 1 if b else 0, "cu_k"),
+                                b, tq, tk, hq, hkv, d, scale, _out_dt(o), _same(o, q),
+                                _floats(lse, 0 if lse is None else tq * hq, "lse"), _stream(q)), "nq_attn_prompt")
+
+
+def nq_kv_append(fmt, k, v, k_scale, v_scale, page_table, lens, cu, k_pages, v_pages):
+    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    t, hkv, d = k.shape
+    (tp, b, width), (kpp, vpp, ps, pages) = _table(page_table), _planes(fmt, k_pages, v_pages, hkv, d)
+    n = hkv if fmt == NQ_KV_E4M3 else 0
+    _check(lib().nq_kv_append(fmt, kp, ks, vp, vs, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"), tp, width,
+                              _ints(lens, b, "lens"), _ints(cu, b + 1, "cu"), b, t, hkv, d, ps, pages, kpp, vpp,
+                              _stream(k, k_pages)), "nq_kv_append")
+
+
+def nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len):
+    return lib().nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len)
+
+
+def alloc_attn_tree_workspace(B, max_q, Hq, Hkv, D, max_len, device):
+    """A workspace for nq_attn_tree at these sizes, or None where it needs none."""
+    n = nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def nq_attn_tree(fmt, q, k_pages, v_pages, k_scale, v_scale, page_table, lens, cu_q, tree_mask, max_q, max_len, scale, o,
+                 lse=None, workspace=None):
+    qp, qs = _rows(q, "q")
+    t, hq, d = q.shape
+    hkv = k_pages.shape[1] if k_pages.dim() == 4 else 0
+    (tp, b, width), (kpp, vpp, ps, pages) = _table(page_table), _planes(fmt, k_pages, v_pages, hkv, d)
+    n = hkv if fmt == NQ_KV_E4M3 else 0
+    wp, wb = _ws(workspace)
+    _check(lib().nq_attn_tree(fmt, qp, qs, kpp, vpp, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"), tp, width,
+                              _ints(lens, b, "lens"), _ints(cu_q, b + 1, "cu_q"), _ints(tree_mask, t, "tree_mask", 8), b,
+                              max_q, t, hq, hkv, d, ps, pages, max_len, scale, _out_dt(o), _same(o, q),
+                              _floats(lse, 0 if lse is None else t * hq, "lse"), wp, wb, _stream(q)), "nq_attn_tree")
+
+
+def nq_kv_reserve(refs, page_table, lens, new_lens, page_size, free_list, shortfall):
+    (tp, b, width), pages = _table(page_table), refs.numel()
+    _check(lib().nq_kv_reserve(_ints(refs, pages, "refs"), pages, tp, width, _ints(lens, b, "lens"),
+                               _ints(new_lens, b, "new_lens"), b, page_size, _ints(free_list, pages, "free_list"),
+                               _ints(shortfall, 1, "shortfall"), _stream(refs)), "nq_kv_reserve")
+
+
+def nq_kv_release(refs, page_table, keep_lens, page_size):
+    (tp, b, width), pages = _table(page_table), refs.numel()
+    _check(lib().nq_kv_release(_ints(refs, pages, "refs"), pages, tp, width, _ints(keep_lens, b, "keep_lens"), b, page_size,
+                               _stream(refs)), "nq_kv_release")
+
+
+def nq_kv_fork(refs, page_table, lens, parents, page_size, child_table, copies, free_list, shortfall):
+    (tp, b, width), (cp, children, cwidth), pages = _table(page_table), _table(child_table), refs.numel()
+    if cwidth != width or parents.numel() != children:
+        raise ValueError("child_table: [children][width] expected")
+    _check(lib().nq_kv_fork(_ints(refs, pages, "refs"), pages, tp, width, _ints(lens, b, "lens"), b,
+                            _ints(parents, children, "parents"), children, page_size, cp,
+                            _ints(copies, 2 * children, "copies"), _ints(free_list, pages, "free_list"),
+                            _ints(shortfall, 1, "shortfall"), _stream(refs)), "nq_kv_fork")
+
+
+def _pool(pool):
+    """Address, planes, bytes of a plane and of a page, pages of [planes][pages][Hkv][page_size][D]."""
+    if pool.dim() != 5:
+        raise ValueError("pool: [planes][pages][Hkv][page_size][D] expected")
+    planes, pages, h, ps, d = pool.shape
+    page = h * ps * d * pool.element_size()
+    return _ptr(pool), planes, pages * page, page, pages
+
+
+def nq_kv_copy_pages(pool, copies):
+    p, planes, plane, page, pages = _pool(pool)
+    n = copies.numel() // 2
+    _check(lib().nq_kv_copy_pages(p, planes, plane, page, pages, _ints(copies, 2 * n, "copies"), n, _stream(pool)),
+           "nq_kv_copy_pages")
+
+
+def nq_kv_compact(pool, page_table, lens, accept, cu_accept):
+    (p, planes, plane, _, pages), (tp, b, width) = _pool(pool), _table(page_table)
+    _, _, h, ps, d = pool.shape
+    _check(lib().nq_kv_compact(p, planes, plane, h, ps, d * pool.element_size(), pages, tp, width, _ints(lens, b, "lens"),
+                               _ints(accept, accept.numel(), "accept"), _ints(cu_accept, b + 1, "cu_accept"), b,
+                               accept.numel(), _stream(pool)), "nq_kv_compact")
