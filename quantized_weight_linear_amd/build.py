@@ -40,10 +40,10 @@ def hipcc():
     raise RuntimeError("hipcc not found (ROCm is required to build libnq.so)")
 
 
-# Per-source additions.  The GEMM and the GEMVs keep their MFMA results in
+# Per-source additions.  The GEMM, the GEMVs and attention keep their MFMA results in
 # ordinary VGPRs, where the FP32 rescales read them directly (no copy out of
 # AGPRs per element; measured 5-12 % faster on the grouped GEMV formats).
-EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in SOURCES if name.startswith(("nq_gemm", "nq_gemv"))}
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in SOURCES if name.startswith(("nq_gemm", "nq_gemv", "nq_attn"))}
 
 
 def _compile(src, verbose):

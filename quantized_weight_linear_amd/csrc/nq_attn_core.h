@@ -4,8 +4,8 @@
 // A wave holds 32 query rows per block (QB blocks) as the columns of its
 // products.  For 32 keys at a time it forms S^T = K Q^T, so that lane l has
 // the logits of query row l % 32 in its own registers (16 of the 32 keys, the
-// other half in lane l ^ 32): the running maximum and sum of the softmax are
-// one value per lane, and one exchange between the wave's halves joins them.
+// other half in lane l ^ 32): the reference and sum of the softmax are one
+// value per lane, and one exchange between the wave's halves joins the maxima.
 // P^T, rounded to BF16 in those same registers, is already the right operand
 // of O^T += V^T P^T: the products sum over the keys in whatever order both
 // operands give them, so V^T is read in the order that S^T's rows come in.
@@ -14,11 +14,10 @@
 //   x_j = c <q, k_j> (c = scale log2 e),  p_j = 2^(x_j - m),  l = sum p_j,
 //   o = sum p_j v_j / l,  log-sum-exp = (m + log2 l) ln 2
 //
-// m is a running upper reference, not the exact maximum: it moves only when a
-// new logit passes it by more than RESCALE_LOG2 (p then stays below
-// 2^RESCALE_LOG2, far from FP32's and BF16's range, and every rounding is
-// relative), so the accumulators are rescaled a few times per row and not once
-// per tile.  Sums, m and l are FP32.  P is rounded once to BF16 (2^-8
+// m is a running reference, not the exact maximum: it moves only when a logit
+// passes it by more than RESCALE_LOG2 (p then stays below 2^RESCALE_LOG2, far
+// inside FP32's and BF16's range, and every rounding is relative), so the
+// accumulators are rescaled a few times per row and not once per tile.  Sums, m and l are FP32.  P is rounded once to BF16 (2^-8
 // relative at most, as a BF16 output is); for FP32 outputs SPLITP makes it
 // three BF16 terms (2^-22), for three products with V instead of one.
 #pragma once
@@ -70,18 +69,26 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 template <int D, bool FP8>
 struct Stager {
     using T = Tile<D, FP8>;
-    int row0, chunk0;                                    // this lane's row and chunk (already permuted) in the first load
-    __device__ __forceinline__ explicit Stager(int lane) {
-        row0 = lane / T::CH;
-        chunk0 = (lane % T::CH) ^ T::sw(row0);
+    int stride, first, chunk0;                           // bytes between rows; this lane's row, and its place in it, in the first load
+    __device__ __forceinline__ Stager(int lane, int stride_bytes) {
+        stride = stride_bytes;
+        first = lane / T::CH * stride;
+        chunk0 = ((lane % T::CH) ^ T::sw(lane / T::CH)) << 4;
     }
-    __device__ __forceinline__ void rows16(__amdgpu_buffer_rsrc_t r, int stride_bytes, lds_ptr dst) const {
+    // The 1 KiB pieces [FIRST, FIRST + N) of the 16 rows' LOADS16.
+    template <int FIRST, int N>
+    __device__ __forceinline__ void pieces(__amdgpu_buffer_rsrc_t r, lds_ptr dst) const {
+        int at = chunk0;
+        if (N >= 4) asm volatile("" : "+v"(at));         // offsets are formed as they are needed, not kept in registers
 #pragma unroll
-        for (int i = 0; i < T::LOADS16; ++i) {
-            const int off = (row0 + i * T::RPI) * stride_bytes + ((chunk0 ^ T::sw(i * T::RPI)) << 4);
+        for (int i = FIRST; i < FIRST + N; ++i) {
+            const int off = (at ^ (T::sw(i * T::RPI) << 4)) + first + i * T::RPI * stride;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) uint32_t*)(dst + i * 1024), 16,
                                                      off, 0, 0, 0);
         }
+    }
+    __device__ __forceinline__ void rows16(__amdgpu_buffer_rsrc_t r, lds_ptr dst) const {
+        pieces<0, T::LOADS16>(r, dst);
     }
 };
 
@@ -119,17 +126,41 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
     return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-// Whether any of 16 staged rows at p holds such a value.
-template <int D, bool FP8>
-__device__ __forceinline__ bool rows16_not_finite(lds_cptr p, int lane) {
-    uint32_t bad = 0;
+// The staged rows at p that hold such a value, as bits: N 1 KiB pieces (N
+// RPI rows) that this wave has loaded.
+template <int D, bool FP8, int N>
+__device__ __forceinline__ uint32_t rows_not_finite(lds_cptr p, int lane) {
+    using T = Tile<D, FP8>;
+    uint32_t rows = 0;
 #pragma unroll
-    for (int i = 0; i < Tile<D, FP8>::LOADS16; ++i) {
+    for (int i = 0; i < N; ++i) {
         const v4u x = *(__attribute__((address_space(3))) const v4u*)(p + i * 1024 + lane * 16);
+        uint32_t bad = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) bad |= not_finite<FP8>(x[w]);
+        const uint64_t lanes = __ballot(bad != 0);
+        if (lanes) {
+            for (int r = 0; r < T::RPI; ++r)
+                if (lanes >> (r * T::CH) & (T::CH == 64 ? ~0ull : (1ull << (T::CH & 63)) - 1)) rows |= 1u << (i * T::RPI + r);
+        }
     }
-    return __ballot(bad != 0) != 0;
+    return rows;
+}
+
+// ... and zeros in the place of such values.
+template <int D, bool FP8, int N>
+__device__ __forceinline__ void rows_made_finite(lds_ptr p, int lane) {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        auto* at = (__attribute__((address_space(3))) v4u*)(p + i * 1024 + lane * 16);
+        v4u x = *at;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t top = not_finite<FP8>(x[w]);                      // the bit above each such field
+            x[w] &= FP8 ? ~((top >> 7) * 0xFFu) : ~((top >> 15) * 0xFFFFu);
+        }
+        *at = x;
+    }
 }
 
 // One wave's rows and their running results.
@@ -139,34 +170,25 @@ struct Rows {
     static constexpr int NS = D / 16;                   // steps of 16 columns in K Q^T
     static constexpr int ND = D / 32;                   // blocks of 32 output columns
     static constexpr int TERMS = SPLITP ? 3 : 1;        // BF16 terms of P
-    static constexpr int KA = FP8 ? ND : (NS < 8 ? NS : 8);
-    static constexpr int VA = FP8 ? ND : (ND < 4 ? ND : 4);
 
     v8bf q[QB][NS];
     v16f o[QB][ND];
     float m[QB], l[QB];                                 // reference (unscaled logit units), this lane's half of the sum
     float c;                                            // scale log2 e (> 0)
-    int ka[KA], va[FP8 ? 1 : 2][VA];                    // byte offsets of this lane's reads in a K and a V tile
+    int ka, va;                                         // byte offsets of this lane's first read in a K and a V tile
     int lane;
 
     __device__ __forceinline__ void init(int lane_, float c_) {
         lane = lane_;
         c = c_;
         const int n = lane & 31, h = lane >> 5, g = lane >> 4, r = lane & 15;
-#pragma unroll
-        for (int s = 0; s < KA; ++s) ka[s] = n * T::ROW + (((2 * s + h) ^ T::sw(n)) << 4);
+        ka = n * T::ROW + ((h ^ T::sw(n)) << 4);
         if constexpr (FP8) {
             const int key = 4 * h + ((r >> 1) & 3) + 8 * (r >> 3);
-#pragma unroll
-            for (int b = 0; b < VA; ++b) va[0][b] = key * T::ROW + (((2 * b + (g & 1)) ^ T::sw(key)) << 4) + (r & 1) * 8;
+            va = key * T::ROW + (((g & 1) ^ T::sw(key)) << 4) + (r & 1) * 8;
         } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int key = 4 * h + (r >> 2) + 8 * e;
-#pragma unroll
-                for (int b = 0; b < VA; ++b)
-                    va[e][b] = key * T::ROW + (((4 * b + 2 * (g & 1) + ((r & 3) >> 1)) ^ T::sw(key)) << 4) + (r & 1) * 8;
-            }
+            const int key = 4 * h + (r >> 2);
+            va = key * T::ROW + (((2 * (g & 1) + ((r & 3) >> 1)) ^ T::sw(key)) << 4) + (r & 1) * 8;
         }
 #pragma unroll
         for (int b = 0; b < QB; ++b) {
@@ -190,100 +212,121 @@ struct Rows {
         }
     }
 
-    __device__ __forceinline__ v8bf v_frag(lds_cptr v, int t, int d) const {
+    // The reads' places: a chunk number is XORed into the row's permuted place
+    // (low four chunk bits), further chunks and rows are added.  LEAN: formed
+    // anew each time (one instruction a read) instead of being kept in registers.
+    static constexpr bool LEAN = QB * (NS * 4 + ND * 16) >= 192;
+    __device__ __forceinline__ int fresh(int at) const {
+        if (LEAN) asm volatile("" : "+v"(at));
+        return at;
+    }
+    __device__ __forceinline__ static int chunk(int at, int c) { return (at ^ ((c & 15) << 4)) + (c >> 4) * 256; }
+
+    __device__ __forceinline__ v8bf v_frag(lds_cptr v, int at, int t, int d) const {
         if constexpr (FP8) {
             const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (__attribute__((address_space(3))) v2i*)(v + va[0][d] + t * 16 * T::ROW));
+                (__attribute__((address_space(3))) v2i*)(v + chunk(at, 2 * d) + t * 16 * T::ROW));
             return e4m3x8_to_frag(x[0], x[1]);
         } else {
-            const int at = (d >> 2) * 256 + t * 16 * T::ROW;
-            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) v4s*)(v + va[0][d & 3] + at));
+            const lds_cptr rows = v + t * 16 * T::ROW;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(rows + chunk(at, 4 * d)));
             const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) v4s*)(v + va[1][d & 3] + at));
+                (__attribute__((address_space(3))) v4s*)(rows + chunk(at, (4 * d) ^ T::sw(8)) + 8 * T::ROW));
             const v2u a = __builtin_bit_cast(v2u, lo), b = __builtin_bit_cast(v2u, hi);
             return as_frag(v4u{a[0], a[1], b[0], b[1]});
         }
     }
 
-    // S^T of KB blocks of 32 keys at k.
-    template <int KB>
-    __device__ __forceinline__ void logits(lds_cptr k, v16f (&s)[QB][KB]) const {
+    // The order of the instructions before it: the LDS reads of FIRST operands,
+    // then an operand's products and the reads of the next operand in turn, N
+    // operands in all (READS LDS reads and PRODUCTS products each).  Left to
+    // itself the compiler reads each operand right before its product, and
+    // every product waits for LDS (16384 causal tokens, 24 heads of 256: 15 %
+    // slower).  FIRST is what the registers bear: 4 for K, 2 for V, beside P.
+    template <int FIRST, int N, int READS, int PRODUCTS>
+    __device__ __forceinline__ static void in_turn() {
+        __builtin_amdgcn_sched_group_barrier(0x100, FIRST * READS, 0);
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS, 0);
+            if (x + FIRST < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        }
+    }
+
+    // S^T of the 32 keys at k.
+    __device__ __forceinline__ void logits(lds_cptr k, v16f (&s)[QB]) const {
 #pragma unroll
         for (int b = 0; b < QB; ++b)
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[b][kb][i] = 0.f;
+            for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+        const int at = fresh(ka);
         if constexpr (FP8) {
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
+            for (int d = 0; d < ND; ++d) {
+                const v4u x = *(__attribute__((address_space(3))) const v4u*)(k + chunk(at, 2 * d));
+                const v8bf f0 = e4m3x8_to_frag(x[0], x[1]), f1 = e4m3x8_to_frag(x[2], x[3]);
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const v4u x = *(__attribute__((address_space(3))) const v4u*)(k + ka[d] + kb * 32 * T::ROW);
-                    const v8bf f0 = e4m3x8_to_frag(x[0], x[1]), f1 = e4m3x8_to_frag(x[2], x[3]);
-#pragma unroll
-                    for (int b = 0; b < QB; ++b) {
-                        s[b][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0, q[b][2 * d], s[b][kb], 0, 0, 0);
-                        s[b][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, q[b][2 * d + 1], s[b][kb], 0, 0, 0);
-                    }
+                for (int b = 0; b < QB; ++b) {
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0, q[b][2 * d], s[b], 0, 0, 0);
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, q[b][2 * d + 1], s[b], 0, 0, 0);
                 }
+            }
         } else {
 #pragma unroll
-            for (int st = 0; st < NS; ++st)
+            for (int st = 0; st < NS; ++st) {
+                const v8bf f = as_frag(*(__attribute__((address_space(3))) const v4u*)(k + chunk(at, 2 * st)));
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    const v8bf f = as_frag(*(__attribute__((address_space(3))) const v4u*)(
-                        k + ka[st & 7] + (st >> 3) * 256 + kb * 32 * T::ROW));
-#pragma unroll
-                    for (int b = 0; b < QB; ++b)
-                        s[b][kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[b][st], s[b][kb], 0, 0, 0);
-                }
+                for (int b = 0; b < QB; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[b][st], s[b], 0, 0, 0);
+            }
+            in_turn<4, NS, 1, QB>();
         }
     }
 
     // Logits of keys that the row does not see become -infinity.  seen: bit j
-    // = key j of these KB blocks.
-    template <int KB>
-    __device__ __forceinline__ void hide(v16f (&s)[KB], uint64_t seen) const {
-        const uint64_t mine = seen >> (4 * (lane >> 5));
+    // = key j of these 32.
+    __device__ __forceinline__ void hide(v16f& s, uint64_t seen) const {
+        const uint32_t w = (uint32_t)(seen >> (4 * (lane >> 5)));
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            const uint32_t w = (uint32_t)(mine >> (32 * kb));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[kb][i] = (w >> (8 * (i >> 2) + (i & 3))) & 1u ? s[kb][i] : -INFINITY;
-        }
+        for (int i = 0; i < 16; ++i) s[i] = (w >> (8 * (i >> 2) + (i & 3))) & 1u ? s[i] : -INFINITY;
     }
 
-    // S^T -> P^T (in place), with m, l and o brought along.
-    template <int KB>
-    __device__ __forceinline__ void softmax(int b, v16f (&s)[KB]) {
-        float top = s[0][0];
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) top = max2(top, s[kb][i]);
-        top = halves_max(top);
-        if (__ballot((top - m[b]) * c > RESCALE_LOG2 || (m[b] == -INFINITY && top > -INFINITY)) != 0) {
-            const float to = max2(m[b], top);
-            const float a = m[b] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[b] - to) * c);
-            m[b] = to;
-            l[b] *= a;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[b][d][i] *= a;
-        }
+    __device__ __forceinline__ float powers(int b, v16f& s) const {
         const float mc = m[b] == -INFINITY ? 0.f : m[b] * c;
         float sum = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int i = 0; i < 16; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
+            sum += s[i];
+        }
+        return sum;
+    }
+
+    // P^T of the 32 keys at k, with m, l and o brought along.
+    template <bool HIDE>
+    __device__ __forceinline__ void weights(lds_cptr k, const uint64_t (&seen)[QB], v16f (&s)[QB]) {
+        logits(k, s);
+        float sum[QB];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], c, -mc));
-                sum += s[kb][i];
+        for (int b = 0; b < QB; ++b) {
+            if (HIDE) hide(s[b], seen[b]);
+            float top = s[b][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top = max2(top, s[b][i]);
+            top = halves_max(top);
+            if (__ballot((top - m[b]) * c > RESCALE_LOG2) != 0) {
+                const float to = max2(m[b], top);
+                const float a = m[b] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[b] - to) * c);
+                m[b] = to;
+                l[b] *= a;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[b][d][i] *= a;
             }
-        l[b] += sum;
+            sum[b] = powers(b, s[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < QB; ++b) l[b] += sum[b];
     }
 
     // The operand of 16 keys: registers i0 .. i0 + 7 of S^T, as BF16.  SPLITP:
@@ -310,17 +353,17 @@ struct Rows {
         }
     }
 
-    // O^T += V^T P^T over KB blocks of 32 keys at v.
-    template <int KB>
-    __device__ __forceinline__ void values(lds_cptr v, const v16f (&p)[QB][KB]) {
+    // O^T += V^T P^T over the 32 keys at v.
+    __device__ __forceinline__ void values(lds_cptr v, const v16f (&p)[QB]) {
+        const int at = fresh(va);
 #pragma unroll
-        for (int t = 0; t < 2 * KB; ++t) {
+        for (int t = 0; t < 2; ++t) {
             v8bf pf[QB][TERMS];
 #pragma unroll
-            for (int b = 0; b < QB; ++b) p_frag(p[b][t >> 1], 8 * (t & 1), pf[b]);
+            for (int b = 0; b < QB; ++b) p_frag(p[b], 8 * t, pf[b]);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const v8bf f = v_frag(v, t, d);
+                const v8bf f = v_frag(v, at, t, d);
 #pragma unroll
                 for (int e = 0; e < TERMS; ++e)
 #pragma unroll
@@ -328,45 +371,45 @@ struct Rows {
                         o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[b][e], o[b][d], 0, 0, 0);
             }
         }
+        in_turn<2, 2 * ND, FP8 ? 1 : 2, QB * TERMS>();
     }
 
-    // The same where some rows must not see keys whose values are not finite:
-    // a product over 16 keys would give 0 x infinity = NaN, so one key at a
-    // time is summed and kept by the rows that see it.
-    template <int KB>
-    __device__ void values_one_by_one(lds_cptr v, const v16f (&p)[QB][KB], const uint64_t (&seen)[QB]) {
-        const int h = lane >> 5;
+    // Values that are not finite, of keys that some rows do not see: a product
+    // over 16 keys would give 0 x infinity = NaN there.  They are added to the
+    // rows that see them (a weight is positive, so the sum is infinite or NaN
+    // by them whatever it is), and then count as zeros in the products.
+    // bad: the keys of the 32 at v that hold such values; seen: as in hide().
+    __device__ __forceinline__ void add_not_finite(lds_cptr v, uint64_t bad, const uint64_t (&seen)[QB]) {
+        while (bad) {
+            const int key = __builtin_ctzll(bad);
+            bad &= bad - 1;
 #pragma unroll
-        for (int t = 0; t < 2 * KB; ++t) {
-            v8bf pf[QB][TERMS];
+            for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int b = 0; b < QB; ++b) p_frag(p[b][t >> 1], 8 * (t & 1), pf[b]);
+                for (int e = 0; e < 4; ++e) {
+                    float x[4];
+                    read4(v, key, column(d, e), x);
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const v4u f = __builtin_bit_cast(v4u, v_frag(v, t, d));
-#pragma unroll 1
-                for (int k = 0; k < 16; ++k) {           // key 16 t + k sits in half (k >> 2) & 1, element 4 (k >> 3) + (k & 3)
-                    const int e = 4 * (k >> 3) + (k & 3);
-                    const uint32_t keep = ((k >> 2) & 1) == h ? (e & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-                    v4u a;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) a[w] = w == (e >> 1) ? f[w] & keep : 0u;
+                    for (int j = 0; j < 4; ++j) x[j] = __builtin_isfinite(x[j]) ? 0.f : x[j];
 #pragma unroll
                     for (int b = 0; b < QB; ++b) {
-                        v16f next = o[b][d];
+                        const bool sees = (seen[b] >> key) & 1u;
 #pragma unroll
-                        for (int term = 0; term < TERMS; ++term) {
-                            v4u x = __builtin_bit_cast(v4u, pf[b][term]);
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) x[w] = w == (e >> 1) ? x[w] & keep : 0u;
-                            next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(a), as_frag(x), next, 0, 0, 0);
-                        }
-                        const bool sees = (seen[b] >> (16 * t + k)) & 1u;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[b][d][i] = sees ? next[i] : o[b][d][i];
+                        for (int j = 0; j < 4; ++j) o[b][d][4 * e + j] += sees ? x[j] : 0.f;
                     }
                 }
-            }
+        }
+    }
+    // Four neighbouring values of a row in a staged tile.
+    __device__ __forceinline__ static void read4(lds_cptr tile, int key, int col, float (&x)[4]) {
+        const int byte = col * (FP8 ? 1 : 2);
+        const lds_cptr at = tile + key * T::ROW + (((byte >> 4) ^ T::sw(key)) << 4) + (byte & 15);
+        if constexpr (FP8) {
+            e4m3x4_to_f32(*(__attribute__((address_space(3))) const uint32_t*)at, x);
+        } else {
+            const v2u w = *(__attribute__((address_space(3))) const v2u*)at;
+            x[0] = bf16_bits_to_f32(w[0] & 0xFFFFu), x[1] = bf16_bits_to_f32(w[0] >> 16);
+            x[2] = bf16_bits_to_f32(w[1] & 0xFFFFu), x[3] = bf16_bits_to_f32(w[1] >> 16);
         }
     }
 

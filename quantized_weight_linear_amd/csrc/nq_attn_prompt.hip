@@ -48,13 +48,15 @@ struct PackedRows {                 // K or V rows of one sequence and KV head
 template <int QB>
 struct CausalSees {
     int clean;                      // every row of the workgroup sees the keys below it
+    int none;                       // no row of the wave sees keys from it on
     int limit[QB];                  // this lane's rows see the keys below it
     __device__ __forceinline__ int all_before() const { return clean; }
+    __device__ __forceinline__ int none_from() const { return none; }
     __device__ __forceinline__ uint64_t seen(int b, int key) const { return bits_below(limit[b] - key); }
 };
 
-template <int D, int QB, int KB, int NW, bool BF16OUT>
-__global__ __launch_bounds__(NW * 64) void attn_prompt_kernel(PromptArgs a) {
+template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
+__global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptArgs a) {
     constexpr int BM = NW * QB * 32;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -81,6 +83,7 @@ __global__ __launch_bounds__(NW * 64) void attn_prompt_kernel(PromptArgs a) {
     R.init(lane, a.c);
     CausalSees<QB> sees;
     sees.clean = first + 1 + ahead;
+    sees.none = first + (wave + 1) * QB * 32 + ahead;
     int row[QB];
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
@@ -96,7 +99,7 @@ __global__ __launch_bounds__(NW * 64) void attn_prompt_kernel(PromptArgs a) {
     src.n = nk;
     src.row_bytes = D * 2;
     const int end = last + ahead;                       // keys that the tile's last row sees
-    attend_rows<D, QB, KB, false, !BF16OUT, NW>(R, (lds_ptr)smem, 0, end, src, sees, wave, lane);
+    attend_rows<RING, NW, D, QB, false, !BF16OUT>(R, (lds_ptr)smem, 0, end, src, sees, wave, lane);
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
         const float l = halves_sum(R.l[i]), inv = inverse_sum(l);
@@ -113,10 +116,10 @@ __global__ __launch_bounds__(NW * 64) void attn_prompt_kernel(PromptArgs a) {
     }
 }
 
-template <int D, int QB, int KB, int NW, bool BF16OUT>
+template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
 hipError_t go(const PromptArgs& a, hipStream_t stream) {
-    constexpr int BM = NW * QB * 32, LDS = RowsLds<D, false, NW>::BYTES;
-    auto kernel = attn_prompt_kernel<D, QB, KB, NW, BF16OUT>;
+    constexpr int BM = NW * QB * 32, LDS = RowsLds<D, false, NW, RING>::BYTES;
+    auto kernel = attn_prompt_kernel<D, QB, NW, RING, PER_SIMD, BF16OUT>;
     if (hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
         return e;
     // every sequence may end in a part of a tile
@@ -135,9 +138,9 @@ hipError_t launch_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_
     const PromptArgs a{q, k, v, q_stride, k_stride, v_stride, cu_q, cu_k, (int)seqs, tq, tk, (int)hq, (int)hkv,
                        scale * LOG2E, o, lse};
     switch (d) {
-        case 64: return bf16_out ? go<64, 1, 2, 4, true>(a, stream) : go<64, 1, 2, 4, false>(a, stream);
-        case 128: return bf16_out ? go<128, 1, 2, 4, true>(a, stream) : go<128, 1, 2, 4, false>(a, stream);
-        default: return bf16_out ? go<256, 1, 2, 4, true>(a, stream) : go<256, 1, 2, 4, false>(a, stream);
+        case 64: return bf16_out ? go<64, 1, 4, 2, 4, true>(a, stream) : go<64, 1, 4, 2, 4, false>(a, stream);
+        case 128: return bf16_out ? go<128, 1, 4, 2, 3, true>(a, stream) : go<128, 1, 4, 2, 3, false>(a, stream);
+        default: return bf16_out ? go<256, 1, 4, 2, 2, true>(a, stream) : go<256, 1, 4, 2, 2, false>(a, stream);
     }
 }
 

@@ -94,6 +94,7 @@ struct TreeSees {
     int len;                        // committed keys: seen by every row
     uint64_t mask[QB];              // drafted keys that this lane's rows see
     __device__ __forceinline__ int all_before() const { return len; }
+    __device__ __forceinline__ int none_from() const { return 1 << 30; }
     __device__ __forceinline__ uint64_t seen(int b, int key) const {
         const int at = len - key;   // where the drafted keys start among these 64
         const uint64_t drafted = at >= 64 ? 0ull : at >= 0 ? mask[b] << at : at > -64 ? mask[b] >> -at : 0ull;
@@ -164,7 +165,7 @@ __device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const
 }
 
 // More than 32 rows: NW waves of 32 QB rows.
-template <int D, int QB, int KB, int NW, bool FP8, bool BF16OUT>
+template <int D, int QB, int NW, bool FP8, bool BF16OUT>
 __global__ __launch_bounds__(NW * 64) void attn_tree_rows_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_rows_kernel(TreeArgs a) {
     for (int i = 0; i < QB; ++i) row[i] = ((rt * NW + wave) * QB + i) * 32 + (lane & 31);
     TreeRows<D, QB, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
     const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, b, kvh);
-    attend_rows<D, QB, KB, FP8, !BF16OUT, NW>(R, (lds_ptr)smem, key0, key1, src, sees, wave, lane);
+    attend_rows<2, NW, D, QB, FP8, !BF16OUT>(R, (lds_ptr)smem, key0, key1, src, sees, wave, lane);
 #pragma unroll
     for (int i = 0; i < QB; ++i)
         TreeRows<D, QB, FP8, BF16OUT>::store(R, a, s, b, kvh, split, r.count <= 1, i, row[i]);
@@ -219,15 +220,15 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
     TreeRows<D, 1, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
     PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, b, kvh);
     src.total = key1;                                   // keys past the range: no rows, zeros
-    const Stager<D, FP8> st(lane);
+    const Stager<D, FP8> st(lane, Tile<D, FP8>::ROW);
     const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
     auto load_k = [&](int key, int slot) {
-        st.rows16(src.k_rows(key), src.k_stride, mine + slot * 2 * L::TILE);
-        st.rows16(src.k_rows(key + 16), src.k_stride, mine + slot * 2 * L::TILE + L::TILE / 2);
+        st.rows16(src.k_rows(key), mine + slot * 2 * L::TILE);
+        st.rows16(src.k_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE / 2);
     };
     auto load_v = [&](int key, int slot) {
-        st.rows16(src.v_rows(key), src.v_stride, mine + slot * 2 * L::TILE + L::TILE);
-        st.rows16(src.v_rows(key + 16), src.v_stride, mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
+        st.rows16(src.v_rows(key), mine + slot * 2 * L::TILE + L::TILE);
+        st.rows16(src.v_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
     };
     constexpr int STEP = NW * 32;
     const int from = key0 + wave * 32;
@@ -239,23 +240,22 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
     int slot = 0;
     for (int key = from; key < key1; key += STEP) {
         const lds_ptr k = mine + slot * 2 * L::TILE, v = k + L::TILE;
-        v16f x[1][1];
-        wait_vm<R1>();
-        R.template logits<1>(k, x);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
-        load_k(key + L::RING * STEP, slot);
+        v16f x[1];
         uint64_t seen[1] = {~0ull};
         const bool partly = key + 32 > sees.all_before();
-        if (partly) {
-            seen[0] = sees.seen(0, key);
-            R.template hide<1>(x[0], seen[0]);
-        }
-        R.template softmax<1>(0, x[0]);
+        if (partly) seen[0] = sees.seen(0, key);
         wait_vm<R1>();
-        if (partly && (rows16_not_finite<D, FP8>(v, lane) || rows16_not_finite<D, FP8>(v + L::TILE / 2, lane)))
-            R.template values_one_by_one<1>(v, x, seen);
-        else
-            R.template values<1>(v, x);
+        R.template weights<true>(k, seen, x);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
+        load_k(key + L::RING * STEP, slot);
+        wait_vm<R1>();
+        if (partly) {
+            if (const uint32_t bad = rows_not_finite<D, FP8, LOADS>(v, lane)) {
+                R.add_not_finite(v, bad, seen);
+                rows_made_finite<D, FP8, LOADS>((lds_ptr)v, lane);
+            }
+        }
+        R.values(v, x);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         load_v(key + L::RING * STEP, slot);
         slot = slot + 1 == L::RING ? 0 : slot + 1;
@@ -376,8 +376,8 @@ hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
         if (hipError_t e = set_lds(kernel, LDS); e != hipSuccess) return e;
         kernel<<<units, 256, LDS, stream>>>(a);
     } else {
-        constexpr int LDS = RowsLds<D, FP8, 4>::BYTES;
-        auto kernel = attn_tree_rows_kernel<D, 1, 2, 4, FP8, BF16OUT>;
+        constexpr int LDS = RowsLds<D, FP8, 4, 2>::BYTES;
+        auto kernel = attn_tree_rows_kernel<D, 1, 4, FP8, BF16OUT>;
         if (hipError_t e = set_lds(kernel, LDS); e != hipSuccess) return e;
         kernel<<<units * a.row_tiles, 256, LDS, stream>>>(a);
     }
