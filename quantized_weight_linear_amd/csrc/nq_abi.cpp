@@ -671,7 +671,7 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
     if (T < 0 || T >= I31 || max_q < 1 || max_q > 64 || max_len < 0 || workspace_bytes < 0 || !heads_ok(Hq, Hkv, D) ||
         !table_ok(B, width, page_size, pages) || !stride_ok(q_stride, Hq, D))
         return NQ_ERR_SHAPE;
-    if (B * Hq * max_q >= MOST_BLOCKS) return NQ_ERR_SHAPE;
+    if (B * Hq * max_q >= MOST_BLOCKS || B * Hq * 4 >= MOST_BLOCKS) return NQ_ERR_SHAPE;
     if (!scale_ok(scale)) return NQ_ERR_RANGE;
     if (B == 0 || T == 0) return NQ_OK;
     NQ_TRY(all_there(q, lens, cu_q, tree_mask, o));

@@ -271,6 +271,7 @@ struct Rows {
                     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, q[b][2 * d + 1], s[b], 0, 0, 0);
                 }
             }
+            in_turn<2, ND, 1, 2 * QB>();
         } else {
 #pragma unroll
             for (int st = 0; st < NS; ++st) {

@@ -120,8 +120,8 @@ template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
 hipError_t go(const PromptArgs& a, hipStream_t stream) {
     constexpr int BM = NW * QB * 32, LDS = RowsLds<D, false, NW, RING>::BYTES;
     auto kernel = attn_prompt_kernel<D, QB, NW, RING, PER_SIMD, BF16OUT>;
-    if (hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, LDS); e != hipSuccess)
-        return e;
+    static LdsLimit limit;
+    if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
     // every sequence may end in a part of a tile
     const int64_t tiles = a.tq / BM + (a.seqs < a.tq ? a.seqs : a.tq);
     kernel<<<(unsigned)(tiles * a.hq), NW * 64, LDS, stream>>>(a);

@@ -44,7 +44,7 @@ __device__ __forceinline__ void attend_rows(Rows<D, QB, FP8, SPLITP>& R, lds_ptr
     using L = RowsLds<D, FP8, NW, RING>;
     using T = Tile<D, FP8>;
     constexpr int ROW = T::ROW, LOADS = 4 * T::LOADS16 / NW;          // a wave's load instructions a step
-    static_assert(NW == 4 || NW == 8, "a step stages four groups of 16 rows");
+    static_assert((NW == 4 || NW == 8) && LOADS * NW == 4 * T::LOADS16, "a step stages four groups of 16 rows");
     const int group = wave & 3, part = (group & 1) * 16;             // groups 0, 1: K; 2, 3: V
     const Stager<D, FP8> st(lane, group < 2 ? src.k_stride : src.v_stride);
     const lds_ptr k_ring = lds, v_ring = lds + RING * L::TILE;

@@ -34,8 +34,9 @@ struct TreeArgs {
     float scale;
     void* o;
     float* lse;
-    float* parts;                   // split outputs, then (m c, l) pairs
-    int splits, chunk;              // at most `splits` ranges of at least `chunk` keys
+    float* parts;                   // parts' outputs, then their (m c, l) pairs, then each sequence's (first part, parts)
+    int want;                       // ranges to split all sequences' keys into, about (0: one a sequence)
+    int least;                      // keys of a range, at least and as a multiple
     int row_tiles;
 };
 
@@ -57,14 +58,72 @@ struct Seq {
     }
 };
 
-// How a sequence's keys are split: ranges of `chunk` keys, as many as asked
-// for at most (longer ranges where the sequence is longer than the caller said).
-struct Ranges {
-    int chunk, count;
-    __device__ __forceinline__ Ranges(const TreeArgs& a, int total) {
-        const int least = ((total + a.splits - 1) / a.splits + KEYS - 1) / KEYS * KEYS;
-        chunk = a.chunk > least ? a.chunk : least;
-        count = (total + chunk - 1) / chunk;
+// How the keys of all sequences are split into ranges: ranges of one length,
+// so that there are about a.want of them whatever the sequences' lengths are,
+// numbered through the sequences in order.  Every workgroup works this out for
+// itself from the lengths (a wave reads 64 sequences at a time).
+constexpr int MOST_PARTS = 128;     // of a sequence
+struct Range {
+    int b, first, parts, key0, key1;                    // its sequence, number of the sequence's first range and of ranges
+    __device__ __forceinline__ static int64_t keys_of(const TreeArgs& a, int b) {
+        if (b >= a.seqs) return 0;
+        const Seq s(a, b);
+        return s.n > 0 ? s.total : -1;                  // -1: nothing to do
+    }
+    // Range `index`; b = -1 where there is none.
+    __device__ __forceinline__ Range(const TreeArgs& a, int index) {
+        const int lane = threadIdx.x & 63;
+        int64_t all = 0, top = 0;
+        int busy = 0;
+        for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+            const int64_t t = keys_of(a, b0 + lane);
+            all += t > 0 ? t : 0;
+            top = t > top ? t : top;
+            busy += t > 0;
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            all += __shfl_xor(all, off, 64);
+            const int64_t o = __shfl_xor(top, off, 64);
+            top = o > top ? o : top;
+            busy += __shfl_xor(busy, off, 64);
+        }
+        int64_t chunk = (int64_t)1 << 30;
+        if (a.want > 0) {
+            // the last range of each sequence is a part of one: aim at `busy` fewer
+            const int aim = a.want - busy > a.want / 2 ? a.want - busy : (a.want + 1) / 2;
+            chunk = (all + aim - 1) / aim;
+            if (chunk < (top + MOST_PARTS - 1) / MOST_PARTS) chunk = (top + MOST_PARTS - 1) / MOST_PARTS;
+            chunk = (chunk + a.least - 1) / a.least * a.least;
+            if (chunk < a.least) chunk = a.least;
+        }
+        b = -1;
+        int before = 0;
+        for (int b0 = 0; b0 < a.seqs && b < 0; b0 += 64) {
+            const int64_t t = keys_of(a, b0 + lane);
+            const int n = b0 + lane >= a.seqs || t < 0 ? 0 : t == 0 ? 1 : (int)((t + chunk - 1) / chunk);
+            int upto = n;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int y = __shfl_up(upto, off, 64);
+                if (lane >= off) upto += y;
+            }
+            const uint64_t past = __ballot(before + upto > index);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                b = b0 + at;
+                parts = __shfl(n, at, 64);
+                first = before + __shfl(upto, at, 64) - parts;
+            }
+            before += __shfl(upto, 63, 64);
+        }
+        if (b < 0) return;
+        b = __builtin_amdgcn_readfirstlane(b);
+        parts = __builtin_amdgcn_readfirstlane(parts);
+        first = __builtin_amdgcn_readfirstlane(first);
+        const int64_t total = keys_of(a, b), from = (index - first) * chunk;
+        key0 = (int)from;
+        key1 = (int)(from + chunk < total ? from + chunk : total);
     }
 };
 
@@ -92,9 +151,10 @@ struct PagedRows {
 template <int QB>
 struct TreeSees {
     int len;                        // committed keys: seen by every row
+    int none = 1 << 30;             // 0: the wave has no rows
     uint64_t mask[QB];              // drafted keys that this lane's rows see
     __device__ __forceinline__ int all_before() const { return len; }
-    __device__ __forceinline__ int none_from() const { return 1 << 30; }
+    __device__ __forceinline__ int none_from() const { return none; }
     __device__ __forceinline__ uint64_t seen(int b, int key) const {
         const int at = len - key;   // where the drafted keys start among these 64
         const uint64_t drafted = at >= 64 ? 0ull : at >= 0 ? mask[b] << at : at > -64 ? mask[b] >> -at : 0ull;
@@ -102,11 +162,15 @@ struct TreeSees {
     }
 };
 
-__device__ __forceinline__ int64_t part_row(const TreeArgs& a, int b, int kvh, int split, int row) {
-    return (((int64_t)b * a.hkv + kvh) * a.splits + split) * ((int64_t)a.max_q * a.group) + row;
+// Parts are numbered as the ranges are; row: max_q group of them a KV head.
+__device__ __forceinline__ int64_t part_row(const TreeArgs& a, int range, int kvh, int row) {
+    return ((int64_t)range * a.hkv + kvh) * ((int64_t)a.max_q * a.group) + row;
 }
 __device__ __forceinline__ float2* part_sums(const TreeArgs& a, int d) {
-    return reinterpret_cast<float2*>(a.parts + (int64_t)a.seqs * a.hkv * a.splits * a.max_q * a.group * d);
+    return reinterpret_cast<float2*>(a.parts + part_row(a, a.want + a.seqs, 0, 0) * d);
+}
+__device__ __forceinline__ int2* part_ranges(const TreeArgs& a, int d) {
+    return reinterpret_cast<int2*>(part_sums(a, d) + part_row(a, a.want + a.seqs, 0, 0));
 }
 
 // Rows [0, n group) of (b, kvh): token row / group, query head kvh group + row % group.
@@ -125,14 +189,14 @@ struct TreeRows {
         }
     }
     // Results of one row block: outputs, or a part of them.
-    __device__ static void store(const Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int b, int kvh, int split,
-                                 bool only, int i, int row) {
+    __device__ static void store(const Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int range, int kvh, bool only,
+                                 int i, int row) {
         const float l = halves_sum(R.l[i]);
         const float mc = R.m[i] == -INFINITY ? 0.f : R.m[i] * R.c;
         if (row >= s.n * a.group) return;
         const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
         const int64_t out = (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
-        const int64_t part = part_row(a, b, kvh, split, row);
+        const int64_t part = part_row(a, range, kvh, row);
         const float f = only ? inverse_sum(l) * vs : 1.0f;
 #pragma unroll
         for (int d = 0; d < D / 32; ++d)
@@ -164,30 +228,26 @@ __device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const
     return src;
 }
 
-// More than 32 rows: NW waves of 32 QB rows.
-template <int D, int QB, int NW, bool FP8, bool BF16OUT>
-__global__ __launch_bounds__(NW * 64) void attn_tree_rows_kernel(TreeArgs a) {
+// More than 32 rows: NW waves of 32 rows.
+template <int D, int NW, bool FP8, bool BF16OUT>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tree_rows_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int split = blockIdx.x % a.splits, rt = blockIdx.x / a.splits % a.row_tiles;
-    const int kvh = blockIdx.x / (a.splits * a.row_tiles) % a.hkv, b = blockIdx.x / (a.splits * a.row_tiles) / a.hkv;
-    const Seq s(a, b);
-    const Ranges r(a, s.total);
-    if (rt * NW * QB * 32 >= s.n * a.group) return;
-    if (split >= r.count && split > 0) return;          // (range 0 of an empty sequence writes its zeros)
-    const int key0 = split * r.chunk, key1 = key0 + r.chunk < s.total ? key0 + r.chunk : s.total;
-    Rows<D, QB, FP8, !BF16OUT> R;
+    const int rt = blockIdx.x % a.row_tiles, kvh = blockIdx.x / a.row_tiles % a.hkv, range = blockIdx.x / a.row_tiles / a.hkv;
+    const Range r(a, range);
+    if (r.b < 0) return;
+    const Seq s(a, r.b);
+    if (rt * NW * 32 >= s.n * a.group) return;
+    if (r.first == range && kvh == 0 && rt == 0 && threadIdx.x == 0 && a.want > 0) part_ranges(a, D)[r.b] = make_int2(r.first, r.parts);
+    Rows<D, 1, FP8, !BF16OUT> R;
     R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
-    TreeSees<QB> sees;
-    int row[QB];
-#pragma unroll
-    for (int i = 0; i < QB; ++i) row[i] = ((rt * NW + wave) * QB + i) * 32 + (lane & 31);
-    TreeRows<D, QB, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
-    const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, b, kvh);
-    attend_rows<2, NW, D, QB, FP8, !BF16OUT>(R, (lds_ptr)smem, key0, key1, src, sees, wave, lane);
-#pragma unroll
-    for (int i = 0; i < QB; ++i)
-        TreeRows<D, QB, FP8, BF16OUT>::store(R, a, s, b, kvh, split, r.count <= 1, i, row[i]);
+    TreeSees<1> sees;
+    const int row[1] = {(rt * NW + wave) * 32 + (lane & 31)};
+    sees.none = (rt * NW + wave) * 32 < s.n * a.group ? 1 << 30 : 0;
+    TreeRows<D, 1, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
+    const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
+    attend_rows<2, NW>(R, (lds_ptr)smem, r.key0, r.key1, src, sees, wave, lane);
+    TreeRows<D, 1, FP8, BF16OUT>::store(R, a, s, range, kvh, r.parts == 1, 0, row[0]);
 }
 
 // Up to 32 rows: wave w takes every NW-th tile of 32 keys of the range, with a
@@ -208,18 +268,18 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
     constexpr int LOADS = 2 * Tile<D, FP8>::LOADS16, R1 = (2 * L::RING - 1) * LOADS;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int split = blockIdx.x % a.splits, kvh = blockIdx.x / a.splits % a.hkv, b = blockIdx.x / a.splits / a.hkv;
-    const Seq s(a, b);
-    const Ranges r(a, s.total);
-    if (s.n == 0 || (split >= r.count && split > 0)) return;
-    const int key0 = split * r.chunk, key1 = key0 + r.chunk < s.total ? key0 + r.chunk : s.total;
+    const int kvh = blockIdx.x % a.hkv, range = blockIdx.x / a.hkv;
+    const Range r(a, range);
+    if (r.b < 0) return;
+    const Seq s(a, r.b);
+    if (r.first == range && kvh == 0 && threadIdx.x == 0 && a.want > 0) part_ranges(a, D)[r.b] = make_int2(r.first, r.parts);
     Rows<D, 1, FP8, !BF16OUT> R;
     R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
     TreeSees<1> sees;
     const int row[1] = {lane & 31};
     TreeRows<D, 1, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
-    PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, b, kvh);
-    src.total = key1;                                   // keys past the range: no rows, zeros
+    PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
+    src.total = r.key1;                                   // keys past the range: no rows, zeros
     const Stager<D, FP8> st(lane, Tile<D, FP8>::ROW);
     const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
     auto load_k = [&](int key, int slot) {
@@ -231,14 +291,14 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
         st.rows16(src.v_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
     };
     constexpr int STEP = NW * 32;
-    const int from = key0 + wave * 32;
+    const int from = r.key0 + wave * 32;
 #pragma unroll
     for (int i = 0; i < L::RING; ++i) {
         load_k(from + i * STEP, i);
         load_v(from + i * STEP, i);
     }
     int slot = 0;
-    for (int key = from; key < key1; key += STEP) {
+    for (int key = from; key < r.key1; key += STEP) {
         const lds_ptr k = mine + slot * 2 * L::TILE, v = k + L::TILE;
         v16f x[1];
         uint64_t seen[1] = {~0ull};
@@ -279,7 +339,7 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
         at[D + 1] = l;
     }
     __syncthreads();
-    const bool only = r.count <= 1;
+    const bool only = r.parts == 1;
     const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
     constexpr int LANES = D / 4;                        // threads a row
     for (int i = threadIdx.x / LANES; i < s.n * a.group; i += NW * 64 / LANES) {
@@ -301,7 +361,7 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
         }
         const float mc = top == -INFINITY ? 0.f : top;
         const int64_t out = (s.t0 + i / a.group) * a.hq + kvh * a.group + i % a.group;
-        const int64_t part = part_row(a, b, kvh, split, i);
+        const int64_t part = part_row(a, range, kvh, i);
         const float f = only ? inverse_sum(sum) * vs : 1.0f;
         if (only) store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
         else store4<false>(a.parts, part * D + col, x[0], x[1], x[2], x[3]);
@@ -323,26 +383,38 @@ __global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a) {
     const int rows = a.max_q * a.group;
     const int row = blockIdx.x % rows, kvh = blockIdx.x / rows % a.hkv, b = blockIdx.x / rows / a.hkv;
     const Seq s(a, b);
-    const Ranges r(a, s.total);
-    if (row >= s.n * a.group || r.count <= 1) return;
+    if (row >= s.n * a.group) return;
+    const int2 r = part_ranges(a, D)[b];                // (first part, parts)
+    if (r.y <= 1) return;
     const float2* ml = part_sums(a, D);
-    constexpr int W = D / 64;                           // columns a lane: 1, 2 or 4
+    constexpr int W = D / 64, BATCH = 8;                // columns a lane: 1, 2 or 4
     float top = -INFINITY;
-    for (int i = lane; i < r.count; i += 64) {
-        const float2 p = ml[part_row(a, b, kvh, i, row)];
+    for (int i = lane; i < r.y; i += 64) {
+        const float2 p = ml[part_row(a, r.x + i, kvh, row)];
         if (p.y != 0.f) top = max2(top, p.x);
     }
     top = wave_max(top);
     float sum = 0.f, x[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) x[j] = 0.f;
-    for (int i = wave; i < r.count; i += 4) {
-        const int64_t at = part_row(a, b, kvh, i, row);
-        const float2 p = ml[at];
-        const float f = p.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(p.x - top);
-        sum += p.y * f;
+    for (int i0 = wave; i0 < r.y; i0 += 4 * BATCH) {    // the loads of BATCH parts are in flight together
+        float2 p[BATCH];
+        float y[BATCH][W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) x[j] += a.parts[at * D + lane * W + j] * f;
+        for (int e = 0; e < BATCH; ++e) {
+            const int64_t at = part_row(a, r.x + (i0 + 4 * e < r.y ? i0 + 4 * e : i0), kvh, row);
+            p[e] = ml[at];
+#pragma unroll
+            for (int j = 0; j < W; ++j) y[e][j] = a.parts[at * D + lane * W + j];
+        }
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+            const bool real = i0 + 4 * e < r.y && p[e].y != 0.f;        // (a part that saw nothing has neither)
+            const float f = real ? __builtin_amdgcn_exp2f(p[e].x - top) : 0.f;
+            sum += p[e].y * f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) x[j] += real ? y[e][j] * f : 0.f;
+        }
     }
 #pragma unroll
     for (int j = 0; j < W; ++j) o_s[wave][lane * W + j] = x[j];
@@ -362,27 +434,39 @@ __global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a) {
     if (lane == 0 && a.lse) a.lse[out] = log_sum_exp(top == -INFINITY ? 0.f : top, sum);
 }
 
-template <class K>
-hipError_t set_lds(K kernel, int bytes) {
-    return hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Rows a workgroup of the launch holds: 32, 128 or 256 (eight waves need a
+// load each for a step's rows: not the 8 KiB of E4M3 rows of 64).
+constexpr int tile_rows(int64_t rows, int64_t d, bool fp8) {
+    return rows <= 32 ? 32 : rows <= 128 || (fp8 && d == 64) ? 128 : 256;
 }
 
 template <int D, bool FP8, bool BF16OUT>
 hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
-    const unsigned units = (unsigned)a.seqs * a.hkv * a.splits;
-    if (a.max_q * a.group <= 32) {
+    const unsigned units = (unsigned)(a.want + a.seqs) * a.hkv;
+    hipError_t e;
+    const int tile = tile_rows(a.max_q * a.group, D, FP8);
+    if (tile == 32) {
         constexpr int LDS = KeysLds<D, FP8, 4>::BYTES;
         auto kernel = attn_tree_keys_kernel<D, 4, FP8, BF16OUT>;
-        if (hipError_t e = set_lds(kernel, LDS); e != hipSuccess) return e;
+        static LdsLimit limit;
+        if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
         kernel<<<units, 256, LDS, stream>>>(a);
-    } else {
+    } else if (tile == 128 || (FP8 && D == 64)) {
         constexpr int LDS = RowsLds<D, FP8, 4, 2>::BYTES;
-        auto kernel = attn_tree_rows_kernel<D, 1, 4, FP8, BF16OUT>;
-        if (hipError_t e = set_lds(kernel, LDS); e != hipSuccess) return e;
+        auto kernel = attn_tree_rows_kernel<D, 4, FP8, BF16OUT>;
+        static LdsLimit limit;
+        if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
         kernel<<<units * a.row_tiles, 256, LDS, stream>>>(a);
+    } else {
+        constexpr int NW = FP8 && D == 64 ? 4 : 8;
+        constexpr int LDS = RowsLds<D, FP8, NW, 2>::BYTES;
+        auto kernel = attn_tree_rows_kernel<D, NW, FP8, BF16OUT>;
+        static LdsLimit limit;
+        if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
+        kernel<<<units * a.row_tiles, NW * 64, LDS, stream>>>(a);
     }
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.splits > 1) {
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.want > 0) {
         attn_tree_join_kernel<D, BF16OUT><<<(unsigned)a.seqs * a.hkv * a.max_q * a.group, 256, 0, stream>>>(a);
         return hipGetLastError();
     }
@@ -391,20 +475,37 @@ hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
 
 }  // namespace attn
 
-// Ranges a sequence's keys are split into: enough workgroups for two rounds of
-// the CUs, none shorter than 256 keys.
-static int tree_splits(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t max_len) {
-    const int64_t rows = max_q * (hq / hkv), tiles = rows <= 32 ? 1 : (rows + 127) / 128;
-    const int64_t units = seqs * hkv * tiles, want = 2 * (int64_t)device_cu_count();
-    int64_t splits = (want + units - 1) / units;
-    const int64_t most = (max_len + 255) / 256;
-    if (splits > most) splits = most;
-    return (int)(splits < 1 ? 1 : splits > 1024 ? 1024 : splits);
+namespace {
+
+struct TreePlan {
+    int want, least, row_tiles;
+    int64_t bytes;
+};
+
+// Ranges of 128 keys (four waves of 32) or, with more rows and so more to
+// write for each part, 256, and up.  Few sequences: one range a CU.  Many: about four
+// a CU, short enough that the last ones to run do not leave most CUs idle.
+TreePlan tree_plan(bool fp8, int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
+    const int64_t rows = max_q * (hq / hkv), tile = attn::tile_rows(rows, d, fp8), tiles = (rows + tile - 1) / tile;
+    const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles, cus = device_cu_count();
+    TreePlan p{0, (int)least, (int)tiles, 0};
+    if (max_len <= least) return p;
+    const int64_t slots = cus * (tile == 128 ? 2 : 1);
+    int64_t want = (2 * units <= slots ? slots : 4 * slots) / (hkv * tiles);
+    const int64_t most = seqs * ((max_len + least - 1) / least) + seqs;
+    if (want > most) want = most;
+    if (want < 1) want = 1;
+    p.want = (int)want;
+    p.bytes = (want + seqs) * hkv * rows * (d * 4 + 8) + seqs * 8;
+    return p;
 }
 
+}  // namespace
+
 int64_t attn_tree_workspace_bytes(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
-    const int64_t splits = tree_splits(seqs, max_q, hq, hkv, max_len);
-    return splits <= 1 ? 0 : seqs * hq * max_q * splits * (d * 4 + 8);
+    // (a query does not name the cache's format: the larger of the two)
+    const int64_t x = tree_plan(false, seqs, max_q, hq, hkv, d, max_len).bytes, y = tree_plan(true, seqs, max_q, hq, hkv, d, max_len).bytes;
+    return x > y ? x : y;
 }
 
 hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
@@ -414,14 +515,11 @@ hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const
                             int64_t max_len, float scale, bool bf16_out, void* o, float* lse, void* workspace,
                             int64_t workspace_bytes, hipStream_t stream) {
     using namespace attn;
-    int splits = tree_splits(seqs, max_q, hq, hkv, max_len);
-    if (splits > 1 && workspace_bytes < attn_tree_workspace_bytes(seqs, max_q, hq, hkv, d, max_len)) splits = 1;
-    const int64_t rows = max_q * (hq / hkv);
-    const int chunk = (int)(((max_len + splits - 1) / splits + KEYS - 1) / KEYS * KEYS);
+    TreePlan p = tree_plan(fp8, seqs, max_q, hq, hkv, d, max_len);
+    if (workspace_bytes < p.bytes) p.want = 0;
     const TreeArgs a{q, q_stride, k_pages, v_pages, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, table, (int)width, lens,
                      cu_q, masks, (int)seqs, (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size),
-                     pages, scale, o, lse, reinterpret_cast<float*>(workspace), splits, chunk < KEYS ? KEYS : chunk,
-                     rows <= 32 ? 1 : (int)((rows + 127) / 128)};
+                     pages, scale, o, lse, reinterpret_cast<float*>(workspace), p.want, p.least, p.row_tiles};
     switch (d) {
         case 64:
             return fp8 ? (bf16_out ? go_tree<64, true, true>(a, stream) : go_tree<64, true, false>(a, stream))

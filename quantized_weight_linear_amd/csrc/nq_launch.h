@@ -4,7 +4,27 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace nq {
+
+// Raises a kernel's limit of dynamic LDS, once per device (one object a
+// kernel).  Two threads may both do it; that is harmless.
+class LdsLimit {
+public:
+    hipError_t raise(const void* kernel, int bytes) {
+        int dev = 0;
+        if (hipError_t e = hipGetDevice(&dev); e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (dev < 64 && (done_.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+        const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == hipSuccess && dev < 64) done_.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+
+private:
+    std::atomic<uint64_t> done_{0};
+};
 
 // Weight formats, same values as nq_wfmt plus the row-scaled FP8 format.
 enum WFmt { W_Q4G64 = 0, W_Q8G32 = 1, W_Q8G64 = 2, W_MXFP8 = 3, W_BF16 = 4, W_Q3G64 = 5, W_Q5G64 = 6, W_Q6G64 = 7,

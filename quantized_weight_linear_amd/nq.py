@@ -116,10 +116,15 @@ _SCALE_BYTES = {NQ_W_Q4G64_F16S: 2 / 64, NQ_W_Q8G32_F16S: 2 / 32, NQ_W_Q8G64_F16
                 NQ_W_Q6G64_F16S: 2 / 64}
 
 
+# The current stream's handle by device index: what torch.cuda.current_stream(d).cuda_stream returns, without making
+# a Stream object for it (a call's host time is a good part of a small step's).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(*tensors):
     for t in tensors:
         if t is not None and t.is_cuda:
-            return torch.cuda.current_stream(t.device).cuda_stream
+            return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
     return None
 
 
@@ -365,73 +370,99 @@ def nq_linear_qbits_g64(fmt, x, T, w_codes, w_scale, N, K, a8, a_q_ws, a_scale_w
 # [planes][pages][Hkv][page_size][D], tables [B][width].
 # ---------------------------------------------------------------------------
 
-def _rows(t, what):
+_TWO_BYTES = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+_ONE_BYTE = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn))
+_INT32 = frozenset((torch.int32, torch.uint32))
+_INT64 = frozenset((torch.int64, torch.uint64))
+_OUT_TYPES = {torch.float32: NQ_OUT_F32, torch.bfloat16: NQ_OUT_BF16, torch.int16: NQ_OUT_BF16, torch.uint16: NQ_OUT_BF16}
+
+
+def _rows(t, shape, what):
     """Address and token stride of rows [T][heads][D]."""
-    if t.dim() != 3 or t.element_size() != 2:
+    if t.dtype not in _TWO_BYTES or len(shape) != 3:
         raise ValueError(f"{what}: BF16 rows [T][heads][D] expected")
-    n, h, d = t.shape
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
     if n == 0:
         return None, h * d
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) < h * d):
+    if s2 != 1 or (s1 != d and h > 1) or (n > 1 and s0 < h * d):
         raise ValueError(f"{what}: a token's heads must be back to back")
-    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    return t.data_ptr(), s0 if n > 1 else h * d
 
 
-def _ints(t, n, what, size=4):
-    """Address of at least n integers of `size` bytes."""
-    if t is None or t.element_size() != size or t.is_floating_point():
-        raise ValueError(f"{what}: integers of {size} bytes expected")
-    _size(t, n * size, what)
-    return _ptr(t)
+def _ints(t, n, what, types=_INT32):
+    """Address of at least n integers."""
+    if t.dtype not in types or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous integers of {8 if types is _INT64 else 4} bytes expected")
+    return t.data_ptr()
 
 
 def _floats(t, n, what):
-    if t is not None and t.dtype != torch.float32:
-        raise ValueError(f"{what}: float32 expected")
-    _size(t, 4 * n, what)
-    return _ptr(t)
+    if t is None:
+        if n:
+            raise ValueError(f"{what}: {n} values expected")
+        return None
+    if t.dtype is not torch.float32 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous float32 values expected")
+    return t.data_ptr()
 
 
 def _table(t):
-    if t.dim() != 2:
-        raise ValueError("page table: [B][width] expected")
-    return _ints(t, t.numel(), "page table"), t.shape[0], t.shape[1]
+    shape = t.shape
+    if len(shape) != 2 or t.dtype not in _INT32 or not t.is_contiguous():
+        raise ValueError("page table: contiguous 32-bit integers [B][width] expected")
+    return t.data_ptr(), shape[0], shape[1]
 
 
 def _planes(fmt, k_pages, v_pages, hkv, d):
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != hkv or k_pages.shape[3] != d:
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape or shape[1] != hkv or shape[3] != d:
         raise ValueError("pages: [pages][Hkv][page_size][D] expected, the same for keys and values")
-    if k_pages.element_size() != v_pages.element_size() or k_pages.element_size() != (1 if fmt == NQ_KV_E4M3 else 2):
+    types = _ONE_BYTE if fmt == NQ_KV_E4M3 else _TWO_BYTES
+    if k_pages.dtype not in types or v_pages.dtype not in types:
         raise ValueError("pages: one byte an element for E4M3, two for BF16")
-    return _ptr(k_pages), _ptr(v_pages), k_pages.shape[2], k_pages.shape[0]
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("pages: tensors must be contiguous")
+    return k_pages.data_ptr(), v_pages.data_ptr(), shape[2], shape[0]
 
 
-def _same(o, q):
-    if o.shape != q.shape:
-        raise ValueError("o: the shape of q expected")
-    return _ptr(o)
+def _out(o, shape):
+    """Address and type of the outputs."""
+    if o.shape != shape or not o.is_contiguous():
+        raise ValueError("o: contiguous, the shape of q expected")
+    if o.dtype not in _OUT_TYPES:
+        raise ValueError("o: float32 or bfloat16 expected")
+    return o.data_ptr(), _OUT_TYPES[o.dtype]
 
 
 def nq_attn_prompt(q, k, v, cu_q, cu_k, scale, o, lse=None):
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    if k.shape != v.shape or k.shape[2] != q.shape[2] or cu_q.numel() != cu_k.numel():
+    qh, kh = q.shape, k.shape
+    qp, qs = _rows(q, qh, "q")
+    kp, ks = _rows(k, kh, "k")
+    vp, vs = _rows(v, kh, "v")
+    b = cu_q.numel() - 1
+    if v.shape != kh or kh[2] != qh[2] or cu_k.numel() != b + 1:
         raise ValueError("q, k and v must have the same D, k and v the same shape, cu_q and cu_k the same length")
-    (tq, hq, d), (tk, hkv, _), b = q.shape, k.shape, max(0, cu_q.numel() - 1)
-    _check(lib().nq_attn_prompt(qp, qs, kp, ks, vp, vs, _ints(cu_q, b + 1 if b else 0, "cu_q"), _ints(cu_k, b + 1 if b else 0, "cu_k"),
-                                b, tq, tk, hq, hkv, d, scale, _out_dt(o), _same(o, q),
-                                _floats(lse, 0 if lse is None else tq * hq, "lse"), _stream(q)), "nq_attn_prompt")
+    op, out = _out(o, qh)
+    cq, ck = _ints(cu_q, 0, "cu_q"), _ints(cu_k, 0, "cu_k")
+    lp = None if lse is None else _floats(lse, qh[0] * qh[1], "lse")
+    _check((_lib or lib()).nq_attn_prompt(qp, qs, kp, ks, vp, vs, cq, ck, b if b > 0 else 0, qh[0], kh[0], qh[1], kh[1], qh[2],
+                                          scale, out, op, lp, _stream(q)), "nq_attn_prompt")
 
 
 def nq_kv_append(fmt, k, v, k_scale, v_scale, page_table, lens, cu, k_pages, v_pages):
-    (kp, ks), (vp, vs) = _rows(k, "k"), _rows(v, "v")
-    if k.shape != v.shape:
+    kh = k.shape
+    kp, ks = _rows(k, kh, "k")
+    vp, vs = _rows(v, kh, "v")
+    if v.shape != kh:
         raise ValueError("k and v must have the same shape")
-    t, hkv, d = k.shape
-    (tp, b, width), (kpp, vpp, ps, pages) = _table(page_table), _planes(fmt, k_pages, v_pages, hkv, d)
+    t, hkv, d = kh
+    tp, b, width = _table(page_table)
+    kpp, vpp, ps, pages = _planes(fmt, k_pages, v_pages, hkv, d)
     n = hkv if fmt == NQ_KV_E4M3 else 0
-    _check(lib().nq_kv_append(fmt, kp, ks, vp, vs, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"), tp, width,
-                              _ints(lens, b, "lens"), _ints(cu, b + 1, "cu"), b, t, hkv, d, ps, pages, kpp, vpp,
-                              _stream(k, k_pages)), "nq_kv_append")
+    _check((_lib or lib()).nq_kv_append(fmt, kp, ks, vp, vs, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"),
+                                        tp, width, _ints(lens, b, "lens"), _ints(cu, b + 1, "cu"), b, t, hkv, d, ps, pages,
+                                        kpp, vpp, _stream(k_pages)), "nq_kv_append")
 
 
 def nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len):
@@ -446,60 +477,70 @@ def alloc_attn_tree_workspace(B, max_q, Hq, Hkv, D, max_len, device):
 
 def nq_attn_tree(fmt, q, k_pages, v_pages, k_scale, v_scale, page_table, lens, cu_q, tree_mask, max_q, max_len, scale, o,
                  lse=None, workspace=None):
-    qp, qs = _rows(q, "q")
-    t, hq, d = q.shape
+    qh = q.shape
+    qp, qs = _rows(q, qh, "q")
+    t, hq, d = qh
     hkv = k_pages.shape[1] if k_pages.dim() == 4 else 0
-    (tp, b, width), (kpp, vpp, ps, pages) = _table(page_table), _planes(fmt, k_pages, v_pages, hkv, d)
+    tp, b, width = _table(page_table)
+    kpp, vpp, ps, pages = _planes(fmt, k_pages, v_pages, hkv, d)
     n = hkv if fmt == NQ_KV_E4M3 else 0
     wp, wb = _ws(workspace)
-    _check(lib().nq_attn_tree(fmt, qp, qs, kpp, vpp, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"), tp, width,
-                              _ints(lens, b, "lens"), _ints(cu_q, b + 1, "cu_q"), _ints(tree_mask, t, "tree_mask", 8), b,
-                              max_q, t, hq, hkv, d, ps, pages, max_len, scale, _out_dt(o), _same(o, q),
-                              _floats(lse, 0 if lse is None else t * hq, "lse"), wp, wb, _stream(q)), "nq_attn_tree")
+    op, out = _out(o, qh)
+    lp = None if lse is None else _floats(lse, t * hq, "lse")
+    _check((_lib or lib()).nq_attn_tree(fmt, qp, qs, kpp, vpp, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"),
+                                        tp, width, _ints(lens, b, "lens"), _ints(cu_q, b + 1, "cu_q"),
+                                        _ints(tree_mask, t, "tree_mask", _INT64), b, max_q, t, hq, hkv, d, ps, pages,
+                                        max_len, scale, out, op, lp, wp, wb, _stream(q)), "nq_attn_tree")
 
 
 def nq_kv_reserve(refs, page_table, lens, new_lens, page_size, free_list, shortfall):
-    (tp, b, width), pages = _table(page_table), refs.numel()
-    _check(lib().nq_kv_reserve(_ints(refs, pages, "refs"), pages, tp, width, _ints(lens, b, "lens"),
-                               _ints(new_lens, b, "new_lens"), b, page_size, _ints(free_list, pages, "free_list"),
-                               _ints(shortfall, 1, "shortfall"), _stream(refs)), "nq_kv_reserve")
+    tp, b, width = _table(page_table)
+    pages = refs.numel()
+    _check((_lib or lib()).nq_kv_reserve(_ints(refs, pages, "refs"), pages, tp, width, _ints(lens, b, "lens"),
+                                         _ints(new_lens, b, "new_lens"), b, page_size, _ints(free_list, pages, "free_list"),
+                                         _ints(shortfall, 1, "shortfall"), _stream(refs)), "nq_kv_reserve")
 
 
 def nq_kv_release(refs, page_table, keep_lens, page_size):
-    (tp, b, width), pages = _table(page_table), refs.numel()
-    _check(lib().nq_kv_release(_ints(refs, pages, "refs"), pages, tp, width, _ints(keep_lens, b, "keep_lens"), b, page_size,
-                               _stream(refs)), "nq_kv_release")
+    tp, b, width = _table(page_table)
+    pages = refs.numel()
+    _check((_lib or lib()).nq_kv_release(_ints(refs, pages, "refs"), pages, tp, width, _ints(keep_lens, b, "keep_lens"), b,
+                                         page_size, _stream(refs)), "nq_kv_release")
 
 
 def nq_kv_fork(refs, page_table, lens, parents, page_size, child_table, copies, free_list, shortfall):
-    (tp, b, width), (cp, children, cwidth), pages = _table(page_table), _table(child_table), refs.numel()
+    tp, b, width = _table(page_table)
+    cp, children, cwidth = _table(child_table)
+    pages = refs.numel()
     if cwidth != width or parents.numel() != children:
         raise ValueError("child_table: [children][width] expected")
-    _check(lib().nq_kv_fork(_ints(refs, pages, "refs"), pages, tp, width, _ints(lens, b, "lens"), b,
-                            _ints(parents, children, "parents"), children, page_size, cp,
-                            _ints(copies, 2 * children, "copies"), _ints(free_list, pages, "free_list"),
-                            _ints(shortfall, 1, "shortfall"), _stream(refs)), "nq_kv_fork")
+    _check((_lib or lib()).nq_kv_fork(_ints(refs, pages, "refs"), pages, tp, width, _ints(lens, b, "lens"), b,
+                                      _ints(parents, children, "parents"), children, page_size, cp,
+                                      _ints(copies, 2 * children, "copies"), _ints(free_list, pages, "free_list"),
+                                      _ints(shortfall, 1, "shortfall"), _stream(refs)), "nq_kv_fork")
 
 
 def _pool(pool):
-    """Address, planes, bytes of a plane and of a page, pages of [planes][pages][Hkv][page_size][D]."""
-    if pool.dim() != 5:
-        raise ValueError("pool: [planes][pages][Hkv][page_size][D] expected")
-    planes, pages, h, ps, d = pool.shape
-    page = h * ps * d * pool.element_size()
-    return _ptr(pool), planes, pages * page, page, pages
+    """Address, shape, bytes of an element, of a page and of a plane of [planes][pages][Hkv][page_size][D]."""
+    shape = pool.shape
+    if len(shape) != 5 or not pool.is_contiguous():
+        raise ValueError("pool: contiguous [planes][pages][Hkv][page_size][D] expected")
+    size = pool.element_size()
+    page = shape[2] * shape[3] * shape[4] * size
+    return pool.data_ptr(), shape, size, page, shape[1] * page
 
 
 def nq_kv_copy_pages(pool, copies):
-    p, planes, plane, page, pages = _pool(pool)
+    p, shape, _, page, plane = _pool(pool)
     n = copies.numel() // 2
-    _check(lib().nq_kv_copy_pages(p, planes, plane, page, pages, _ints(copies, 2 * n, "copies"), n, _stream(pool)),
-           "nq_kv_copy_pages")
+    _check((_lib or lib()).nq_kv_copy_pages(p, shape[0], plane, page, shape[1], _ints(copies, 2 * n, "copies"), n,
+                                            _stream(pool)), "nq_kv_copy_pages")
 
 
 def nq_kv_compact(pool, page_table, lens, accept, cu_accept):
-    (p, planes, plane, _, pages), (tp, b, width) = _pool(pool), _table(page_table)
-    _, _, h, ps, d = pool.shape
-    _check(lib().nq_kv_compact(p, planes, plane, h, ps, d * pool.element_size(), pages, tp, width, _ints(lens, b, "lens"),
-                               _ints(accept, accept.numel(), "accept"), _ints(cu_accept, b + 1, "cu_accept"), b,
-                               accept.numel(), _stream(pool)), "nq_kv_compact")
+    p, shape, size, _, plane = _pool(pool)
+    tp, b, width = _table(page_table)
+    n = accept.numel()
+    _check((_lib or lib()).nq_kv_compact(p, shape[0], plane, shape[2], shape[3], shape[4] * size, shape[1], tp, width,
+                                         _ints(lens, b, "lens"), _ints(accept, n, "accept"),
+                                         _ints(cu_accept, b + 1, "cu_accept"), b, n, _stream(pool)), "nq_kv_compact")
