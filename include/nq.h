@@ -543,9 +543,10 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
  *   planes, plane_bytes apart; pairs with a number outside [0, pages) are
  *   skipped.  No page may be written by one pair and named by another.
  * compact: the end of a verify step.  accept (int32, the drafted tokens that
- *   sequence b keeps, in order: accept[cu_accept[b]] ..) are moved together:
- *   row lens[b] + accept[i] to row lens[b] + i, in every plane, for i below 64.
- *   `accepted` is accept's length; rows without a page are skipped.
+ *   sequence b keeps, ascending: accept[cu_accept[b]] ..) are moved together:
+ *   row lens[b] + accept[i] to row lens[b] + i, in every plane, for i and
+ *   accept[i] below 64.  `accepted` is accept's length; rows without a page
+ *   are skipped.
  */
 nq_status nq_kv_reserve(int32_t* refs, int64_t pages, int32_t* page_table, int64_t width, const int32_t* lens,
                         const int32_t* new_lens, int64_t B, int64_t page_size, int32_t* free_list,

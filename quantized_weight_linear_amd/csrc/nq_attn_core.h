@@ -37,7 +37,12 @@ typedef __attribute__((address_space(3))) const unsigned char* lds_cptr;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
-constexpr int BUF_RAW = 0x00027000;      // raw buffer, no format conversion: loads past num_records give zeros
+constexpr int BUF_RAW = 0x00027000;      // raw buffer, no format conversion
+
+// Arrays of the call that no kernel of it writes, read at uniform places: by
+// scalar loads, which no wait for vector loads in flight holds up.
+typedef __attribute__((address_space(4))) const int32_t* uniform_ints;
+__device__ __forceinline__ int uniform(const int32_t* p, int64_t i) { return ((uniform_ints)(uintptr_t)p)[i]; }
 
 // A tile's rows in LDS: key-major, ROW bytes a key, in 16-byte chunks whose
 // place in the row is permuted by the key's low four bits (XOR), so that the
@@ -58,9 +63,21 @@ struct Tile {
     }
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, int rows, int stride_bytes, int row_bytes) {
-    const int n = rows > 0 ? (rows - 1) * stride_bytes + row_bytes : 0;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, n, BUF_RAW);
+// A raw buffer of `rows` rows from base on: loads past it give zeros.
+__device__ __forceinline__ v4i rows_rsrc(const void* base, int rows, int stride_bytes, int row_bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    return v4i{(int)(uint32_t)at, (int)(uint32_t)(at >> 32) & 0xFFFF, rows > 0 ? (rows - 1) * stride_bytes + row_bytes : 0, BUF_RAW};
+}
+
+// 16 bytes a lane from the buffer at `off` to LDS at dst + 16 lane.  Written
+// as one instruction, not as the builtin: the compiler would wait for every
+// such load in flight before any LDS read that it cannot tell from their
+// targets.  Whoever reads the rows waits with wait_vm.  (No register is
+// written; the wait state between M0 and its use is part of the block.)
+__device__ __forceinline__ void load_to_lds(v4i r, int off, lds_ptr dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r)
+                 : "memory", "m0");
 }
 
 // 16 rows (keys 16-aligned in the tile) from memory into LDS at dst, no
@@ -77,17 +94,16 @@ struct Stager {
     }
     // The 1 KiB pieces [FIRST, FIRST + N) of the 16 rows' LOADS16.
     template <int FIRST, int N>
-    __device__ __forceinline__ void pieces(__amdgpu_buffer_rsrc_t r, lds_ptr dst) const {
+    __device__ __forceinline__ void pieces(v4i r, lds_ptr dst) const {
         int at = chunk0;
-        if (N >= 4) asm volatile("" : "+v"(at));         // offsets are formed as they are needed, not kept in registers
+        asm volatile("" : "+v"(at));                     // offsets are formed as they are needed, not kept in registers
 #pragma unroll
         for (int i = FIRST; i < FIRST + N; ++i) {
             const int off = (at ^ (T::sw(i * T::RPI) << 4)) + first + i * T::RPI * stride;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) uint32_t*)(dst + i * 1024), 16,
-                                                     off, 0, 0, 0);
+            load_to_lds(r, off, dst + i * 1024);
         }
     }
-    __device__ __forceinline__ void rows16(__amdgpu_buffer_rsrc_t r, lds_ptr dst) const {
+    __device__ __forceinline__ void rows16(v4i r, lds_ptr dst) const {
         pieces<0, T::LOADS16>(r, dst);
     }
 };
@@ -211,6 +227,14 @@ struct Rows {
             q[b][s] = as_frag(row ? *reinterpret_cast<const v4u*>(row + col) : v4u{0u, 0u, 0u, 0u});
         }
     }
+    // Waits for the queries here, once: a wait at their first use would stand
+    // in the loop over the keys and hold up its loads in every turn.
+    __device__ __forceinline__ void queries_ready() {
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+#pragma unroll
+            for (int s = 0; s < NS; ++s) asm volatile("" : "+v"(q[b][s]));
+    }
 
     // The reads' places: a chunk number is XORed into the row's permuted place
     // (low four chunk bits), further chunks and rows are added.  LEAN: formed
@@ -271,7 +295,7 @@ struct Rows {
                     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, q[b][2 * d + 1], s[b], 0, 0, 0);
                 }
             }
-            in_turn<2, ND, 1, 2 * QB>();
+            in_turn<3, ND, 1, 2 * QB>();
         } else {
 #pragma unroll
             for (int st = 0; st < NS; ++st) {
@@ -372,7 +396,7 @@ struct Rows {
                         o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[b][e], o[b][d], 0, 0, 0);
             }
         }
-        in_turn<2, 2 * ND, FP8 ? 1 : 2, QB * TERMS>();
+        in_turn<FP8 ? 4 : 2, 2 * ND, FP8 ? 1 : 2, QB * TERMS>();
     }
 
     // Values that are not finite, of keys that some rows do not see: a product

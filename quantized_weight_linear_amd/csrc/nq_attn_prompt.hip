@@ -27,7 +27,7 @@ struct PromptArgs {
 
 // A packed offset, kept inside [0, total] and in order whatever the array holds.
 __device__ __forceinline__ int64_t offset_of(const int32_t* cu, int i, int64_t total) {
-    const int64_t x = cu[i];
+    const int64_t x = uniform(cu, i);
     return x < 0 ? 0 : x > total ? total : x;
 }
 
@@ -35,11 +35,11 @@ struct PackedRows {                 // K or V rows of one sequence and KV head
     const uint16_t *k, *v;
     int k_stride, v_stride;         // bytes
     int n, row_bytes;
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t k_rows(int key) const {
+    __device__ __forceinline__ v4i k_rows(int key) const {
         const int rows = n - key < 16 ? n - key : 16;
         return rows_rsrc((const char*)k + (rows > 0 ? (int64_t)key * k_stride : 0), rows, k_stride, row_bytes);
     }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t v_rows(int key) const {
+    __device__ __forceinline__ v4i v_rows(int key) const {
         const int rows = n - key < 16 ? n - key : 16;
         return rows_rsrc((const char*)v + (rows > 0 ? (int64_t)key * v_stride : 0), rows, v_stride, row_bytes);
     }
@@ -89,7 +89,6 @@ __global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptAr
     for (int i = 0; i < QB; ++i) {
         row[i] = first + (wave * QB + i) * 32 + (lane & 31);
         sees.limit[i] = row[i] + 1 + ahead;
-        R.load_q(i, row[i] < nq ? a.q + (q0 + row[i]) * a.qs + head * D : nullptr);
     }
     PackedRows src;
     src.k = a.k + k0 * a.ks + kvh * D;
@@ -99,7 +98,11 @@ __global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptAr
     src.n = nk;
     src.row_bytes = D * 2;
     const int end = last + ahead;                       // keys that the tile's last row sees
-    attend_rows<RING, NW, D, QB, false, !BF16OUT>(R, (lds_ptr)smem, 0, end, src, sees, wave, lane);
+    auto queries = [&] {
+#pragma unroll
+        for (int i = 0; i < QB; ++i) R.load_q(i, row[i] < nq ? a.q + (q0 + row[i]) * a.qs + head * D : nullptr);
+    };
+    attend_rows<RING, NW>(R, (lds_ptr)smem, 0, end, src, sees, queries, wave, lane);
 #pragma unroll
     for (int i = 0; i < QB; ++i) {
         const float l = halves_sum(R.l[i]), inv = inverse_sum(l);

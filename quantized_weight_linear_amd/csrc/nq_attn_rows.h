@@ -38,9 +38,11 @@ __device__ __forceinline__ void lds_barrier() {
 // Sees: all_before() = every row of the workgroup sees all keys below it;
 // none_from() = no row of this wave sees keys from it on; seen(b, key) = the
 // 64 keys from `key` on as bits, for this lane's row of block b.
-template <int RING, int NW, int D, int QB, bool FP8, bool SPLITP, class Source, class Sees>
+// Queries: loads the rows' queries; called once the first keys are on their way.
+template <int RING, int NW, int D, int QB, bool FP8, bool SPLITP, class Source, class Sees, class Queries>
 __device__ __forceinline__ void attend_rows(Rows<D, QB, FP8, SPLITP>& R, lds_ptr lds, int key0, int key1,
-                                            const Source& src, const Sees& sees, int wave, int lane) {
+                                            const Source& src, const Sees& sees, const Queries& queries,
+                                            int wave, int lane) {
     using L = RowsLds<D, FP8, NW, RING>;
     using T = Tile<D, FP8>;
     constexpr int ROW = T::ROW, LOADS = 4 * T::LOADS16 / NW;          // a wave's load instructions a step
@@ -48,7 +50,7 @@ __device__ __forceinline__ void attend_rows(Rows<D, QB, FP8, SPLITP>& R, lds_ptr
     const int group = wave & 3, part = (group & 1) * 16;             // groups 0, 1: K; 2, 3: V
     const Stager<D, FP8> st(lane, group < 2 ? src.k_stride : src.v_stride);
     const lds_ptr k_ring = lds, v_ring = lds + RING * L::TILE;
-    auto load = [&](__amdgpu_buffer_rsrc_t r, lds_ptr dst) {
+    auto load = [&](v4i r, lds_ptr dst) {
         if (NW == 4 || wave < 4) st.template pieces<0, LOADS>(r, dst);
         else st.template pieces<NW == 4 ? 0 : LOADS, LOADS>(r, dst);
     };
@@ -61,6 +63,8 @@ __device__ __forceinline__ void attend_rows(Rows<D, QB, FP8, SPLITP>& R, lds_ptr
     const int n = (key1 - key0 + KEYS - 1) / KEYS;
 #pragma unroll
     for (int i = 0; i < RING - 1; ++i) stage(i, i);
+    queries();
+    R.queries_ready();
     auto step = [&](int i, int slot, auto partly) {
         constexpr bool PARTLY = decltype(partly)::value;
         const int key = key0 + i * KEYS;

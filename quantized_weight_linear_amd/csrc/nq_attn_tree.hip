@@ -36,7 +36,7 @@ struct TreeArgs {
     float* lse;
     float* parts;                   // parts' outputs, then their (m c, l) pairs, then each sequence's (first part, parts)
     int want;                       // ranges to split all sequences' keys into, about (0: one a sequence)
-    int least;                      // keys of a range, at least and as a multiple
+    int least, step;                // keys of a range: at least, and a multiple of
     int row_tiles;
 };
 
@@ -44,14 +44,14 @@ struct TreeArgs {
 struct Seq {
     int64_t t0;
     int n, len, total;
-    __device__ __forceinline__ Seq(const TreeArgs& a, int b) {
-        int64_t x0 = a.cu[b], x1 = a.cu[b + 1];
+    // `b` is the same in all lanes: scalar loads
+    __device__ __forceinline__ Seq(const TreeArgs& a, int b) : Seq(a, uniform(a.cu, b), uniform(a.cu, b + 1), uniform(a.lens, b)) {}
+    __device__ __forceinline__ Seq(const TreeArgs& a, int64_t x0, int64_t x1, int64_t ln) {
         x0 = x0 < 0 ? 0 : x0 > a.t ? a.t : x0;
         x1 = x1 < x0 ? x0 : x1 > a.t ? a.t : x1;
         t0 = x0;
         n = (int)(x1 - x0 < a.max_q ? x1 - x0 : a.max_q);
         const int64_t cap = (int64_t)a.width << a.page_shift;
-        int64_t ln = a.lens[b];
         ln = ln < 0 ? 0 : ln > cap ? cap : ln;
         len = (int)ln;
         total = (int)(ln + n < cap ? ln + n : cap);
@@ -67,12 +67,32 @@ struct Range {
     int b, first, parts, key0, key1;                    // its sequence, number of the sequence's first range and of ranges
     __device__ __forceinline__ static int64_t keys_of(const TreeArgs& a, int b) {
         if (b >= a.seqs) return 0;
-        const Seq s(a, b);
+        const Seq s(a, a.cu[b], a.cu[b + 1], a.lens[b]);
         return s.n > 0 ? s.total : -1;                  // -1: nothing to do
+    }
+    // Keys of a range, for `all` keys in `busy` sequences, `top` in the longest.
+    __device__ __forceinline__ static int64_t length(const TreeArgs& a, int64_t all, int64_t top, int busy) {
+        if (a.want == 0) return (int64_t)1 << 30;
+        // the last range of each sequence is a part of one: aim at `busy` fewer
+        const int aim = a.want - busy > a.want / 2 ? a.want - busy : (a.want + 1) / 2;
+        int64_t chunk = (all + aim - 1) / aim;
+        if (chunk < (top + MOST_PARTS - 1) / MOST_PARTS) chunk = (top + MOST_PARTS - 1) / MOST_PARTS;
+        if (chunk < a.least) chunk = a.least;
+        return (chunk + a.step - 1) / a.step * a.step;
     }
     // Range `index`; b = -1 where there is none.
     __device__ __forceinline__ Range(const TreeArgs& a, int index) {
         const int lane = threadIdx.x & 63;
+        if (a.seqs == 1) {                              // the same without the lanes' exchanges (a third of a short decode step)
+            const Seq s(a, 0);
+            const int64_t c = length(a, s.total, s.total, s.total > 0);
+            first = 0;
+            parts = s.n == 0 ? 0 : s.total == 0 ? 1 : (int)((s.total + c - 1) / c);
+            b = index < parts ? 0 : -1;
+            key0 = (int)(index * c < s.total ? index * c : s.total);
+            key1 = (int)(key0 + c < s.total ? key0 + c : s.total);
+            return;
+        }
         int64_t all = 0, top = 0;
         int busy = 0;
         for (int b0 = 0; b0 < a.seqs; b0 += 64) {
@@ -88,15 +108,7 @@ struct Range {
             top = o > top ? o : top;
             busy += __shfl_xor(busy, off, 64);
         }
-        int64_t chunk = (int64_t)1 << 30;
-        if (a.want > 0) {
-            // the last range of each sequence is a part of one: aim at `busy` fewer
-            const int aim = a.want - busy > a.want / 2 ? a.want - busy : (a.want + 1) / 2;
-            chunk = (all + aim - 1) / aim;
-            if (chunk < (top + MOST_PARTS - 1) / MOST_PARTS) chunk = (top + MOST_PARTS - 1) / MOST_PARTS;
-            chunk = (chunk + a.least - 1) / a.least * a.least;
-            if (chunk < a.least) chunk = a.least;
-        }
+        const int64_t chunk = length(a, all, top, busy);
         b = -1;
         int before = 0;
         for (int b0 = 0; b0 < a.seqs && b < 0; b0 += 64) {
@@ -122,8 +134,8 @@ struct Range {
         parts = __builtin_amdgcn_readfirstlane(parts);
         first = __builtin_amdgcn_readfirstlane(first);
         const int64_t total = keys_of(a, b), from = (index - first) * chunk;
-        key0 = (int)from;
-        key1 = (int)(from + chunk < total ? from + chunk : total);
+        key0 = __builtin_amdgcn_readfirstlane((int)from);
+        key1 = __builtin_amdgcn_readfirstlane((int)(from + chunk < total ? from + chunk : total));
     }
 };
 
@@ -137,15 +149,15 @@ struct PagedRows {
     int64_t page_bytes, head_bytes; // bytes of a page; of the heads before this one
     int page_shift, total;
     static constexpr int k_stride = Tile<D, FP8>::ROW, v_stride = Tile<D, FP8>::ROW;
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const char* base, int key) const {
+    __device__ __forceinline__ v4i rows(const char* base, int key) const {
         int rows = total - key < 16 ? total - key : 16;
-        const int64_t page = rows > 0 ? table[key >> page_shift] : -1;
+        const int64_t page = rows > 0 ? uniform(table, key >> page_shift) : -1;
         if (page < 0 || page >= pages) rows = 0;
         const int64_t at = rows > 0 ? page * page_bytes + head_bytes + (int64_t)(key & ((1 << page_shift) - 1)) * k_stride : 0;
         return rows_rsrc(base + at, rows, k_stride, k_stride);
     }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t k_rows(int key) const { return rows(k, key); }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t v_rows(int key) const { return rows(v, key); }
+    __device__ __forceinline__ v4i k_rows(int key) const { return rows(k, key); }
+    __device__ __forceinline__ v4i v_rows(int key) const { return rows(v, key); }
 };
 
 template <int QB>
@@ -177,16 +189,18 @@ __device__ __forceinline__ int2* part_ranges(const TreeArgs& a, int d) {
 template <int D, int QB, bool FP8, bool BF16OUT>
 struct TreeRows {
     static constexpr bool SPLITP = !BF16OUT;
-    __device__ static void load(Rows<D, QB, FP8, SPLITP>& R, TreeSees<QB>& sees, const TreeArgs& a, const Seq& s, int kvh,
-                                const int (&row)[QB]) {
+    __device__ static void masks(TreeSees<QB>& sees, const TreeArgs& a, const Seq& s, const int (&row)[QB]) {
         sees.len = s.len;
 #pragma unroll
-        for (int i = 0; i < QB; ++i) {
-            const bool real = row[i] < s.n * a.group;
-            const int tok = real ? row[i] / a.group : 0, head = kvh * a.group + (real ? row[i] % a.group : 0);
-            sees.mask[i] = real ? a.masks[s.t0 + tok] & bits_below(s.total - s.len) : ~0ull;
-            R.load_q(i, real ? a.q + (s.t0 + tok) * a.qs + (int64_t)head * D : nullptr);
-        }
+        for (int i = 0; i < QB; ++i)
+            sees.mask[i] = row[i] < s.n * a.group ? a.masks[s.t0 + row[i] / a.group] & bits_below(s.total - s.len) : ~0ull;
+    }
+    __device__ static void load(Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int kvh, const int (&row)[QB]) {
+#pragma unroll
+        for (int i = 0; i < QB; ++i)
+            R.load_q(i, row[i] < s.n * a.group ? a.q + (s.t0 + row[i] / a.group) * a.qs +
+                                                     (int64_t)(kvh * a.group + row[i] % a.group) * D
+                                               : nullptr);
     }
     // Results of one row block: outputs, or a part of them.
     __device__ static void store(const Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int range, int kvh, bool only,
@@ -244,9 +258,10 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 2 : D == 128 ? 3 : 4) void attn
     TreeSees<1> sees;
     const int row[1] = {(rt * NW + wave) * 32 + (lane & 31)};
     sees.none = (rt * NW + wave) * 32 < s.n * a.group ? 1 << 30 : 0;
-    TreeRows<D, 1, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
+    TreeRows<D, 1, FP8, BF16OUT>::masks(sees, a, s, row);
     const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
-    attend_rows<2, NW>(R, (lds_ptr)smem, r.key0, r.key1, src, sees, wave, lane);
+    auto queries = [&] { TreeRows<D, 1, FP8, BF16OUT>::load(R, a, s, kvh, row); };
+    attend_rows<2, NW>(R, (lds_ptr)smem, r.key0, r.key1, src, sees, queries, wave, lane);
     TreeRows<D, 1, FP8, BF16OUT>::store(R, a, s, range, kvh, r.parts == 1, 0, row[0]);
 }
 
@@ -256,8 +271,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 2 : D == 128 ? 3 : 4) void attn
 template <int D, bool FP8, int NW>
 struct KeysLds {
     static constexpr int TILE = 32 * Tile<D, FP8>::ROW;
-    static constexpr int RING = TILE >= 16384 ? 1 : TILE >= 8192 ? 2 : 4;
-    static constexpr int WAVE = 2 * RING * TILE;                    // 32 KiB (D = 64, E4M3: 16 KiB)
+    static constexpr int RING = TILE >= 8192 ? 1 : TILE >= 4096 ? 2 : 4;
+    static constexpr int WAVE = 2 * RING * TILE;                    // 16 KiB (BF16 rows of 256: 32 KiB)
     static constexpr int JOIN = NW * 32 * (D + 4) * 4;              // the waves' results at the end
     static constexpr int BYTES = NW * WAVE > JOIN ? NW * WAVE : JOIN;
 };
@@ -277,7 +292,7 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
     R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
     TreeSees<1> sees;
     const int row[1] = {lane & 31};
-    TreeRows<D, 1, FP8, BF16OUT>::load(R, sees, a, s, kvh, row);
+    TreeRows<D, 1, FP8, BF16OUT>::masks(sees, a, s, row);
     PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
     src.total = r.key1;                                   // keys past the range: no rows, zeros
     const Stager<D, FP8> st(lane, Tile<D, FP8>::ROW);
@@ -297,6 +312,8 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
         load_k(from + i * STEP, i);
         load_v(from + i * STEP, i);
     }
+    TreeRows<D, 1, FP8, BF16OUT>::load(R, a, s, kvh, row);
+    R.queries_ready();
     int slot = 0;
     for (int key = from; key < r.key1; key += STEP) {
         const lds_ptr k = mine + slot * 2 * L::TILE, v = k + L::TILE;
@@ -373,61 +390,72 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
 }
 
 // The parts of a row, joined in the order of their keys (one result whatever
-// the order in which the parts were made).  One workgroup a row: wave w sums
-// every fourth part, then the waves are added.
-template <int D, bool BF16OUT>
-__global__ __launch_bounds__(256) void attn_tree_join_kernel(TreeArgs a) {
-    __shared__ float top_s[4], sum_s[4];
-    __shared__ __align__(16) float o_s[4][D];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// the order in which the parts were made).  WAVES waves a row, each summing
+// every WAVES-th part; then the waves are added.
+template <int D, int WAVES, bool BF16OUT>
+__global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) {
+    __shared__ float sum_s[WAVES];
+    __shared__ __align__(16) float o_s[WAVES][D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rows = a.max_q * a.group;
     const int row = blockIdx.x % rows, kvh = blockIdx.x / rows % a.hkv, b = blockIdx.x / rows / a.hkv;
     const Seq s(a, b);
     if (row >= s.n * a.group) return;
-    const int2 r = part_ranges(a, D)[b];                // (first part, parts)
-    if (r.y <= 1) return;
+    const int* ranges = reinterpret_cast<const int*>(part_ranges(a, D));
+    const int first = uniform(ranges, 2 * b), parts = uniform(ranges, 2 * b + 1);
+    if (parts <= 1) return;
     const float2* ml = part_sums(a, D);
-    constexpr int W = D / 64, BATCH = 8;                // columns a lane: 1, 2 or 4
+    constexpr int W = D / 64, BATCH = 16;               // columns a lane; parts whose loads are in flight together
+    typedef float vw __attribute__((ext_vector_type(W)));
     float top = -INFINITY;
-    for (int i = lane; i < r.y; i += 64) {
-        const float2 p = ml[part_row(a, r.x + i, kvh, row)];
+    for (int i = lane; i < parts; i += 64) {
+        const float2 p = ml[part_row(a, first + i, kvh, row)];
         if (p.y != 0.f) top = max2(top, p.x);
     }
-    top = wave_max(top);
     float sum = 0.f, x[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) x[j] = 0.f;
-    for (int i0 = wave; i0 < r.y; i0 += 4 * BATCH) {    // the loads of BATCH parts are in flight together
+    bool have = false;
+    for (int i0 = wave; i0 < parts; i0 += WAVES * BATCH) {
         float2 p[BATCH];
-        float y[BATCH][W];
+        vw y[BATCH];
 #pragma unroll
         for (int e = 0; e < BATCH; ++e) {
-            const int64_t at = part_row(a, r.x + (i0 + 4 * e < r.y ? i0 + 4 * e : i0), kvh, row);
+            const int64_t at = part_row(a, first + (i0 + WAVES * e < parts ? i0 + WAVES * e : i0), kvh, row);
             p[e] = ml[at];
-#pragma unroll
-            for (int j = 0; j < W; ++j) y[e][j] = a.parts[at * D + lane * W + j];
+            y[e] = *reinterpret_cast<const vw*>(a.parts + at * D + lane * W);
         }
+        if (!have) top = wave_max(top);                 // (beside the first loads)
+        have = true;
 #pragma unroll
         for (int e = 0; e < BATCH; ++e) {
-            const bool real = i0 + 4 * e < r.y && p[e].y != 0.f;        // (a part that saw nothing has neither)
+            const bool real = i0 + WAVES * e < parts && p[e].y != 0.f;        // (a part that saw nothing has neither)
             const float f = real ? __builtin_amdgcn_exp2f(p[e].x - top) : 0.f;
-            sum += p[e].y * f;
+            sum += real ? p[e].y * f : 0.f;
 #pragma unroll
             for (int j = 0; j < W; ++j) x[j] += real ? y[e][j] * f : 0.f;
         }
     }
+    if (!have) top = wave_max(top);
+    if constexpr (WAVES > 1) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) o_s[wave][lane * W + j] = x[j];
-    if (lane == 0) sum_s[wave] = sum;
-    __syncthreads();
-    if (wave != 0) return;
-    sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+        for (int j = 0; j < W; ++j) o_s[wave][lane * W + j] = x[j];
+        if (lane == 0) sum_s[wave] = sum;
+        __syncthreads();
+        if (wave != 0) return;
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            sum += sum_s[w];
+#pragma unroll
+            for (int j = 0; j < W; ++j) x[j] += o_s[w][lane * W + j];
+        }
+    }
     const float f = inverse_sum(sum) * (a.v_scale ? a.v_scale[kvh] : 1.0f);
     const int64_t out = (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         const int col = lane * W + j;
-        const float y = (o_s[0][col] + o_s[1][col] + o_s[2][col] + o_s[3][col]) * f;
+        const float y = x[j] * f;
         if constexpr (BF16OUT) reinterpret_cast<uint16_t*>(a.o)[out * D + col] = (uint16_t)f32_to_bf16_rne(y);
         else reinterpret_cast<float*>(a.o)[out * D + col] = y;
     }
@@ -467,7 +495,10 @@ hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.want > 0) {
-        attn_tree_join_kernel<D, BF16OUT><<<(unsigned)a.seqs * a.hkv * a.max_q * a.group, 256, 0, stream>>>(a);
+        // four waves a row where rows are few; one where they fill the CUs by themselves (most have one part then)
+        const unsigned rows = (unsigned)a.seqs * a.hkv * a.max_q * a.group;
+        if (rows < 2048) attn_tree_join_kernel<D, 4, BF16OUT><<<rows, 256, 0, stream>>>(a);
+        else attn_tree_join_kernel<D, 1, BF16OUT><<<rows, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
     return hipSuccess;
@@ -478,20 +509,21 @@ hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
 namespace {
 
 struct TreePlan {
-    int want, least, row_tiles;
+    int want, least, step, row_tiles;
     int64_t bytes;
 };
 
 // Ranges of 128 keys (four waves of 32) or, with more rows and so more to
-// write for each part, 256, and up.  Few sequences: one range a CU.  Many: about four
-// a CU, short enough that the last ones to run do not leave most CUs idle.
+// write for each part, 256, and up.  Few sequences: as many
+// workgroups as run at once.  Many: about four times as many, short enough
+// that the last ones to run do not leave most CUs idle.
 TreePlan tree_plan(bool fp8, int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
     const int64_t rows = max_q * (hq / hkv), tile = attn::tile_rows(rows, d, fp8), tiles = (rows + tile - 1) / tile;
     const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles, cus = device_cu_count();
-    TreePlan p{0, (int)least, (int)tiles, 0};
+    TreePlan p{0, (int)least, rows <= 32 ? 128 : 32, (int)tiles, 0};
     if (max_len <= least) return p;
-    const int64_t slots = cus * (tile == 128 ? 2 : 1);
-    int64_t want = (2 * units <= slots ? slots : 4 * slots) / (hkv * tiles);
+    const int64_t slots = cus * (tile == 256 || (tile == 32 && d == 256) ? 1 : 2);        // workgroups that run at once
+    int64_t want = (2 * units <= slots ? slots : 4 * cus) / (hkv * tiles);
     const int64_t most = seqs * ((max_len + least - 1) / least) + seqs;
     if (want > most) want = most;
     if (want < 1) want = 1;
@@ -519,7 +551,7 @@ hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const
     if (workspace_bytes < p.bytes) p.want = 0;
     const TreeArgs a{q, q_stride, k_pages, v_pages, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, table, (int)width, lens,
                      cu_q, masks, (int)seqs, (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size),
-                     pages, scale, o, lse, reinterpret_cast<float*>(workspace), p.want, p.least, p.row_tiles};
+                     pages, scale, o, lse, reinterpret_cast<float*>(workspace), p.want, p.least, p.step, p.row_tiles};
     switch (d) {
         case 64:
             return fp8 ? (bf16_out ? go_tree<64, true, true>(a, stream) : go_tree<64, true, false>(a, stream))

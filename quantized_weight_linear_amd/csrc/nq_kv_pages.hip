@@ -130,12 +130,14 @@ __device__ int collect_free(const int32_t* refs, int64_t pages, int wanted, int3
 __device__ __forceinline__ int64_t ceil_pages(int64_t n, int shift) { return n <= 0 ? 0 : (n + (1 << shift) - 1) >> shift; }
 
 // One workgroup: entries [lens >> shift, ceil(new_lens)) of each table row that
-// are negative get pages, rows in order.  A wave counts a row at a time; the
-// rows' first ranks go to `rank` (LDS).
+// are negative get pages, rows in order.  A thread takes a row with up to FEW
+// such entries (a decode step), a wave a longer one (a prompt); the rows'
+// counts, then first ranks, are in `rank` (LDS).
+constexpr int FEW = 4;
 __global__ __launch_bounds__(POOL_THREADS) void kv_reserve_kernel(int32_t* refs, int64_t pages, int32_t* table, int64_t width,
                                                                   const int32_t* lens, const int32_t* new_lens, int seqs,
                                                                   int shift, int32_t* list, int32_t* shortfall) {
-    extern __shared__ int rank[];                        // [seqs]
+    extern __shared__ int rank[];                        // [seqs]; -1 in the first pass: a wave counts the row
     __shared__ int part[POOL_THREADS / 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     auto range = [&](int b, int64_t& e0, int64_t& e1) {
@@ -143,7 +145,21 @@ __global__ __launch_bounds__(POOL_THREADS) void kv_reserve_kernel(int32_t* refs,
         e1 = ceil_pages(new_lens[b], shift);
         if (e1 > width) e1 = width;
     };
+    auto few = [&](int b, int64_t e0, int64_t e1) {      // the missing ones of a short row's entries, as bits
+        uint32_t missing = 0;
+#pragma unroll
+        for (int j = 0; j < FEW; ++j)
+            if (e0 + j < e1 && table[b * width + e0 + j] < 0) missing |= 1u << j;
+        return missing;
+    };
+    for (int b = threadIdx.x; b < seqs; b += POOL_THREADS) {
+        int64_t e0, e1;
+        range(b, e0, e1);
+        rank[b] = e1 - e0 > FEW ? -1 : __builtin_popcount(few(b, e0, e1));
+    }
+    __syncthreads();
     for (int b = wave; b < seqs; b += POOL_THREADS / 64) {
+        if (rank[b] >= 0) continue;
         int64_t e0, e1;
         range(b, e0, e1);
         int n = 0;
@@ -161,20 +177,30 @@ __global__ __launch_bounds__(POOL_THREADS) void kv_reserve_kernel(int32_t* refs,
         wanted += total;
     }
     const int found = wanted ? collect_free(refs, pages, wanted, list, part) : 0;
+    auto give = [&](int64_t entry, int at) {
+        if (at >= found) return;
+        const int32_t page = list[at];
+        table[entry] = page;
+        refs[page] = 1;
+    };
     __syncthreads();
-    for (int b = wave; b < seqs; b += POOL_THREADS / 64) {
+    for (int b = threadIdx.x; b < seqs && wanted; b += POOL_THREADS) {
         int64_t e0, e1;
         range(b, e0, e1);
+        if (e1 - e0 > FEW) continue;
+        int at = rank[b];
+        for (uint32_t missing = few(b, e0, e1); missing; missing &= missing - 1)
+            give(b * width + e0 + __builtin_ctz(missing), at++);
+    }
+    for (int b = wave; b < seqs && wanted; b += POOL_THREADS / 64) {
+        int64_t e0, e1;
+        range(b, e0, e1);
+        if (e1 - e0 <= FEW) continue;
         int r = rank[b];
         for (int64_t e = e0; e < e1; e += 64) {
             const bool mine = e + lane < e1 && table[b * width + e + lane] < 0;
             const uint64_t all = __ballot(mine);
-            const int at = r + __builtin_popcountll(all & ((1ull << lane) - 1));
-            if (mine && at < found) {
-                const int32_t page = list[at];
-                table[b * width + e + lane] = page;
-                refs[page] = 1;
-            }
+            if (mine) give(b * width + e + lane, r + __builtin_popcountll(all & ((1ull << lane) - 1)));
             r += __builtin_popcountll(all);
         }
     }
@@ -282,43 +308,57 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(char* pool, int64_t plane_
         if (at + j * 4096 < page_bytes) *reinterpret_cast<v4u*>(plane + dst * page_bytes + at + j * 4096) = x[j];
 }
 
-// The accepted rows of one (sequence, plane, head): all are read before any is
-// written, since a row may be both.
-constexpr int MOVE_ROWS = 64, MOVE_ROW_BYTES = 512, MOVE_PIECES = MOVE_ROWS * MOVE_ROW_BYTES / 16 / 256;
-__global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t plane_bytes, int hkv, int shift, int row_bytes,
-                                                         int64_t pages, const int32_t* table, int64_t width,
+// The accepted rows of a (sequence, head) in PLANES planes, one wave: the
+// places are worked out once for all planes, and the rows of a batch are all
+// read before any is written, since a row may be both.  Later batches never
+// read what an earlier one wrote: accepted tokens ascend, so the place that
+// row i moves to lies below every row read after it.
+constexpr int MOVE_ROWS = 64, MOVE_PLANES = 4, MOVE_BATCH = 4;
+__global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t plane_bytes, int planes, int hkv, int shift,
+                                                         int row_bytes, int64_t pages, const int32_t* table, int64_t width,
                                                          const int32_t* lens, const int32_t* accept, const int32_t* cu,
                                                          int64_t accepted) {
-    const int head = blockIdx.x % hkv, b = blockIdx.x / hkv;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = blockIdx.x % hkv, b = blockIdx.x / hkv, plane0 = (blockIdx.y * 4 + wave) * MOVE_PLANES;
     const int32_t* row = table + b * width;
     int64_t a0 = cu[b], a1 = cu[b + 1];
     a0 = a0 < 0 ? 0 : a0;
     a1 = a1 > accepted ? accepted : a1;
     const int n = (int)(a1 - a0 > MOVE_ROWS ? MOVE_ROWS : a1 - a0), len = lens[b], per = row_bytes / 16;
-    if (len < 0) return;
-    char* plane = pool + blockIdx.y * plane_bytes;
+    if (len < 0 || plane0 >= planes) return;
+    pool += plane0 * plane_bytes;
     auto place = [&](int64_t at) -> int64_t {
         const int64_t page = page_of(row, width, pages, shift, at);
         return page < 0 ? -1 : (((page * hkv + head) << shift) + (at & ((1 << shift) - 1))) * row_bytes;
     };
-    v4u x[MOVE_PIECES];
-    int64_t to[MOVE_PIECES];
+    for (int p0 = 0; p0 < n * per; p0 += 64 * MOVE_BATCH) {
+        int64_t src[MOVE_BATCH], dst[MOVE_BATCH];
+        v4u x[MOVE_BATCH][MOVE_PLANES];
 #pragma unroll
-    for (int j = 0; j < MOVE_PIECES; ++j) {
-        const int p = j * 256 + threadIdx.x, i = p / per;
-        to[j] = -1;
-        if (i >= n) continue;
-        const int from = accept[a0 + i];
-        if (from == i || from < 0 || from >= MOVE_ROWS) continue;
-        const int64_t src = place((int64_t)len + from), dst = place((int64_t)len + i);
-        if (src < 0 || dst < 0) continue;
-        to[j] = dst + p % per * 16;
-        x[j] = *reinterpret_cast<const v4u*>(plane + src + p % per * 16);
+        for (int j = 0; j < MOVE_BATCH; ++j) {
+            const int p = p0 + j * 64 + lane, i = p / per;
+            const int from = i < n ? accept[a0 + i] : i;
+            src[j] = dst[j] = -1;
+            if (from != i && from >= 0 && from < MOVE_ROWS) {
+                src[j] = place((int64_t)len + from);
+                dst[j] = place((int64_t)len + i);
+                if (src[j] < 0) dst[j] = -1;
+                src[j] += p % per * 16;
+                if (dst[j] >= 0) dst[j] += p % per * 16;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < MOVE_BATCH; ++j)
+#pragma unroll
+            for (int q = 0; q < MOVE_PLANES; ++q)
+                if (dst[j] >= 0 && plane0 + q < planes) x[j][q] = *reinterpret_cast<const v4u*>(pool + q * plane_bytes + src[j]);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < MOVE_BATCH; ++j)
+#pragma unroll
+            for (int q = 0; q < MOVE_PLANES; ++q)
+                if (dst[j] >= 0 && plane0 + q < planes) *reinterpret_cast<v4u*>(pool + q * plane_bytes + dst[j]) = x[j][q];
     }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < MOVE_PIECES; ++j)
-        if (to[j] >= 0) *reinterpret_cast<v4u*>(plane + to[j]) = x[j];
 }
 
 int shift_of(int64_t page_size) { return __builtin_ctzll(page_size); }
@@ -375,9 +415,9 @@ hipError_t launch_kv_compact(void* pool, int64_t planes, int64_t plane_bytes, in
                              int64_t row_bytes, int64_t pages, const int32_t* table, int64_t width, const int32_t* lens,
                              const int32_t* accept, const int32_t* cu_accept, int64_t seqs, int64_t accepted,
                              hipStream_t stream) {
-    kv_compact_kernel<<<dim3((unsigned)(seqs * hkv), (unsigned)planes), 256, 0, stream>>>(
-        (char*)pool, plane_bytes, (int)hkv, shift_of(page_size), (int)row_bytes, pages, table, width, lens, accept, cu_accept,
-        accepted);
+    kv_compact_kernel<<<dim3((unsigned)(seqs * hkv), (unsigned)((planes + 4 * MOVE_PLANES - 1) / (4 * MOVE_PLANES))), 256, 0,
+                        stream>>>((char*)pool, plane_bytes, (int)planes, (int)hkv, shift_of(page_size), (int)row_bytes, pages,
+                                  table, width, lens, accept, cu_accept, accepted);
     return hipGetLastError();
 }
 
