@@ -246,36 +246,32 @@ struct Rows {
     }
     __device__ __forceinline__ static int chunk(int at, int c) { return (at ^ ((c & 15) << 4)) + (c >> 4) * 256; }
 
-    __device__ __forceinline__ v8bf v_frag(lds_cptr v, int at, int t, int d) const {
+    // The raw operand of V^T: 16 keys from 16 t on, columns 32 d ..
+    __device__ __forceinline__ v4u read_v(lds_cptr v, int at, int t, int d) const {
         if constexpr (FP8) {
             const v2i x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
                 (__attribute__((address_space(3))) v2i*)(v + chunk(at, 2 * d) + t * 16 * T::ROW));
-            return e4m3x8_to_frag(x[0], x[1]);
+            return v4u{(uint32_t)x[0], (uint32_t)x[1], 0u, 0u};
         } else {
             const lds_cptr rows = v + t * 16 * T::ROW;
             const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(rows + chunk(at, 4 * d)));
             const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) v4s*)(rows + chunk(at, (4 * d) ^ T::sw(8)) + 8 * T::ROW));
             const v2u a = __builtin_bit_cast(v2u, lo), b = __builtin_bit_cast(v2u, hi);
-            return as_frag(v4u{a[0], a[1], b[0], b[1]});
+            return v4u{a[0], a[1], b[0], b[1]};
         }
+    }
+    __device__ __forceinline__ static v8bf v_frag(v4u x) {
+        if constexpr (FP8) return e4m3x8_to_frag(x[0], x[1]);
+        else return as_frag(x);
     }
 
-    // The order of the instructions before it: the LDS reads of FIRST operands,
-    // then an operand's products and the reads of the next operand in turn, N
-    // operands in all (READS LDS reads and PRODUCTS products each).  Left to
-    // itself the compiler reads each operand right before its product, and
-    // every product waits for LDS (16384 causal tokens, 24 heads of 256: 15 %
-    // slower).  FIRST is what the registers bear: 4 for K, 2 for V, beside P.
-    template <int FIRST, int N, int READS, int PRODUCTS>
-    __device__ __forceinline__ static void in_turn() {
-        __builtin_amdgcn_sched_group_barrier(0x100, FIRST * READS, 0);
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-            __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS, 0);
-            if (x + FIRST < N) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-        }
-    }
+    // Keeps LDS reads and products in the order written (the vector and scalar
+    // unit's other work may cross).  Left to itself the compiler reads each
+    // operand right before its product, and every product waits for LDS; so
+    // the operands are read AHEAD products before their use.  AHEAD is what the
+    // registers bear beside the rest.
+    __device__ __forceinline__ static void in_order() { __builtin_amdgcn_sched_barrier(0x406); }
 
     // S^T of the 32 keys at k.
     __device__ __forceinline__ void logits(lds_cptr k, v16f (&s)[QB]) const {
@@ -284,26 +280,26 @@ struct Rows {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
         const int at = fresh(ka);
-        if constexpr (FP8) {
+        constexpr int READS = FP8 ? ND : NS, AHEAD = FP8 ? 3 : 4;          // 16 bytes a read: 16 codes or 8 values
+        v4u x[AHEAD];
+        auto read = [&](int i) { return *(__attribute__((address_space(3))) const v4u*)(k + chunk(at, 2 * i)); };
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const v4u x = *(__attribute__((address_space(3))) const v4u*)(k + chunk(at, 2 * d));
-                const v8bf f0 = e4m3x8_to_frag(x[0], x[1]), f1 = e4m3x8_to_frag(x[2], x[3]);
+        for (int i = 0; i < AHEAD && i < READS; ++i) x[i] = read(i);
+        in_order();
 #pragma unroll
-                for (int b = 0; b < QB; ++b) {
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f0, q[b][2 * d], s[b], 0, 0, 0);
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f1, q[b][2 * d + 1], s[b], 0, 0, 0);
+        for (int i = 0; i < READS; ++i) {
+            const v4u w = x[i % AHEAD];
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                if constexpr (FP8) {
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_frag(w[0], w[1]), q[b][2 * i], s[b], 0, 0, 0);
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_frag(w[2], w[3]), q[b][2 * i + 1], s[b], 0, 0, 0);
+                } else {
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(w), q[b][i], s[b], 0, 0, 0);
                 }
             }
-            in_turn<3, ND, 1, 2 * QB>();
-        } else {
-#pragma unroll
-            for (int st = 0; st < NS; ++st) {
-                const v8bf f = as_frag(*(__attribute__((address_space(3))) const v4u*)(k + chunk(at, 2 * st)));
-#pragma unroll
-                for (int b = 0; b < QB; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[b][st], s[b], 0, 0, 0);
-            }
-            in_turn<4, NS, 1, QB>();
+            if (i + AHEAD < READS) x[i % AHEAD] = read(i + AHEAD);
+            in_order();
         }
     }
 
@@ -381,22 +377,27 @@ struct Rows {
     // O^T += V^T P^T over the 32 keys at v.
     __device__ __forceinline__ void values(lds_cptr v, const v16f (&p)[QB]) {
         const int at = fresh(va);
+        constexpr int AHEAD = FP8 ? 4 : 2;
+        v4u x[AHEAD];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            v8bf pf[QB][TERMS];
+        for (int i = 0; i < AHEAD; ++i) x[i] = read_v(v, at, i / ND, i % ND);
+        in_order();
+        v8bf pf[QB][TERMS];
 #pragma unroll
-            for (int b = 0; b < QB; ++b) p_frag(p[b], 8 * t, pf[b]);
+        for (int i = 0; i < 2 * ND; ++i) {
+            if (i % ND == 0) {
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const v8bf f = v_frag(v, at, t, d);
-#pragma unroll
-                for (int e = 0; e < TERMS; ++e)
-#pragma unroll
-                    for (int b = 0; b < QB; ++b)
-                        o[b][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[b][e], o[b][d], 0, 0, 0);
+                for (int b = 0; b < QB; ++b) p_frag(p[b], 8 * (i / ND), pf[b]);
             }
+            const v8bf f = v_frag(x[i % AHEAD]);
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e)
+#pragma unroll
+                for (int b = 0; b < QB; ++b)
+                    o[b][i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[b][e], o[b][i % ND], 0, 0, 0);
+            if (i + AHEAD < 2 * ND) x[i % AHEAD] = read_v(v, at, (i + AHEAD) / ND, (i + AHEAD) % ND);
+            in_order();
         }
-        in_turn<FP8 ? 4 : 2, 2 * ND, FP8 ? 1 : 2, QB * TERMS>();
     }
 
     // Values that are not finite, of keys that some rows do not see: a product

@@ -7,7 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
-#include "nq_attn_rows.h"
+#include "nq_attn_keys.h"
 #include "nq_launch.h"
 
 namespace nq {
@@ -55,29 +55,84 @@ struct CausalSees {
     __device__ __forceinline__ uint64_t seen(int b, int key) const { return bits_below(limit[b] - key); }
 };
 
+// The tile of BM query rows that workgroup `index` of a head has: the
+// sequences in order, in each its last tile, which sees most keys, first.
+struct QueryTile {
+    int64_t q0, k0;                 // the sequence's first query and key
+    int nq, nk, first, last;        // its lengths; rows [first, last) of it
+    bool real;
+    __device__ __forceinline__ QueryTile(const PromptArgs& a, int index, int bm) {
+        int64_t q1 = 0;
+        int b = 0, tiles = 0;
+        q0 = 0;
+        for (; b < a.seqs; ++b) {
+            q0 = offset_of(a.cu_q, b, a.tq);
+            q1 = offset_of(a.cu_q, b + 1, a.tq);
+            tiles = q1 > q0 ? (int)((q1 - q0 + bm - 1) / bm) : 0;
+            if (index < tiles) break;
+            index -= tiles;
+        }
+        real = b < a.seqs;
+        if (!real) return;
+        k0 = offset_of(a.cu_k, b, a.tk);
+        const int64_t k1 = offset_of(a.cu_k, b + 1, a.tk);
+        nq = (int)(q1 - q0);
+        nk = k1 > k0 ? (int)(k1 - k0) : 0;
+        first = (tiles - 1 - index) * bm;
+        last = first + bm < nq ? first + bm : nq;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ PackedRows packed_rows(const PromptArgs& a, const QueryTile& t, int kvh, int keys) {
+    PackedRows src;
+    src.k = a.k + t.k0 * a.ks + kvh * D;
+    src.v = a.v + t.k0 * a.vs + kvh * D;
+    src.k_stride = (int)(a.ks * 2);
+    src.v_stride = (int)(a.vs * 2);
+    src.n = keys;
+    src.row_bytes = D * 2;
+    return src;
+}
+
+// Few tiles: 32 rows a workgroup, whose four waves take different keys.
+template <int D, bool BF16OUT>
+__global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = blockIdx.x % a.hq;
+    const QueryTile t(a, blockIdx.x / a.hq, 32);
+    if (!t.real) return;
+    const int ahead = t.nk - t.nq, row = t.first + (lane & 31);
+    Rows<D, 1, false, !BF16OUT> R;
+    R.init(lane, a.c);
+    CausalSees<1> sees;
+    sees.clean = t.first + 1 + ahead;
+    sees.none = t.last + ahead;
+    sees.limit[0] = row + 1 + ahead;
+    const int keys = t.last + ahead > 0 ? t.last + ahead : 0;
+    const PackedRows src = packed_rows<D>(a, t, head / (a.hq / a.hkv), keys);
+    auto queries = [&] { R.load_q(0, row < t.nq ? a.q + (t.q0 + row) * a.qs + head * D : nullptr); };
+    auto emit = [&](int i, int col, const v4f& x, float mc, float l) {
+        const int64_t out = (t.q0 + t.first + i) * a.hq + head;
+        const float f = inverse_sum(l);
+        store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        if (col == 0 && a.lse) a.lse[out] = log_sum_exp(mc, l);
+    };
+    attend_keys<4>(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
+}
+
+// Many tiles: NW waves with 32 QB rows each.
 template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
 __global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptArgs a) {
     constexpr int BM = NW * QB * 32;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.x % a.hq;
-    int tile = blockIdx.x / a.hq;
-    // which sequence, which tile of it (the last one, with the most keys, first)
-    int64_t q0 = 0, q1 = 0;
-    int b = 0, tiles = 0;
-    for (; b < a.seqs; ++b) {
-        q0 = offset_of(a.cu_q, b, a.tq);
-        q1 = offset_of(a.cu_q, b + 1, a.tq);
-        tiles = q1 > q0 ? (int)((q1 - q0 + BM - 1) / BM) : 0;
-        if (tile < tiles) break;
-        tile -= tiles;
-    }
-    if (b == a.seqs) return;
-    tile = tiles - 1 - tile;
-    const int64_t k0 = offset_of(a.cu_k, b, a.tk), k1 = offset_of(a.cu_k, b + 1, a.tk);
-    const int nq = (int)(q1 - q0), nk = k1 > k0 ? (int)(k1 - k0) : 0, ahead = nk - nq;
-    const int first = tile * BM, last = first + BM < nq ? first + BM : nq;      // rows [first, last)
-    const int kvh = head / (a.hq / a.hkv);
+    const QueryTile t(a, blockIdx.x / a.hq, BM);
+    if (!t.real) return;
+    const int64_t q0 = t.q0;
+    const int nq = t.nq, ahead = t.nk - t.nq, first = t.first, last = t.last;
 
     Rows<D, QB, false, !BF16OUT> R;
     R.init(lane, a.c);
@@ -90,13 +145,7 @@ __global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptAr
         row[i] = first + (wave * QB + i) * 32 + (lane & 31);
         sees.limit[i] = row[i] + 1 + ahead;
     }
-    PackedRows src;
-    src.k = a.k + k0 * a.ks + kvh * D;
-    src.v = a.v + k0 * a.vs + kvh * D;
-    src.k_stride = (int)(a.ks * 2);
-    src.v_stride = (int)(a.vs * 2);
-    src.n = nk;
-    src.row_bytes = D * 2;
+    const PackedRows src = packed_rows<D>(a, t, head / (a.hq / a.hkv), t.nk);
     const int end = last + ahead;                       // keys that the tile's last row sees
     auto queries = [&] {
 #pragma unroll
@@ -119,15 +168,26 @@ __global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptAr
     }
 }
 
+// Tiles of bm rows at most: every sequence may end in a part of one.
+int64_t tiles_of(const PromptArgs& a, int bm) { return a.tq / bm + (a.seqs < a.tq ? a.seqs : a.tq); }
+
 template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
 hipError_t go(const PromptArgs& a, hipStream_t stream) {
     constexpr int BM = NW * QB * 32, LDS = RowsLds<D, false, NW, RING>::BYTES;
     auto kernel = attn_prompt_kernel<D, QB, NW, RING, PER_SIMD, BF16OUT>;
     static LdsLimit limit;
     if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
-    // every sequence may end in a part of a tile
-    const int64_t tiles = a.tq / BM + (a.seqs < a.tq ? a.seqs : a.tq);
-    kernel<<<(unsigned)(tiles * a.hq), NW * 64, LDS, stream>>>(a);
+    kernel<<<(unsigned)(tiles_of(a, BM) * a.hq), NW * 64, LDS, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int D, bool BF16OUT>
+hipError_t go_keys(const PromptArgs& a, hipStream_t stream) {
+    constexpr int LDS = KeysLds<D, false, 4>::BYTES;
+    auto kernel = attn_prompt_keys_kernel<D, BF16OUT>;
+    static LdsLimit limit;
+    if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
+    kernel<<<(unsigned)(tiles_of(a, 32) * a.hq), 256, LDS, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -140,6 +200,18 @@ hipError_t launch_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_
     using namespace attn;
     const PromptArgs a{q, k, v, q_stride, k_stride, v_stride, cu_q, cu_k, (int)seqs, tq, tk, (int)hq, (int)hkv,
                        scale * LOG2E, o, lse};
+    // Few tiles of 128 rows: 32 rows a workgroup, so that more CUs have one
+    // and each row's keys are walked four at a time; 512 tokens of 24 heads of
+    // 256 take 25 us so and 29 us the other way, of 32 heads of 128 11 and 17,
+    // 1024 of 24 of 256 60 and 50.  (With two key tiles there is nothing to share out: 33
+    // tokens of 24 heads of 256 11 and 8.5 us.)
+    if (tiles_of(a, 128) * hq * (d == 256 ? 2 : 1) <= device_cu_count() && tk > 64 * seqs) {
+        switch (d) {
+            case 64: return bf16_out ? go_keys<64, true>(a, stream) : go_keys<64, false>(a, stream);
+            case 128: return bf16_out ? go_keys<128, true>(a, stream) : go_keys<128, false>(a, stream);
+            default: return bf16_out ? go_keys<256, true>(a, stream) : go_keys<256, false>(a, stream);
+        }
+    }
     switch (d) {
         case 64: return bf16_out ? go<64, 1, 4, 2, 4, true>(a, stream) : go<64, 1, 4, 2, 4, false>(a, stream);
         case 128: return bf16_out ? go<128, 1, 4, 2, 3, true>(a, stream) : go<128, 1, 4, 2, 3, false>(a, stream);

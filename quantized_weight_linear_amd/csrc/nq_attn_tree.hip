@@ -11,7 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
-#include "nq_attn_rows.h"
+#include "nq_attn_keys.h"
 #include "nq_launch.h"
 
 namespace nq {
@@ -265,22 +265,9 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 2 : D == 128 ? 3 : 4) void attn
     TreeRows<D, 1, FP8, BF16OUT>::store(R, a, s, range, kvh, r.parts == 1, 0, row[0]);
 }
 
-// Up to 32 rows: wave w takes every NW-th tile of 32 keys of the range, with a
-// ring of RING tiles of its own in LDS.  K and V of a tile are waited for
-// separately: each slot is loaded again as soon as it has been read.
-template <int D, bool FP8, int NW>
-struct KeysLds {
-    static constexpr int TILE = 32 * Tile<D, FP8>::ROW;
-    static constexpr int RING = TILE >= 8192 ? 1 : TILE >= 4096 ? 2 : 4;
-    static constexpr int WAVE = 2 * RING * TILE;                    // 16 KiB (BF16 rows of 256: 32 KiB)
-    static constexpr int JOIN = NW * 32 * (D + 4) * 4;              // the waves' results at the end
-    static constexpr int BYTES = NW * WAVE > JOIN ? NW * WAVE : JOIN;
-};
-
+// Up to 32 rows: the waves take different keys.
 template <int D, int NW, bool FP8, bool BF16OUT>
 __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
-    using L = KeysLds<D, FP8, NW>;
-    constexpr int LOADS = 2 * Tile<D, FP8>::LOADS16, R1 = (2 * L::RING - 1) * LOADS;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.hkv, range = blockIdx.x / a.hkv;
@@ -294,99 +281,23 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
     const int row[1] = {lane & 31};
     TreeRows<D, 1, FP8, BF16OUT>::masks(sees, a, s, row);
     PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
-    src.total = r.key1;                                   // keys past the range: no rows, zeros
-    const Stager<D, FP8> st(lane, Tile<D, FP8>::ROW);
-    const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
-    auto load_k = [&](int key, int slot) {
-        st.rows16(src.k_rows(key), mine + slot * 2 * L::TILE);
-        st.rows16(src.k_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE / 2);
-    };
-    auto load_v = [&](int key, int slot) {
-        st.rows16(src.v_rows(key), mine + slot * 2 * L::TILE + L::TILE);
-        st.rows16(src.v_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
-    };
-    constexpr int STEP = NW * 32;
-    const int from = r.key0 + wave * 32;
-#pragma unroll
-    for (int i = 0; i < L::RING; ++i) {
-        load_k(from + i * STEP, i);
-        load_v(from + i * STEP, i);
-    }
-    TreeRows<D, 1, FP8, BF16OUT>::load(R, a, s, kvh, row);
-    R.queries_ready();
-    int slot = 0;
-    for (int key = from; key < r.key1; key += STEP) {
-        const lds_ptr k = mine + slot * 2 * L::TILE, v = k + L::TILE;
-        v16f x[1];
-        uint64_t seen[1] = {~0ull};
-        const bool partly = key + 32 > sees.all_before();
-        if (partly) seen[0] = sees.seen(0, key);
-        wait_vm<R1>();
-        R.template weights<true>(k, seen, x);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
-        load_k(key + L::RING * STEP, slot);
-        wait_vm<R1>();
-        if (partly) {
-            if (const uint32_t bad = rows_not_finite<D, FP8, LOADS>(v, lane)) {
-                R.add_not_finite(v, bad, seen);
-                rows_made_finite<D, FP8, LOADS>((lds_ptr)v, lane);
-            }
-        }
-        R.values(v, x);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        load_v(key + L::RING * STEP, slot);
-        slot = slot + 1 == L::RING ? 0 : slot + 1;
-    }
-    // The waves' rows, joined: wave w's results go to LDS and every wave
-    // finishes D / NW columns' worth of each row.
-    wait_vm<0>();
-    __syncthreads();
-    float* join = reinterpret_cast<float*>(smem);
-    constexpr int PITCH = D + 4;                        // floats a row
-    const float l = halves_sum(R.l[0]);
-    float* at = join + (wave * 32 + (lane & 31)) * PITCH;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<v4f*>(at + R.column(d, e)) =
-                v4f{R.o[0][d][4 * e], R.o[0][d][4 * e + 1], R.o[0][d][4 * e + 2], R.o[0][d][4 * e + 3]};
-    if (lane < 32) {
-        at[D] = R.m[0] == -INFINITY ? -INFINITY : R.m[0] * R.c;
-        at[D + 1] = l;
-    }
-    __syncthreads();
+    src.total = r.key1;                                 // keys past the range: no rows, zeros
+    auto queries = [&] { TreeRows<D, 1, FP8, BF16OUT>::load(R, a, s, kvh, row); };
     const bool only = r.parts == 1;
     const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
-    constexpr int LANES = D / 4;                        // threads a row
-    for (int i = threadIdx.x / LANES; i < s.n * a.group; i += NW * 64 / LANES) {
-        const int col = threadIdx.x % LANES * 4;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) top = max2(top, join[(w * 32 + i) * PITCH + D]);
-        v4f x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float* p = join + (w * 32 + i) * PITCH;
-            const float lw = p[D + 1];
-            // a wave that saw nothing has neither sum nor outputs
-            const float f = lw == 0.f ? 0.f : __builtin_amdgcn_exp2f(p[D] == -INFINITY ? 0.f : p[D] - top);
-            const v4f y = *reinterpret_cast<const v4f*>(p + col);
-            sum += lw * f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] += y[j] * f;
-        }
-        const float mc = top == -INFINITY ? 0.f : top;
+    auto emit = [&](int i, int col, const v4f& x, float mc, float l) {
         const int64_t out = (s.t0 + i / a.group) * a.hq + kvh * a.group + i % a.group;
-        const int64_t part = part_row(a, range, kvh, i);
-        const float f = only ? inverse_sum(sum) * vs : 1.0f;
-        if (only) store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
-        else store4<false>(a.parts, part * D + col, x[0], x[1], x[2], x[3]);
-        if (col == 0) {
-            if (!only) part_sums(a, D)[part] = make_float2(mc, sum);
-            else if (a.lse) a.lse[out] = log_sum_exp(mc, sum);
+        if (only) {
+            const float f = inverse_sum(l) * vs;
+            store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+            if (col == 0 && a.lse) a.lse[out] = log_sum_exp(mc, l);
+        } else {
+            const int64_t part = part_row(a, range, kvh, i);
+            store4<false>(a.parts, part * D + col, x[0], x[1], x[2], x[3]);
+            if (col == 0) part_sums(a, D)[part] = make_float2(mc, l);
         }
-    }
+    };
+    attend_keys<NW>(R, smem, r.key0, r.key1, s.n * a.group, src, sees, queries, emit, wave, lane);
 }
 
 // The parts of a row, joined in the order of their keys (one result whatever
