@@ -443,13 +443,13 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
  *     runs; offsets outside the arrays are cut back to them.
  *   - o [Tq][Hq][D] is FP32 or BF16 (out_dt); lse [Tq][Hq] FP32, or NULL:
  *     the natural logarithm of the sum of exp(logits) (it joins this result
- *     with attention over other keys).  A row that sees no key gets o = 0 and
- *     lse = -infinity.  Keys and values that a row does not see do not touch
+ *     with attention over other keys).  A row that sees no key, or whose logits
+ *     are all -infinity, gets o = 0 and lse = -infinity.  Keys and values that a row does not see do not touch
  *     its result, whatever they hold, infinities and NaN included.
  *   - Logits, softmax statistics and sums are FP32.  The weights of the
  *     softmax are rounded to BF16 for a BF16 output, and to three BF16 terms
  *     (22 bits) for an FP32 output.
- *   - `scale` multiplies the logits; it must be finite and positive
+ *   - `scale` multiplies the logits; it must lie in [1e-30, 1e30]
  *     (NQ_ERR_RANGE).
  */
 

@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
-#include <cmath>
 #include <mutex>
 
 #include "nq.h"
@@ -606,7 +605,7 @@ bool table_ok(int64_t B, int64_t width, int64_t page_size, int64_t pages) {
     return B >= 0 && B < MOST_BLOCKS && width >= 0 && pages >= 0 && pages < I31 && page_ok(page_size) &&
            width * page_size <= ((int64_t)1 << 30);
 }
-bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.0f; }
+bool scale_ok(float scale) { return scale >= 1e-30f && scale <= 1e30f; }       // (false for NaN)
 
 template <class... P>
 nq_status all_there(P... p) {

@@ -1,8 +1,7 @@
 // Attention tiles on the BF16 matrix cores, shared by the prompt and the tree
 // kernels.
 //
-// A wave holds 32 query rows per block (QB blocks) as the columns of its
-// products.  For 32 keys at a time it forms S^T = K Q^T, so that lane l has
+// A wave holds 32 query rows as the columns of its products.  For 32 keys at a time it forms S^T = K Q^T, so that lane l has
 // the logits of query row l % 32 in its own registers (16 of the 32 keys, the
 // other half in lane l ^ 32): the reference and sum of the softmax are one
 // value per lane, and one exchange between the wave's halves joins the maxima.
@@ -92,19 +91,12 @@ struct Stager {
         first = lane / T::CH * stride;
         chunk0 = ((lane % T::CH) ^ T::sw(lane / T::CH)) << 4;
     }
-    // The 1 KiB pieces [FIRST, FIRST + N) of the 16 rows' LOADS16.
-    template <int FIRST, int N>
-    __device__ __forceinline__ void pieces(v4i r, lds_ptr dst) const {
+    __device__ __forceinline__ void rows16(v4i r, lds_ptr dst) const {
         int at = chunk0;
         asm volatile("" : "+v"(at));                     // offsets are formed as they are needed, not kept in registers
 #pragma unroll
-        for (int i = FIRST; i < FIRST + N; ++i) {
-            const int off = (at ^ (T::sw(i * T::RPI) << 4)) + first + i * T::RPI * stride;
-            load_to_lds(r, off, dst + i * 1024);
-        }
-    }
-    __device__ __forceinline__ void rows16(v4i r, lds_ptr dst) const {
-        pieces<0, T::LOADS16>(r, dst);
+        for (int i = 0; i < T::LOADS16; ++i)
+            load_to_lds(r, (at ^ (T::sw(i * T::RPI) << 4)) + first + i * T::RPI * stride, dst + i * 1024);
     }
 };
 
@@ -142,8 +134,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
     return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-// The staged rows at p that hold such a value, as bits: N 1 KiB pieces (N
-// RPI rows) that this wave has loaded.
+// The staged rows at p that hold such a value, as bits: N pieces of 1 KiB (RPI
+// rows each) that this wave has loaded.
 template <int D, bool FP8, int N>
 __device__ __forceinline__ uint32_t rows_not_finite(lds_cptr p, int lane) {
     using T = Tile<D, FP8>;
@@ -157,7 +149,7 @@ __device__ __forceinline__ uint32_t rows_not_finite(lds_cptr p, int lane) {
         const uint64_t lanes = __ballot(bad != 0);
         if (lanes) {
             for (int r = 0; r < T::RPI; ++r)
-                if (lanes >> (r * T::CH) & (T::CH == 64 ? ~0ull : (1ull << (T::CH & 63)) - 1)) rows |= 1u << (i * T::RPI + r);
+                if (lanes >> (r * T::CH) & ((1ull << T::CH) - 1)) rows |= 1u << (i * T::RPI + r);
         }
     }
     return rows;
@@ -179,24 +171,30 @@ __device__ __forceinline__ void rows_made_finite(lds_ptr p, int lane) {
     }
 }
 
-// One wave's rows and their running results.
-template <int D, int QB, bool FP8, bool SPLITP>
+// One wave's 32 rows and their running results; a lane has one row (lane % 32).
+template <int D, bool FP8, bool SPLITP>
 struct Rows {
     using T = Tile<D, FP8>;
     static constexpr int NS = D / 16;                   // steps of 16 columns in K Q^T
     static constexpr int ND = D / 32;                   // blocks of 32 output columns
     static constexpr int TERMS = SPLITP ? 3 : 1;        // BF16 terms of P
 
-    v8bf q[QB][NS];
-    v16f o[QB][ND];
-    float m[QB], l[QB];                                 // reference (unscaled logit units), this lane's half of the sum
-    float c;                                            // scale log2 e (> 0)
+    v8bf q[NS];
+    v16f o[ND];
+    float m, l;                                         // reference (unscaled logit units), this lane's half of the sum
+    float c;                                            // scale log2 e, made positive
+    uint32_t q_and, q_xor;                              // what that makes of the queries' bits
     int ka, va;                                         // byte offsets of this lane's first read in a K and a V tile
     int lane;
 
     __device__ __forceinline__ void init(int lane_, float c_) {
         lane = lane_;
-        c = c_;
+        // A negative scale becomes the queries' sign, and with a scale of zero
+        // they are zeros, so that larger logits are larger ones of c <q, k>
+        // and -infinity (a hidden key) stays what it is.
+        c = c_ == 0.f ? 1.0f : __builtin_fabsf(c_);
+        q_and = c_ == 0.f ? 0u : ~0u;
+        q_xor = c_ < 0.f ? 0x80008000u : 0u;
         const int n = lane & 31, h = lane >> 5, g = lane >> 4, r = lane & 15;
         ka = n * T::ROW + ((h ^ T::sw(n)) << 4);
         if constexpr (FP8) {
@@ -206,40 +204,35 @@ struct Rows {
             const int key = 4 * h + (r >> 2);
             va = key * T::ROW + (((2 * (g & 1) + ((r & 3) >> 1)) ^ T::sw(key)) << 4) + (r & 1) * 8;
         }
+        m = -INFINITY;
+        l = 0.f;
 #pragma unroll
-        for (int b = 0; b < QB; ++b) {
-            m[b] = -INFINITY;
-            l[b] = 0.f;
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[b][d][i] = 0.f;
-        }
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
     }
 
-    // The query row of this lane in block b (NULL: no such row, zeros).  The
-    // columns of step s are those that K's reads give it.
-    __device__ __forceinline__ void load_q(int b, const uint16_t* row) {
+    // The query row of this lane (NULL: no such row, zeros).  The columns of
+    // step s are those that K's reads give it.
+    __device__ __forceinline__ void load_q(const uint16_t* row) {
         const int h = lane >> 5;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const int col = FP8 ? 32 * (s >> 1) + 16 * h + 8 * (s & 1) : 16 * s + 8 * h;
-            q[b][s] = as_frag(row ? *reinterpret_cast<const v4u*>(row + col) : v4u{0u, 0u, 0u, 0u});
+            q[s] = as_frag(row ? (*reinterpret_cast<const v4u*>(row + col) & q_and) ^ q_xor : v4u{0u, 0u, 0u, 0u});
         }
     }
     // Waits for the queries here, once: a wait at their first use would stand
     // in the loop over the keys and hold up its loads in every turn.
     __device__ __forceinline__ void queries_ready() {
 #pragma unroll
-        for (int b = 0; b < QB; ++b)
-#pragma unroll
-            for (int s = 0; s < NS; ++s) asm volatile("" : "+v"(q[b][s]));
+        for (int s = 0; s < NS; ++s) asm volatile("" : "+v"(q[s]));
     }
 
     // The reads' places: a chunk number is XORed into the row's permuted place
     // (low four chunk bits), further chunks and rows are added.  LEAN: formed
     // anew each time (one instruction a read) instead of being kept in registers.
-    static constexpr bool LEAN = QB * (NS * 4 + ND * 16) >= 192;
+    static constexpr bool LEAN = D == 256;
     __device__ __forceinline__ int fresh(int at) const {
         if (LEAN) asm volatile("" : "+v"(at));
         return at;
@@ -274,11 +267,9 @@ struct Rows {
     __device__ __forceinline__ static void in_order() { __builtin_amdgcn_sched_barrier(0x406); }
 
     // S^T of the 32 keys at k.
-    __device__ __forceinline__ void logits(lds_cptr k, v16f (&s)[QB]) const {
+    __device__ __forceinline__ void logits(lds_cptr k, v16f& s) const {
 #pragma unroll
-        for (int b = 0; b < QB; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
         const int at = fresh(ka);
         constexpr int READS = FP8 ? ND : NS, AHEAD = FP8 ? 3 : 4;          // 16 bytes a read: 16 codes or 8 values
         v4u x[AHEAD];
@@ -289,14 +280,11 @@ struct Rows {
 #pragma unroll
         for (int i = 0; i < READS; ++i) {
             const v4u w = x[i % AHEAD];
-#pragma unroll
-            for (int b = 0; b < QB; ++b) {
-                if constexpr (FP8) {
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_frag(w[0], w[1]), q[b][2 * i], s[b], 0, 0, 0);
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_frag(w[2], w[3]), q[b][2 * i + 1], s[b], 0, 0, 0);
-                } else {
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(w), q[b][i], s[b], 0, 0, 0);
-                }
+            if constexpr (FP8) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_frag(w[0], w[1]), q[2 * i], s, 0, 0, 0);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3x8_to_frag(w[2], w[3]), q[2 * i + 1], s, 0, 0, 0);
+            } else {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(w), q[i], s, 0, 0, 0);
             }
             if (i + AHEAD < READS) x[i % AHEAD] = read(i + AHEAD);
             in_order();
@@ -311,43 +299,33 @@ struct Rows {
         for (int i = 0; i < 16; ++i) s[i] = (w >> (8 * (i >> 2) + (i & 3))) & 1u ? s[i] : -INFINITY;
     }
 
-    __device__ __forceinline__ float powers(int b, v16f& s) const {
-        const float mc = m[b] == -INFINITY ? 0.f : m[b] * c;
+    // P^T of the 32 keys at k, with m, l and o brought along.
+    template <bool HIDE>
+    __device__ __forceinline__ void weights(lds_cptr k, uint64_t seen, v16f& s) {
+        logits(k, s);
+        if (HIDE) hide(s, seen);
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = max2(top, s[i]);
+        top = halves_max(top);
+        if (__ballot((top - m) * c > RESCALE_LOG2) != 0) {
+            const float to = max2(m, top);
+            const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - to) * c);
+            m = to;
+            l *= a;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= a;
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
             sum += s[i];
         }
-        return sum;
-    }
-
-    // P^T of the 32 keys at k, with m, l and o brought along.
-    template <bool HIDE>
-    __device__ __forceinline__ void weights(lds_cptr k, const uint64_t (&seen)[QB], v16f (&s)[QB]) {
-        logits(k, s);
-        float sum[QB];
-#pragma unroll
-        for (int b = 0; b < QB; ++b) {
-            if (HIDE) hide(s[b], seen[b]);
-            float top = s[b][0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) top = max2(top, s[b][i]);
-            top = halves_max(top);
-            if (__ballot((top - m[b]) * c > RESCALE_LOG2) != 0) {
-                const float to = max2(m[b], top);
-                const float a = m[b] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[b] - to) * c);
-                m[b] = to;
-                l[b] *= a;
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[b][d][i] *= a;
-            }
-            sum[b] = powers(b, s[b]);
-        }
-#pragma unroll
-        for (int b = 0; b < QB; ++b) l[b] += sum[b];
+        l += sum;
     }
 
     // The operand of 16 keys: registers i0 .. i0 + 7 of S^T, as BF16.  SPLITP:
@@ -375,26 +353,20 @@ struct Rows {
     }
 
     // O^T += V^T P^T over the 32 keys at v.
-    __device__ __forceinline__ void values(lds_cptr v, const v16f (&p)[QB]) {
+    __device__ __forceinline__ void values(lds_cptr v, const v16f& p) {
         const int at = fresh(va);
         constexpr int AHEAD = FP8 ? 4 : 2;
         v4u x[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) x[i] = read_v(v, at, i / ND, i % ND);
         in_order();
-        v8bf pf[QB][TERMS];
+        v8bf pf[TERMS];
 #pragma unroll
         for (int i = 0; i < 2 * ND; ++i) {
-            if (i % ND == 0) {
-#pragma unroll
-                for (int b = 0; b < QB; ++b) p_frag(p[b], 8 * (i / ND), pf[b]);
-            }
+            if (i % ND == 0) p_frag(p, 8 * (i / ND), pf);
             const v8bf f = v_frag(x[i % AHEAD]);
 #pragma unroll
-            for (int e = 0; e < TERMS; ++e)
-#pragma unroll
-                for (int b = 0; b < QB; ++b)
-                    o[b][i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[b][e], o[b][i % ND], 0, 0, 0);
+            for (int e = 0; e < TERMS; ++e) o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[e], o[i % ND], 0, 0, 0);
             if (i + AHEAD < 2 * ND) x[i % AHEAD] = read_v(v, at, (i + AHEAD) / ND, (i + AHEAD) % ND);
             in_order();
         }
@@ -405,9 +377,10 @@ struct Rows {
     // rows that see them (a weight is positive, so the sum is infinite or NaN
     // by them whatever it is), and then count as zeros in the products.
     // bad: the keys of the 32 at v that hold such values; seen: as in hide().
-    __device__ __forceinline__ void add_not_finite(lds_cptr v, uint64_t bad, const uint64_t (&seen)[QB]) {
+    __device__ __forceinline__ void add_not_finite(lds_cptr v, uint32_t bad, uint64_t seen) {
         while (bad) {
-            const int key = __builtin_ctzll(bad);
+            const int key = __builtin_ctz(bad);
+            const bool sees = (seen >> key) & 1u;
             bad &= bad - 1;
 #pragma unroll
             for (int d = 0; d < ND; ++d)
@@ -418,11 +391,7 @@ struct Rows {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[j] = __builtin_isfinite(x[j]) ? 0.f : x[j];
 #pragma unroll
-                    for (int b = 0; b < QB; ++b) {
-                        const bool sees = (seen[b] >> key) & 1u;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[b][d][4 * e + j] += sees ? x[j] : 0.f;
-                    }
+                    for (int j = 0; j < 4; ++j) o[d][4 * e + j] += sees ? x[j] : 0.f;
                 }
         }
     }
@@ -439,7 +408,7 @@ struct Rows {
         }
     }
 
-    // This lane's output column block: o[b][d][4 e + j] is column 32 d + 8 e + 4 h + j.
+    // o[d][4 e + j] is this lane's output column 32 d + 8 e + 4 h + j.
     __device__ __forceinline__ int column(int d, int e) const { return 32 * d + 8 * e + 4 * (lane >> 5); }
 };
 

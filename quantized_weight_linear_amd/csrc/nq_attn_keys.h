@@ -1,6 +1,6 @@
-// The workgroup form with up to 32 query rows: NW waves take different keys of
-// the same rows, every NW-th tile of 32, each through LDS of its own without
-// barriers, and join at the end.
+// The workgroup form with up to 32 query rows: four waves take different keys
+// of the same rows, every fourth tile of 32, each through LDS of its own
+// without barriers, and join at the end.
 #pragma once
 
 #include "nq_attn_rows.h"
@@ -10,26 +10,28 @@ namespace attn {
 
 // A ring of RING tiles a wave; K and V of a tile are waited for separately,
 // and each slot is loaded again as soon as it has been read.
-template <int D, bool FP8, int NW>
+constexpr int KEY_WAVES = 4;
+
+template <int D, bool FP8>
 struct KeysLds {
     static constexpr int TILE = 32 * Tile<D, FP8>::ROW;
     static constexpr int RING = TILE >= 8192 ? 1 : TILE >= 4096 ? 2 : 4;
     static constexpr int WAVE = 2 * RING * TILE;                    // 16 KiB (BF16 rows of 256: 32 KiB)
     static constexpr int PITCH = D + 4;                             // floats a row of the waves' results at the end
-    static constexpr int JOIN = NW * 32 * PITCH * 4;
-    static constexpr int BYTES = NW * WAVE > JOIN ? NW * WAVE : JOIN;
+    static constexpr int JOIN = KEY_WAVES * 32 * PITCH * 4;
+    static constexpr int BYTES = KEY_WAVES * WAVE > JOIN ? KEY_WAVES * WAVE : JOIN;
 };
 
 // Source, Sees and Queries as for attend_rows (keys from key1 on are outside
 // the source's descriptors).  emit(row, column, x, mc, l): four neighbouring
 // columns of a row's sum of p v, its reference in log2 units and its sum of p;
 // once for each of the first `rows` rows and every fourth column.
-template <int NW, int D, bool FP8, bool SPLITP, class Source, class Sees, class Queries, class Emit>
-__device__ __forceinline__ void attend_keys(Rows<D, 1, FP8, SPLITP>& R, unsigned char* smem, int key0, int key1, int rows,
+template <int D, bool FP8, bool SPLITP, class Source, class Sees, class Queries, class Emit>
+__device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned char* smem, int key0, int key1, int rows,
                                             const Source& src, const Sees& sees, const Queries& queries, const Emit& emit,
                                             int wave, int lane) {
-    using L = KeysLds<D, FP8, NW>;
-    constexpr int LOADS = 2 * Tile<D, FP8>::LOADS16, LATER = (2 * L::RING - 1) * LOADS, STEP = NW * 32;
+    using L = KeysLds<D, FP8>;
+    constexpr int LOADS = 2 * Tile<D, FP8>::LOADS16, LATER = (2 * L::RING - 1) * LOADS, STEP = KEY_WAVES * 32;
     const Stager<D, FP8> st_k(lane, src.k_stride), st_v(lane, src.v_stride);
     const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
     auto load_k = [&](int key, int slot) {
@@ -51,9 +53,9 @@ __device__ __forceinline__ void attend_keys(Rows<D, 1, FP8, SPLITP>& R, unsigned
     auto step = [&](int key, int slot, auto partly) {
         constexpr bool PARTLY = decltype(partly)::value;
         const lds_ptr k = mine + slot * 2 * L::TILE, v = k + L::TILE;
-        v16f x[1];
-        uint64_t seen[1];
-        if (PARTLY) seen[0] = sees.seen(0, key);
+        v16f x;
+        uint64_t seen = 0;
+        if (PARTLY) seen = sees.seen(key);
         wait_vm<LATER>();
         R.template weights<PARTLY>(k, seen, x);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
@@ -83,28 +85,28 @@ __device__ __forceinline__ void attend_keys(Rows<D, 1, FP8, SPLITP>& R, unsigned
     __syncthreads();
     // The waves' results go to LDS, and the workgroup's threads finish the rows.
     float* join = reinterpret_cast<float*>(smem);
-    const float l = halves_sum(R.l[0]);
+    const float l = halves_sum(R.l);
     float* at = join + (wave * 32 + (lane & 31)) * L::PITCH;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             *reinterpret_cast<v4f*>(at + R.column(d, e)) =
-                v4f{R.o[0][d][4 * e], R.o[0][d][4 * e + 1], R.o[0][d][4 * e + 2], R.o[0][d][4 * e + 3]};
+                v4f{R.o[d][4 * e], R.o[d][4 * e + 1], R.o[d][4 * e + 2], R.o[d][4 * e + 3]};
     if (lane < 32) {
-        at[D] = R.m[0] == -INFINITY ? -INFINITY : R.m[0] * R.c;
+        at[D] = R.m == -INFINITY ? -INFINITY : R.m * R.c;
         at[D + 1] = l;
     }
     __syncthreads();
     constexpr int LANES = D / 4;                        // threads a row
-    for (int i = threadIdx.x / LANES; i < rows; i += NW * 64 / LANES) {
+    for (int i = threadIdx.x / LANES; i < rows; i += KEY_WAVES * 64 / LANES) {
         const int col = threadIdx.x % LANES * 4;
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) top = max2(top, join[(w * 32 + i) * L::PITCH + D]);
+        for (int w = 0; w < KEY_WAVES; ++w) top = max2(top, join[(w * 32 + i) * L::PITCH + D]);
         v4f x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
+        for (int w = 0; w < KEY_WAVES; ++w) {
             const float* p = join + (w * 32 + i) * L::PITCH;
             const float lw = p[D + 1];
             // a wave that saw nothing has neither sum nor outputs

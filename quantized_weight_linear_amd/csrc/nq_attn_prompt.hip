@@ -45,14 +45,13 @@ struct PackedRows {                 // K or V rows of one sequence and KV head
     }
 };
 
-template <int QB>
 struct CausalSees {
     int clean;                      // every row of the workgroup sees the keys below it
     int none;                       // no row of the wave sees keys from it on
-    int limit[QB];                  // this lane's rows see the keys below it
+    int limit;                      // this lane's row sees the keys below it
     __device__ __forceinline__ int all_before() const { return clean; }
     __device__ __forceinline__ int none_from() const { return none; }
-    __device__ __forceinline__ uint64_t seen(int b, int key) const { return bits_below(limit[b] - key); }
+    __device__ __forceinline__ uint64_t seen(int key) const { return bits_below(limit - key); }
 };
 
 // The tile of BM query rows that workgroup `index` of a head has: the
@@ -104,90 +103,71 @@ __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     const QueryTile t(a, blockIdx.x / a.hq, 32);
     if (!t.real) return;
     const int ahead = t.nk - t.nq, row = t.first + (lane & 31);
-    Rows<D, 1, false, !BF16OUT> R;
+    Rows<D, false, !BF16OUT> R;
     R.init(lane, a.c);
-    CausalSees<1> sees;
+    CausalSees sees;
     sees.clean = t.first + 1 + ahead;
     sees.none = t.last + ahead;
-    sees.limit[0] = row + 1 + ahead;
+    sees.limit = row + 1 + ahead;
     const int keys = t.last + ahead > 0 ? t.last + ahead : 0;
     const PackedRows src = packed_rows<D>(a, t, head / (a.hq / a.hkv), keys);
-    auto queries = [&] { R.load_q(0, row < t.nq ? a.q + (t.q0 + row) * a.qs + head * D : nullptr); };
+    auto queries = [&] { R.load_q(row < t.nq ? a.q + (t.q0 + row) * a.qs + head * D : nullptr); };
     auto emit = [&](int i, int col, const v4f& x, float mc, float l) {
         const int64_t out = (t.q0 + t.first + i) * a.hq + head;
         const float f = inverse_sum(l);
         store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
         if (col == 0 && a.lse) a.lse[out] = log_sum_exp(mc, l);
     };
-    attend_keys<4>(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
+    attend_keys(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
 }
 
-// Many tiles: NW waves with 32 QB rows each.
-template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
-__global__ __launch_bounds__(NW * 64, PER_SIMD) void attn_prompt_kernel(PromptArgs a) {
-    constexpr int BM = NW * QB * 32;
+// Many tiles: 128 rows a workgroup.
+template <int D, bool BF16OUT>
+__global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_prompt_rows_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.x % a.hq;
-    const QueryTile t(a, blockIdx.x / a.hq, BM);
+    const QueryTile t(a, blockIdx.x / a.hq, 128);
     if (!t.real) return;
-    const int64_t q0 = t.q0;
-    const int nq = t.nq, ahead = t.nk - t.nq, first = t.first, last = t.last;
-
-    Rows<D, QB, false, !BF16OUT> R;
+    const int ahead = t.nk - t.nq, row = t.first + wave * 32 + (lane & 31);
+    Rows<D, false, !BF16OUT> R;
     R.init(lane, a.c);
-    CausalSees<QB> sees;
-    sees.clean = first + 1 + ahead;
-    sees.none = first + (wave + 1) * QB * 32 + ahead;
-    int row[QB];
-#pragma unroll
-    for (int i = 0; i < QB; ++i) {
-        row[i] = first + (wave * QB + i) * 32 + (lane & 31);
-        sees.limit[i] = row[i] + 1 + ahead;
-    }
+    CausalSees sees;
+    sees.clean = t.first + 1 + ahead;
+    sees.none = t.first + (wave + 1) * 32 + ahead;
+    sees.limit = row + 1 + ahead;
     const PackedRows src = packed_rows<D>(a, t, head / (a.hq / a.hkv), t.nk);
-    const int end = last + ahead;                       // keys that the tile's last row sees
-    auto queries = [&] {
+    auto queries = [&] { R.load_q(row < t.nq ? a.q + (t.q0 + row) * a.qs + head * D : nullptr); };
+    attend_rows(R, (lds_ptr)smem, 0, t.last + ahead, src, sees, queries, wave, lane);
+    const float l = halves_sum(R.l), inv = inverse_sum(l);
+    if (row >= t.nq) return;
+    const int64_t out = (t.q0 + row) * a.hq + head;
 #pragma unroll
-        for (int i = 0; i < QB; ++i) R.load_q(i, row[i] < nq ? a.q + (q0 + row[i]) * a.qs + head * D : nullptr);
-    };
-    attend_rows<RING, NW>(R, (lds_ptr)smem, 0, end, src, sees, queries, wave, lane);
+    for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-    for (int i = 0; i < QB; ++i) {
-        const float l = halves_sum(R.l[i]), inv = inverse_sum(l);
-        if (row[i] < nq) {
-            const int64_t at = ((q0 + row[i]) * a.hq + head) * D;
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    store4<BF16OUT>(a.o, at + R.column(d, e), R.o[i][d][4 * e] * inv, R.o[i][d][4 * e + 1] * inv,
-                                    R.o[i][d][4 * e + 2] * inv, R.o[i][d][4 * e + 3] * inv);
-            if (a.lse && lane < 32) a.lse[(q0 + row[i]) * a.hq + head] = log_sum_exp(l == 0.f ? 0.f : R.m[i] * a.c, l);
-        }
-    }
+        for (int e = 0; e < 4; ++e)
+            store4<BF16OUT>(a.o, out * D + R.column(d, e), R.o[d][4 * e] * inv, R.o[d][4 * e + 1] * inv,
+                            R.o[d][4 * e + 2] * inv, R.o[d][4 * e + 3] * inv);
+    if (a.lse && lane < 32) a.lse[out] = log_sum_exp(l == 0.f ? 0.f : R.m * R.c, l);
 }
 
 // Tiles of bm rows at most: every sequence may end in a part of one.
 int64_t tiles_of(const PromptArgs& a, int bm) { return a.tq / bm + (a.seqs < a.tq ? a.seqs : a.tq); }
 
-template <int D, int QB, int NW, int RING, int PER_SIMD, bool BF16OUT>
-hipError_t go(const PromptArgs& a, hipStream_t stream) {
-    constexpr int BM = NW * QB * 32, LDS = RowsLds<D, false, NW, RING>::BYTES;
-    auto kernel = attn_prompt_kernel<D, QB, NW, RING, PER_SIMD, BF16OUT>;
-    static LdsLimit limit;
-    if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
-    kernel<<<(unsigned)(tiles_of(a, BM) * a.hq), NW * 64, LDS, stream>>>(a);
-    return hipGetLastError();
-}
-
 template <int D, bool BF16OUT>
-hipError_t go_keys(const PromptArgs& a, hipStream_t stream) {
-    constexpr int LDS = KeysLds<D, false, 4>::BYTES;
-    auto kernel = attn_prompt_keys_kernel<D, BF16OUT>;
-    static LdsLimit limit;
-    if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
-    kernel<<<(unsigned)(tiles_of(a, 32) * a.hq), 256, LDS, stream>>>(a);
+hipError_t go(const PromptArgs& a, bool few, hipStream_t stream) {
+    constexpr int KEYS_LDS = KeysLds<D, false>::BYTES, ROWS_LDS = RowsLds<D, false>::BYTES;
+    static LdsLimit keys_limit, rows_limit;
+    hipError_t e;
+    if (few) {
+        auto kernel = attn_prompt_keys_kernel<D, BF16OUT>;
+        if ((e = keys_limit.raise((const void*)kernel, KEYS_LDS)) != hipSuccess) return e;
+        kernel<<<(unsigned)(tiles_of(a, 32) * a.hq), 256, KEYS_LDS, stream>>>(a);
+    } else {
+        auto kernel = attn_prompt_rows_kernel<D, BF16OUT>;
+        if ((e = rows_limit.raise((const void*)kernel, ROWS_LDS)) != hipSuccess) return e;
+        kernel<<<(unsigned)(tiles_of(a, 128) * a.hq), 256, ROWS_LDS, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -205,17 +185,16 @@ hipError_t launch_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_
     // 256 take 25 us so and 29 us the other way, of 32 heads of 128 11 and 17,
     // 1024 of 24 of 256 60 and 50.  (With two key tiles there is nothing to share out: 33
     // tokens of 24 heads of 256 11 and 8.5 us.)
-    if (tiles_of(a, 128) * hq * (d == 256 ? 2 : 1) <= device_cu_count() && tk > 64 * seqs) {
-        switch (d) {
-            case 64: return bf16_out ? go_keys<64, true>(a, stream) : go_keys<64, false>(a, stream);
-            case 128: return bf16_out ? go_keys<128, true>(a, stream) : go_keys<128, false>(a, stream);
-            default: return bf16_out ? go_keys<256, true>(a, stream) : go_keys<256, false>(a, stream);
-        }
-    }
+    // Few tiles of 128 rows: 32 rows a workgroup, so that more CUs have one and
+    // each row's keys are walked four at a time; 512 tokens of 24 heads of 256
+    // take 25 us so and 29 the other way, of 32 heads of 128 11 and 17, 1024 of
+    // 24 of 256 60 and 50.  (With two key tiles there is nothing to share out:
+    // 33 tokens of 24 heads of 256 11 and 8.5 us.)
+    const bool few = tiles_of(a, 128) * hq * (d == 256 ? 2 : 1) <= device_cu_count() && tk > 64 * seqs;
     switch (d) {
-        case 64: return bf16_out ? go<64, 1, 4, 2, 4, true>(a, stream) : go<64, 1, 4, 2, 4, false>(a, stream);
-        case 128: return bf16_out ? go<128, 1, 4, 2, 3, true>(a, stream) : go<128, 1, 4, 2, 3, false>(a, stream);
-        default: return bf16_out ? go<256, 1, 4, 2, 2, true>(a, stream) : go<256, 1, 4, 2, 2, false>(a, stream);
+        case 64: return bf16_out ? go<64, true>(a, few, stream) : go<64, false>(a, few, stream);
+        case 128: return bf16_out ? go<128, true>(a, few, stream) : go<128, false>(a, few, stream);
+        default: return bf16_out ? go<256, true>(a, few, stream) : go<256, false>(a, few, stream);
     }
 }
 

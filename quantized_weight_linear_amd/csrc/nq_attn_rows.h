@@ -1,8 +1,11 @@
-// The workgroup form with many query rows: NW waves with 32 QB rows each walk
+// The workgroup form with many query rows: four waves with 32 rows each walk
 // the keys together, 32 at a time.  Every 32-key tile of K and V is loaded
-// into LDS once per workgroup, into rings of RING tiles: the loads of tile
-// i + RING - 1 are issued when tile i is complete.  The matrix work of one
-// wave runs beside the softmax of the others on its SIMD.
+// into LDS once per workgroup, two tiles deep: the loads of the next one are
+// issued when a tile is complete.  Two to four workgroups run on a CU (by the
+// registers), and the matrix work of one wave runs beside the softmax of the
+// others on its SIMD.  (16384 causal tokens of 24 heads of 256: eight waves a
+// workgroup 3 % slower, rings of three 2 %; logits of the next tile beside the
+// softmax of this one within a wave, with fewer waves, 30 %.)
 #pragma once
 
 #include <type_traits>
@@ -14,11 +17,11 @@ namespace attn {
 
 constexpr int KEYS = 32;        // keys a step
 
-template <int D, bool FP8, int NW, int RING>
+template <int D, bool FP8>
 struct RowsLds {
     static constexpr int TILE = KEYS * Tile<D, FP8>::ROW;
-    static constexpr int FLAGS = 2 * RING * TILE;        // [2] steps x NW words: the staged values that are not finite
-    static constexpr int BYTES = FLAGS + 2 * NW * 4;
+    static constexpr int FLAGS = 4 * TILE;               // [2] steps x 4 waves: the staged rows that are not finite
+    static constexpr int BYTES = FLAGS + 2 * 4 * 4;
 };
 
 // Bits below n (0 .. 64 and beyond either end).
@@ -36,82 +39,66 @@ __device__ __forceinline__ void lds_barrier() {
 // 16-aligned key on (keys past the last one are outside it), k_stride /
 // v_stride the bytes between rows.
 // Sees: all_before() = every row of the workgroup sees all keys below it;
-// none_from() = no row of this wave sees keys from it on; seen(b, key) = the
-// 64 keys from `key` on as bits, for this lane's row of block b.
+// none_from() = no row of this wave sees keys from it on; seen(key) = the
+// 64 keys from `key` on as bits, for this lane's row.
 // Queries: loads the rows' queries; called once the first keys are on their way.
-template <int RING, int NW, int D, int QB, bool FP8, bool SPLITP, class Source, class Sees, class Queries>
-__device__ __forceinline__ void attend_rows(Rows<D, QB, FP8, SPLITP>& R, lds_ptr lds, int key0, int key1,
-                                            const Source& src, const Sees& sees, const Queries& queries,
-                                            int wave, int lane) {
-    using L = RowsLds<D, FP8, NW, RING>;
-    using T = Tile<D, FP8>;
-    constexpr int ROW = T::ROW, LOADS = 4 * T::LOADS16 / NW;          // a wave's load instructions a step
-    static_assert((NW == 4 || NW == 8) && LOADS * NW == 4 * T::LOADS16, "a step stages four groups of 16 rows");
-    const int group = wave & 3, part = (group & 1) * 16;             // groups 0, 1: K; 2, 3: V
-    const Stager<D, FP8> st(lane, group < 2 ? src.k_stride : src.v_stride);
-    const lds_ptr k_ring = lds, v_ring = lds + RING * L::TILE;
-    auto load = [&](v4i r, lds_ptr dst) {
-        if (NW == 4 || wave < 4) st.template pieces<0, LOADS>(r, dst);
-        else st.template pieces<NW == 4 ? 0 : LOADS, LOADS>(r, dst);
-    };
+template <int D, bool FP8, bool SPLITP, class Source, class Sees, class Queries>
+__device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds, int key0, int key1, const Source& src,
+                                            const Sees& sees, const Queries& queries, int wave, int lane) {
+    using L = RowsLds<D, FP8>;
+    constexpr int ROW = Tile<D, FP8>::ROW, LOADS = Tile<D, FP8>::LOADS16;
+    // waves 0, 1 stage K's rows, 2, 3 V's, 16 each
+    const bool is_k = wave < 2;
+    const int part = (wave & 1) * 16;
+    const Stager<D, FP8> st(lane, is_k ? src.k_stride : src.v_stride);
+    const lds_ptr k_ring = lds, v_ring = lds + 2 * L::TILE;
     auto stage = [&](int i, int slot) {
         const int key = key0 + i * KEYS + part;
-        if (group < 2) load(src.k_rows(key), k_ring + slot * L::TILE + part * ROW);
-        else load(src.v_rows(key), v_ring + slot * L::TILE + part * ROW);
+        if (is_k) st.rows16(src.k_rows(key), k_ring + slot * L::TILE + part * ROW);
+        else st.rows16(src.v_rows(key), v_ring + slot * L::TILE + part * ROW);
     };
     if (key0 >= key1) return;
     const int n = (key1 - key0 + KEYS - 1) / KEYS;
-#pragma unroll
-    for (int i = 0; i < RING - 1; ++i) stage(i, i);
+    stage(0, 0);
     queries();
     R.queries_ready();
     auto step = [&](int i, int slot, auto partly) {
         constexpr bool PARTLY = decltype(partly)::value;
         const int key = key0 + i * KEYS;
         const lds_ptr k = k_ring + slot * L::TILE, v = v_ring + slot * L::TILE;
-        auto* flags = (__attribute__((address_space(3))) uint32_t*)(lds + L::FLAGS) + (i & 1) * NW;
-        wait_vm<(RING - 2) * LOADS>();
+        auto* flags = (__attribute__((address_space(3))) uint32_t*)(lds + L::FLAGS) + (i & 1) * 4;
+        wait_vm<0>();
         if (PARTLY) {
-            uint32_t rows = 0;
-            if (group >= 2) {
-                const lds_cptr p = v + part * ROW + (wave >> 2) * LOADS * 1024;
-                rows = rows_not_finite<D, FP8, LOADS>(p, lane) << (part + (wave >> 2) * LOADS * T::RPI);
-            }
+            const uint32_t rows = is_k ? 0u : rows_not_finite<D, FP8, LOADS>(v + part * ROW, lane) << part;
             if (lane == 0) flags[wave] = rows;
         }
         lds_barrier();
-        stage(i + RING - 1, slot == 0 ? RING - 1 : slot - 1);
+        stage(i + 1, slot ^ 1);
         uint32_t bad = 0;
         bool some = true;
-        uint64_t seen[QB];
+        uint64_t seen = 0;
         if (PARTLY) {
             some = key < sees.none_from();
-#pragma unroll
-            for (int w = 0; w < NW; ++w) bad |= flags[w];
-            bad = __builtin_amdgcn_readfirstlane(bad);
-#pragma unroll
-            for (int b = 0; b < QB; ++b) seen[b] = sees.seen(b, key);
+            bad = __builtin_amdgcn_readfirstlane(flags[2] | flags[3]);
+            seen = sees.seen(key);
         }
-        v16f s[QB];
+        v16f s;
         if (some) R.template weights<PARTLY>(k, seen, s);
         if (PARTLY && bad) {
             if (some) R.add_not_finite(v, bad, seen);
             lds_barrier();
-            if (group >= 2) rows_made_finite<D, FP8, LOADS>(v + part * ROW + (wave >> 2) * LOADS * 1024, lane);
+            if (!is_k) rows_made_finite<D, FP8, LOADS>(v + part * ROW, lane);
             lds_barrier();
         }
         if (some) R.values(v, s);
     };
     const int clean = sees.all_before() - key0 < 0 ? 0 : (sees.all_before() - key0) / KEYS;
-    int i = 0, slot = 0;
-    for (const int whole = (clean < n ? clean : n) - RING; i <= whole; i += RING) {
-#pragma unroll
-        for (int j = 0; j < RING; ++j) step(i + j, j, std::false_type{});
+    int i = 0;
+    for (const int whole = (clean < n ? clean : n) - 2; i <= whole; i += 2) {       // by two: the slots' places are constants
+        step(i, 0, std::false_type{});
+        step(i + 1, 1, std::false_type{});
     }
-    for (; i < n; ++i) {
-        step(i, slot, std::true_type{});
-        slot = slot == RING - 1 ? 0 : slot + 1;
-    }
+    for (; i < n; ++i) step(i, i & 1, std::true_type{});
     wait_vm<0>();                                        // nothing may land in LDS after the workgroup has gone
 }
 

@@ -160,16 +160,15 @@ struct PagedRows {
     __device__ __forceinline__ v4i v_rows(int key) const { return rows(v, key); }
 };
 
-template <int QB>
 struct TreeSees {
     int len;                        // committed keys: seen by every row
     int none = 1 << 30;             // 0: the wave has no rows
-    uint64_t mask[QB];              // drafted keys that this lane's rows see
+    uint64_t mask;                  // drafted keys that this lane's row sees
     __device__ __forceinline__ int all_before() const { return len; }
     __device__ __forceinline__ int none_from() const { return none; }
-    __device__ __forceinline__ uint64_t seen(int b, int key) const {
+    __device__ __forceinline__ uint64_t seen(int key) const {
         const int at = len - key;   // where the drafted keys start among these 64
-        const uint64_t drafted = at >= 64 ? 0ull : at >= 0 ? mask[b] << at : at > -64 ? mask[b] >> -at : 0ull;
+        const uint64_t drafted = at >= 64 ? 0ull : at >= 0 ? mask << at : at > -64 ? mask >> -at : 0ull;
         return bits_below(at) | drafted;
     }
 };
@@ -186,47 +185,19 @@ __device__ __forceinline__ int2* part_ranges(const TreeArgs& a, int d) {
 }
 
 // Rows [0, n group) of (b, kvh): token row / group, query head kvh group + row % group.
-template <int D, int QB, bool FP8, bool BF16OUT>
-struct TreeRows {
-    static constexpr bool SPLITP = !BF16OUT;
-    __device__ static void masks(TreeSees<QB>& sees, const TreeArgs& a, const Seq& s, const int (&row)[QB]) {
-        sees.len = s.len;
-#pragma unroll
-        for (int i = 0; i < QB; ++i)
-            sees.mask[i] = row[i] < s.n * a.group ? a.masks[s.t0 + row[i] / a.group] & bits_below(s.total - s.len) : ~0ull;
-    }
-    __device__ static void load(Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int kvh, const int (&row)[QB]) {
-#pragma unroll
-        for (int i = 0; i < QB; ++i)
-            R.load_q(i, row[i] < s.n * a.group ? a.q + (s.t0 + row[i] / a.group) * a.qs +
-                                                     (int64_t)(kvh * a.group + row[i] % a.group) * D
-                                               : nullptr);
-    }
-    // Results of one row block: outputs, or a part of them.
-    __device__ static void store(const Rows<D, QB, FP8, SPLITP>& R, const TreeArgs& a, const Seq& s, int range, int kvh, bool only,
-                                 int i, int row) {
-        const float l = halves_sum(R.l[i]);
-        const float mc = R.m[i] == -INFINITY ? 0.f : R.m[i] * R.c;
-        if (row >= s.n * a.group) return;
-        const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
-        const int64_t out = (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
-        const int64_t part = part_row(a, range, kvh, row);
-        const float f = only ? inverse_sum(l) * vs : 1.0f;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x0 = R.o[i][d][4 * e] * f, x1 = R.o[i][d][4 * e + 1] * f, x2 = R.o[i][d][4 * e + 2] * f,
-                            x3 = R.o[i][d][4 * e + 3] * f;
-                if (only) store4<BF16OUT>(a.o, out * D + R.column(d, e), x0, x1, x2, x3);
-                else store4<false>(a.parts, part * D + R.column(d, e), x0, x1, x2, x3);
-            }
-        if (R.lane < 32) {
-            if (!only) part_sums(a, D)[part] = make_float2(mc, l);
-            else if (a.lse) a.lse[out] = log_sum_exp(mc, l);
-        }
-    }
-};
+__device__ __forceinline__ TreeSees tree_sees(const TreeArgs& a, const Seq& s, int row) {
+    TreeSees sees;
+    sees.len = s.len;
+    sees.mask = row < s.n * a.group ? a.masks[s.t0 + row / a.group] & bits_below(s.total - s.len) : ~0ull;
+    return sees;
+}
+__device__ __forceinline__ const uint16_t* tree_query(const TreeArgs& a, const Seq& s, int kvh, int row, int d) {
+    if (row >= s.n * a.group) return nullptr;
+    return a.q + (s.t0 + row / a.group) * a.qs + (int64_t)(kvh * a.group + row % a.group) * d;
+}
+__device__ __forceinline__ int64_t tree_out(const TreeArgs& a, const Seq& s, int kvh, int row) {
+    return (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
+}
 
 template <int D, bool FP8>
 __device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const Seq& s, int b, int kvh) {
@@ -242,32 +213,49 @@ __device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const
     return src;
 }
 
-// More than 32 rows: NW waves of 32 rows.
-template <int D, int NW, bool FP8, bool BF16OUT>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tree_rows_kernel(TreeArgs a) {
+// More than 32 rows: 128 a workgroup.
+template <int D, bool FP8, bool BF16OUT>
+__global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tree_rows_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rt = blockIdx.x % a.row_tiles, kvh = blockIdx.x / a.row_tiles % a.hkv, range = blockIdx.x / a.row_tiles / a.hkv;
+    // the row tiles of one range are 8 apart: on the same XCD, whose L2 gives all but the first their keys
+    const int rt = blockIdx.x / 8 % a.row_tiles, unit = blockIdx.x / (8 * a.row_tiles) * 8 + blockIdx.x % 8;
+    const int kvh = unit % a.hkv, range = unit / a.hkv;
     const Range r(a, range);
     if (r.b < 0) return;
     const Seq s(a, r.b);
-    if (rt * NW * 32 >= s.n * a.group) return;
+    if (rt * 128 >= s.n * a.group) return;
     if (r.first == range && kvh == 0 && rt == 0 && threadIdx.x == 0 && a.want > 0) part_ranges(a, D)[r.b] = make_int2(r.first, r.parts);
-    Rows<D, 1, FP8, !BF16OUT> R;
+    Rows<D, FP8, !BF16OUT> R;
     R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
-    TreeSees<1> sees;
-    const int row[1] = {(rt * NW + wave) * 32 + (lane & 31)};
-    sees.none = (rt * NW + wave) * 32 < s.n * a.group ? 1 << 30 : 0;
-    TreeRows<D, 1, FP8, BF16OUT>::masks(sees, a, s, row);
+    const int row = (rt * 4 + wave) * 32 + (lane & 31);
+    TreeSees sees = tree_sees(a, s, row);
+    if ((rt * 4 + wave) * 32 >= s.n * a.group) sees.none = 0;
     const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
-    auto queries = [&] { TreeRows<D, 1, FP8, BF16OUT>::load(R, a, s, kvh, row); };
-    attend_rows<2, NW>(R, (lds_ptr)smem, r.key0, r.key1, src, sees, queries, wave, lane);
-    TreeRows<D, 1, FP8, BF16OUT>::store(R, a, s, range, kvh, r.parts == 1, 0, row[0]);
+    auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
+    attend_rows(R, (lds_ptr)smem, r.key0, r.key1, src, sees, queries, wave, lane);
+    const float l = halves_sum(R.l), mc = R.m == -INFINITY ? 0.f : R.m * R.c;
+    if (row >= s.n * a.group) return;
+    const bool only = r.parts == 1;
+    const int64_t out = tree_out(a, s, kvh, row), part = part_row(a, range, kvh, row);
+    const float f = only ? inverse_sum(l) * (FP8 ? a.v_scale[kvh] : 1.0f) : 1.0f;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x0 = R.o[d][4 * e] * f, x1 = R.o[d][4 * e + 1] * f, x2 = R.o[d][4 * e + 2] * f, x3 = R.o[d][4 * e + 3] * f;
+            if (only) store4<BF16OUT>(a.o, out * D + R.column(d, e), x0, x1, x2, x3);
+            else store4<false>(a.parts, part * D + R.column(d, e), x0, x1, x2, x3);
+        }
+    if (lane < 32) {
+        if (!only) part_sums(a, D)[part] = make_float2(mc, l);
+        else if (a.lse) a.lse[out] = log_sum_exp(mc, l);
+    }
 }
 
 // Up to 32 rows: the waves take different keys.
-template <int D, int NW, bool FP8, bool BF16OUT>
-__global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
+template <int D, bool FP8, bool BF16OUT>
+__global__ __launch_bounds__(256) void attn_tree_keys_kernel(TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.hkv, range = blockIdx.x / a.hkv;
@@ -275,18 +263,17 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
     if (r.b < 0) return;
     const Seq s(a, r.b);
     if (r.first == range && kvh == 0 && threadIdx.x == 0 && a.want > 0) part_ranges(a, D)[r.b] = make_int2(r.first, r.parts);
-    Rows<D, 1, FP8, !BF16OUT> R;
+    Rows<D, FP8, !BF16OUT> R;
     R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
-    TreeSees<1> sees;
-    const int row[1] = {lane & 31};
-    TreeRows<D, 1, FP8, BF16OUT>::masks(sees, a, s, row);
+    const int row = lane & 31;
+    const TreeSees sees = tree_sees(a, s, row);
     PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
     src.total = r.key1;                                 // keys past the range: no rows, zeros
-    auto queries = [&] { TreeRows<D, 1, FP8, BF16OUT>::load(R, a, s, kvh, row); };
+    auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
     const bool only = r.parts == 1;
     const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
     auto emit = [&](int i, int col, const v4f& x, float mc, float l) {
-        const int64_t out = (s.t0 + i / a.group) * a.hq + kvh * a.group + i % a.group;
+        const int64_t out = tree_out(a, s, kvh, i);
         if (only) {
             const float f = inverse_sum(l) * vs;
             store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
@@ -297,7 +284,7 @@ __global__ __launch_bounds__(NW * 64) void attn_tree_keys_kernel(TreeArgs a) {
             if (col == 0) part_sums(a, D)[part] = make_float2(mc, l);
         }
     };
-    attend_keys<NW>(R, smem, r.key0, r.key1, s.n * a.group, src, sees, queries, emit, wave, lane);
+    attend_keys(R, smem, r.key0, r.key1, s.n * a.group, src, sees, queries, emit, wave, lane);
 }
 
 // The parts of a row, joined in the order of their keys (one result whatever
@@ -362,7 +349,7 @@ __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) 
         }
     }
     const float f = inverse_sum(sum) * (a.v_scale ? a.v_scale[kvh] : 1.0f);
-    const int64_t out = (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
+    const int64_t out = tree_out(a, s, kvh, row);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         const int col = lane * W + j;
@@ -373,36 +360,27 @@ __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) 
     if (lane == 0 && a.lse) a.lse[out] = log_sum_exp(top == -INFINITY ? 0.f : top, sum);
 }
 
-// Rows a workgroup of the launch holds: 32, 128 or 256 (eight waves need a
-// load each for a step's rows: not the 8 KiB of E4M3 rows of 64).
-constexpr int tile_rows(int64_t rows, int64_t d, bool fp8) {
-    return rows <= 32 ? 32 : rows <= 128 || (fp8 && d == 64) ? 128 : 256;
-}
+// Rows a workgroup of the launch holds.  (Eight waves with 256 rows, one
+// workgroup a CU, took the same time for 198 rows of 256 over 32768 E4M3 keys
+// as two workgroups of four.)
+constexpr int tile_rows(int64_t rows) { return rows <= 32 ? 32 : 128; }
 
 template <int D, bool FP8, bool BF16OUT>
 hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
     const unsigned units = (unsigned)(a.want + a.seqs) * a.hkv;
     hipError_t e;
-    const int tile = tile_rows(a.max_q * a.group, D, FP8);
-    if (tile == 32) {
-        constexpr int LDS = KeysLds<D, FP8, 4>::BYTES;
-        auto kernel = attn_tree_keys_kernel<D, 4, FP8, BF16OUT>;
+    if (tile_rows(a.max_q * a.group) == 32) {
+        constexpr int LDS = KeysLds<D, FP8>::BYTES;
+        auto kernel = attn_tree_keys_kernel<D, FP8, BF16OUT>;
         static LdsLimit limit;
         if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
         kernel<<<units, 256, LDS, stream>>>(a);
-    } else if (tile == 128 || (FP8 && D == 64)) {
-        constexpr int LDS = RowsLds<D, FP8, 4, 2>::BYTES;
-        auto kernel = attn_tree_rows_kernel<D, 4, FP8, BF16OUT>;
-        static LdsLimit limit;
-        if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
-        kernel<<<units * a.row_tiles, 256, LDS, stream>>>(a);
     } else {
-        constexpr int NW = FP8 && D == 64 ? 4 : 8;
-        constexpr int LDS = RowsLds<D, FP8, NW, 2>::BYTES;
-        auto kernel = attn_tree_rows_kernel<D, NW, FP8, BF16OUT>;
+        constexpr int LDS = RowsLds<D, FP8>::BYTES;
+        auto kernel = attn_tree_rows_kernel<D, FP8, BF16OUT>;
         static LdsLimit limit;
         if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
-        kernel<<<units * a.row_tiles, NW * 64, LDS, stream>>>(a);
+        kernel<<<(units + 7) / 8 * 8 * a.row_tiles, 256, LDS, stream>>>(a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.want > 0) {
@@ -428,12 +406,15 @@ struct TreePlan {
 // write for each part, 256, and up.  Few sequences: as many
 // workgroups as run at once.  Many: about four times as many, short enough
 // that the last ones to run do not leave most CUs idle.
-TreePlan tree_plan(bool fp8, int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
-    const int64_t rows = max_q * (hq / hkv), tile = attn::tile_rows(rows, d, fp8), tiles = (rows + tile - 1) / tile;
+TreePlan tree_plan(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
+    const int64_t rows = max_q * (hq / hkv), tile = attn::tile_rows(rows), tiles = (rows + tile - 1) / tile;
     const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles, cus = device_cu_count();
     TreePlan p{0, (int)least, rows <= 32 ? 128 : 32, (int)tiles, 0};
-    if (max_len <= least) return p;
-    const int64_t slots = cus * (tile == 256 || (tile == 32 && d == 256) ? 1 : 2);        // workgroups that run at once
+    // Short contexts: one range a sequence and one launch.  (701 keys of 24 / 4
+    // heads of 256: 10 + 5 us of kernels and two launches, or 16 us and one;
+    // 19.2 and 17.9 us a step, the cache's append included.)
+    if (max_len <= 768) return p;
+    const int64_t slots = cus * (tile == 32 && d == 256 ? 1 : 2);        // workgroups that run at once
     int64_t want = (2 * units <= slots ? slots : 4 * cus) / (hkv * tiles);
     const int64_t most = seqs * ((max_len + least - 1) / least) + seqs;
     if (want > most) want = most;
@@ -446,9 +427,7 @@ TreePlan tree_plan(bool fp8, int64_t seqs, int64_t max_q, int64_t hq, int64_t hk
 }  // namespace
 
 int64_t attn_tree_workspace_bytes(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
-    // (a query does not name the cache's format: the larger of the two)
-    const int64_t x = tree_plan(false, seqs, max_q, hq, hkv, d, max_len).bytes, y = tree_plan(true, seqs, max_q, hq, hkv, d, max_len).bytes;
-    return x > y ? x : y;
+    return tree_plan(seqs, max_q, hq, hkv, d, max_len).bytes;
 }
 
 hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
@@ -458,7 +437,7 @@ hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const
                             int64_t max_len, float scale, bool bf16_out, void* o, float* lse, void* workspace,
                             int64_t workspace_bytes, hipStream_t stream) {
     using namespace attn;
-    TreePlan p = tree_plan(fp8, seqs, max_q, hq, hkv, d, max_len);
+    TreePlan p = tree_plan(seqs, max_q, hq, hkv, d, max_len);
     if (workspace_bytes < p.bytes) p.want = 0;
     const TreeArgs a{q, q_stride, k_pages, v_pages, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, table, (int)width, lens,
                      cu_q, masks, (int)seqs, (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size),

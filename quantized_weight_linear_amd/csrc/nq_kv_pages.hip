@@ -250,8 +250,17 @@ struct Branch {
     }
 };
 
+// Entry e of child c: whole pages are shared and counted.
+__device__ __forceinline__ void share_entry(const ForkArgs& a, const Branch& br, int c, int64_t e) {
+    int32_t page = e < br.full ? br.row[e] : e == br.full ? a.copies[2 * c + 1] : -1;
+    if (page >= a.pages) page = -1;
+    if (e < br.full && page >= 0) atomicAdd(&a.refs[page], 1);
+    a.child[c * a.width + e] = page < 0 ? -1 : page;
+}
+
 // One workgroup: a page for every child whose parent ends inside a page.
-__global__ __launch_bounds__(POOL_THREADS) void kv_fork_pages_kernel(ForkArgs a) {
+// `share`: the entries too (few of them; otherwise the next kernel's work).
+__global__ __launch_bounds__(POOL_THREADS) void kv_fork_pages_kernel(ForkArgs a, bool share) {
     __shared__ int part[POOL_THREADS / 64];
     int wanted = 0, total;
     for (int c0 = 0; c0 < a.children; c0 += POOL_THREADS) {
@@ -276,18 +285,18 @@ __global__ __launch_bounds__(POOL_THREADS) void kv_fork_pages_kernel(ForkArgs a)
         }
     }
     if (threadIdx.x == 0) *a.shortfall = wanted - found;
+    if (!share) return;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < a.children * a.width; i += POOL_THREADS) {
+        const int c = (int)(i / a.width);
+        share_entry(a, Branch(a, c), c, i % a.width);
+    }
 }
 
-// Then a thread an entry: whole pages are shared and counted.
 __global__ __launch_bounds__(256) void kv_fork_share_kernel(ForkArgs a) {
     const int64_t e = (int64_t)blockIdx.y * 256 + threadIdx.x;
     const int c = blockIdx.x;
-    if (e >= a.width) return;
-    const Branch br(a, c);
-    int32_t page = e < br.full ? br.row[e] : e == br.full ? a.copies[2 * c + 1] : -1;
-    if (page >= a.pages) page = -1;
-    if (e < br.full && page >= 0) atomicAdd(&a.refs[page], 1);
-    a.child[c * a.width + e] = page < 0 ? -1 : page;
+    if (e < a.width) share_entry(a, Branch(a, c), c, e);
 }
 
 // 16 KiB of one page a workgroup.
@@ -397,8 +406,10 @@ hipError_t launch_kv_fork(int32_t* refs, int64_t pages, const int32_t* table, in
                           int32_t* free_list, int32_t* shortfall, hipStream_t stream) {
     const ForkArgs a{refs, pages, table, width, lens, (int)seqs, parents, (int)children, shift_of(page_size), child_table,
                      copies, free_list, shortfall};
-    kv_fork_pages_kernel<<<1, POOL_THREADS, 0, stream>>>(a);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    // a few rounds of one workgroup take less than another launch
+    const bool share = children * width <= 4 * POOL_THREADS;
+    kv_fork_pages_kernel<<<1, POOL_THREADS, 0, stream>>>(a, share);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || share) return e;
     kv_fork_share_kernel<<<dim3((unsigned)children, (unsigned)((width + 255) / 256)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }

@@ -393,6 +393,24 @@ def test_tree_unseen_drafts_do_not_matter(fp8, d, n, poison):
         check(*run_tree(q, cache, lens, drafts, masks, 0.1, out), *ref, out)
 
 
+@pytest.mark.parametrize("n", [2, 40])
+def test_tree_scales_of_zero_and_below(n):
+    """An all-zero head has a scale of zero; nothing forbids a negative one.  Masked keys stay masked."""
+    lens, drafts = [75, 3], [n, n]
+    cache, masks = Cache(lens, drafts, 3, 64, 16, True, 63), trees(drafts, 64)
+    ks, vs = torch.tensor([0.0, -0.013, 0.01]), torch.tensor([-0.02, 0.01, 0.0])
+    for b in range(2):
+        cache.k[b] *= (ks.double() / cache.ks.double())[:, None]
+        cache.v[b] *= (vs.double() / cache.vs.double())[:, None]
+    cache.ks, cache.vs = ks, vs
+    q = randn((2 * n, 6, 64), 65)
+    o, lse = run_tree(q, cache, lens, drafts, masks, 0.125, torch.float32)
+    ref, rl = tree_oracle(q, cache, lens, drafts, masks, 0.125)
+    err = (o.double().cpu() - ref).norm() / ref.norm()
+    assert err <= FP32_TOL
+    assert ((lse.double().cpu() - rl).abs() <= LSE_TOL * rl.abs().clamp(min=1)).all()
+
+
 def test_tree_pages_outside_the_pool_read_as_zeros():
     lens, drafts = [100], [2]
     cache, masks = Cache(lens, drafts, 1, 64, 16, False, 55), trees(drafts, 56)
