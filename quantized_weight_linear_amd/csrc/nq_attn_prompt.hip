@@ -1,6 +1,6 @@
 // Causal attention over packed prompts (nq_attn_prompt).
 //
-// One workgroup per (128 or 256 query tokens of a sequence, query head): the
+// One workgroup per (128 or 32 query tokens of a sequence, query head): the
 // keys and values that tile sees are read from LDS, where the workgroup's
 // waves share them; grouped query heads read the same K and V through L2.
 // Bound by the matrix cores: 4 D flops per (row, visible key).
@@ -25,11 +25,8 @@ struct PromptArgs {
     float* lse;
 };
 
-// A packed offset, kept inside [0, total] and in order whatever the array holds.
-__device__ __forceinline__ int64_t offset_of(const int32_t* cu, int i, int64_t total) {
-    const int64_t x = uniform(cu, i);
-    return x < 0 ? 0 : x > total ? total : x;
-}
+// A packed offset, kept inside [0, total] whatever the array holds.
+__device__ __forceinline__ int cut_offset(int x, int64_t total) { return x < 0 ? 0 : x > (int)total ? (int)total : x; }
 
 struct PackedRows {                 // K or V rows of one sequence and KV head
     const uint16_t *k, *v;
@@ -54,30 +51,69 @@ struct CausalSees {
     __device__ __forceinline__ uint64_t seen(int key) const { return bits_below(limit - key); }
 };
 
-// The tile of BM query rows that workgroup `index` of a head has: the
-// sequences in order, in each its last tile, which sees most keys, first.
+// The tile of bm query rows that workgroup `index` of a head has: the
+// sequences in order, in each its last tile, which sees most keys, first.  A
+// wave looks through 256 sequences at a time (1000 of 1 .. 33 tokens, 24 heads
+// of 256: one after another 5.4 ms, 64 at a time 0.86, so 0.75).
 struct QueryTile {
     int64_t q0, k0;                 // the sequence's first query and key
     int nq, nk, first, last;        // its lengths; rows [first, last) of it
     bool real;
-    __device__ __forceinline__ QueryTile(const PromptArgs& a, int index, int bm) {
-        int64_t q1 = 0;
-        int b = 0, tiles = 0;
-        q0 = 0;
-        for (; b < a.seqs; ++b) {
-            q0 = offset_of(a.cu_q, b, a.tq);
-            q1 = offset_of(a.cu_q, b + 1, a.tq);
-            tiles = q1 > q0 ? (int)((q1 - q0 + bm - 1) / bm) : 0;
-            if (index < tiles) break;
-            index -= tiles;
+    __device__ __forceinline__ static uint32_t tiles_of(int q0, int q1, int bm) { return q1 > q0 ? ((uint32_t)(q1 - q0) + bm - 1) / bm : 0u; }
+    __device__ __forceinline__ QueryTile(const PromptArgs& a, uint32_t index, int bm) {
+        constexpr int PER = 4;      // sequences a lane
+        int b = 0;
+        real = a.seqs == 1;
+        if (!real) {
+            const int lane = threadIdx.x & 63;
+            for (int b0 = 0; b0 < a.seqs && !real; b0 += 64 * PER) {
+                int edge[PER + 1];
+#pragma unroll
+                for (int e = 0; e <= PER; ++e) {
+                    const int at = b0 + lane * PER + e;
+                    edge[e] = a.cu_q[at < a.seqs ? at : a.seqs];
+                }
+                uint32_t n[PER], mine = 0;              // (a tile count is below 2^26; in 64 bits for offsets out of order)
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    n[e] = tiles_of(cut_offset(edge[e], a.tq), cut_offset(edge[e + 1], a.tq), bm);
+                    mine += n[e];
+                }
+                uint64_t upto = mine;
+#pragma unroll
+                for (int off = 1; off < 64; off <<= 1) {
+                    const uint64_t y = __shfl_up(upto, off, 64);
+                    if (lane >= off) upto += y;
+                }
+                const uint64_t past = __ballot(upto > index);
+                real = past != 0;
+                if (!real) {
+                    index -= __builtin_amdgcn_readlane((uint32_t)upto, 63);
+                    continue;
+                }
+                const int which = __builtin_ctzll(past);
+                index -= __builtin_amdgcn_readlane((uint32_t)upto - mine, which);
+                b = b0 + which * PER;
+#pragma unroll
+                for (int e = 0; e + 1 < PER; ++e) {     // past the lane's first sequences
+                    const uint32_t here = __builtin_amdgcn_readlane(n[e], which);
+                    if (b != b0 + which * PER + e || index < here) continue;
+                    index -= here;
+                    ++b;
+                }
+            }
+            if (!real) return;
         }
-        real = b < a.seqs;
+        q0 = cut_offset(uniform(a.cu_q, b), a.tq);
+        const int64_t q1 = cut_offset(uniform(a.cu_q, b + 1), a.tq);
+        const uint32_t tiles = tiles_of((int)q0, (int)q1, bm);
+        real = index < tiles;
         if (!real) return;
-        k0 = offset_of(a.cu_k, b, a.tk);
-        const int64_t k1 = offset_of(a.cu_k, b + 1, a.tk);
+        k0 = cut_offset(uniform(a.cu_k, b), a.tk);
+        const int64_t k1 = cut_offset(uniform(a.cu_k, b + 1), a.tk);
         nq = (int)(q1 - q0);
         nk = k1 > k0 ? (int)(k1 - k0) : 0;
-        first = (tiles - 1 - index) * bm;
+        first = (int)(tiles - 1 - index) * bm;
         last = first + bm < nq ? first + bm : nq;
     }
 };
@@ -180,11 +216,6 @@ hipError_t launch_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_
     using namespace attn;
     const PromptArgs a{q, k, v, q_stride, k_stride, v_stride, cu_q, cu_k, (int)seqs, tq, tk, (int)hq, (int)hkv,
                        scale * LOG2E, o, lse};
-    // Few tiles of 128 rows: 32 rows a workgroup, so that more CUs have one
-    // and each row's keys are walked four at a time; 512 tokens of 24 heads of
-    // 256 take 25 us so and 29 us the other way, of 32 heads of 128 11 and 17,
-    // 1024 of 24 of 256 60 and 50.  (With two key tiles there is nothing to share out: 33
-    // tokens of 24 heads of 256 11 and 8.5 us.)
     // Few tiles of 128 rows: 32 rows a workgroup, so that more CUs have one and
     // each row's keys are walked four at a time; 512 tokens of 24 heads of 256
     // take 25 us so and 29 the other way, of 32 heads of 128 11 and 17, 1024 of

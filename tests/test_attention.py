@@ -139,6 +139,18 @@ def test_prompt_many_tiles(d):
         check(o, lse, *prompt_oracle(q, k, v, n, n, 1 / math.sqrt(d)), out)
 
 
+@pytest.mark.parametrize("hq,hkv,longest", [(2, 1, 33), (12, 1, 300)])
+def test_prompt_many_sequences(hq, hkv, longest):
+    """More sequences than a wave has lanes, empty ones among them and at the ends."""
+    g = gen(3)
+    ns = [0, 0] + torch.randint(1, longest + 1, (150,), generator=g).tolist() + [0]
+    ns[63], ns[64], ns[100] = 0, 0, longest
+    ms = [n + int(e) for n, e in zip(ns, torch.randint(0, 3, (len(ns),), generator=g))]
+    q, k, v = randn((sum(ns), hq, 64), 4), randn((sum(ms), hkv, 64), 5), randn((sum(ms), hkv, 64), 6)
+    o, lse = run_prompt(q, k, v, ns, ms, 0.125, torch.float32)
+    check(o, lse, *prompt_oracle(q, k, v, ns, ms, 0.125), torch.float32)
+
+
 @pytest.mark.parametrize("d", [64, 256])
 def test_prompt_rising_and_large_logits(d):
     """Keys that grow along the sequence move the running reference again and again; logits reach several hundred."""
