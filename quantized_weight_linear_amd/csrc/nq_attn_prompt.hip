@@ -3,7 +3,10 @@
 // One workgroup per (128 or 32 query tokens of a sequence, query head): the
 // keys and values that tile sees are read from LDS, where the workgroup's
 // waves share them; grouped query heads read the same K and V through L2.
-// Bound by the matrix cores: 4 D flops per (row, visible key).
+// Bound by the matrix cores: 4 D flops per (row, visible key).  Neighbouring
+// workgroups are heads of one tile, so that one round of them reads the same
+// keys; 1792 tokens on top of 8192 keys, 24 heads of 256, take 0.45 ms (336
+// workgroups for 512 places: 885 TFLOP/s).
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
@@ -130,7 +133,8 @@ __device__ __forceinline__ PackedRows packed_rows(const PromptArgs& a, const Que
     return src;
 }
 
-// Few tiles: 32 rows a workgroup, whose four waves take different keys.
+// Few tiles: 32 rows a workgroup, whose four waves take different keys (167
+// tokens of 24 heads of 256: 12 us, latency).
 template <int D, bool BF16OUT>
 __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -157,7 +161,8 @@ __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     attend_keys(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
 }
 
-// Many tiles: 128 rows a workgroup.
+// Many tiles: 128 rows a workgroup (16384 tokens of 24 heads of 256: 1170
+// TFLOP/s).
 template <int D, bool BF16OUT>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_prompt_rows_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
