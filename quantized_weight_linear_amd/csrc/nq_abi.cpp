@@ -603,7 +603,7 @@ bool stride_ok(int64_t stride, int64_t heads, int64_t D) {
 bool page_ok(int64_t page_size) { return page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0; }
 bool table_ok(int64_t B, int64_t width, int64_t page_size, int64_t pages) {
     return B >= 0 && B < MOST_BLOCKS && width >= 0 && pages >= 0 && pages < I31 && page_ok(page_size) &&
-           width * page_size <= ((int64_t)1 << 30);
+           width <= ((int64_t)1 << 30) / page_size;
 }
 bool scale_ok(float scale) { return scale >= 1e-30f && scale <= 1e30f; }       // (false for NaN)
 
@@ -726,7 +726,7 @@ nq_status nq_kv_fork(int32_t* refs, int64_t pages, const int32_t* page_table, in
 nq_status nq_kv_copy_pages(void* pool, int64_t planes, int64_t plane_bytes, int64_t page_bytes, int64_t pages,
                            const int32_t* copies, int64_t n, void* stream) {
     if (planes < 0 || planes > 65535 || page_bytes < 0 || page_bytes % 16 != 0 || page_bytes >= I31 || pages < 0 ||
-        pages >= I31 || plane_bytes % 16 != 0 || (pages > 0 && plane_bytes / pages < page_bytes) || n < 0 ||
+        pages >= I31 || plane_bytes % 16 != 0 || (pages > 0 && plane_bytes / pages < page_bytes) || n < 0 || n >= I31 ||
         n * ((page_bytes + 16383) / 16384) >= MOST_BLOCKS)
         return NQ_ERR_SHAPE;
     if (planes == 0 || page_bytes == 0 || pages == 0 || n == 0) return NQ_OK;

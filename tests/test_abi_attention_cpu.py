@@ -92,6 +92,17 @@ def test_cache_refusals(L):
     assert L.nq_kv_compact(*dict(good, accepted=0, accept=None).values()) == nq.NQ_OK
 
 
+@pytest.mark.parametrize("width", [1 << 27, 1 << 57, 1 << 59, (1 << 63) - 1])
+def test_tables_beyond_all_sizes(L, width):
+    """Widths whose product with the page size passes 2^30 tokens, 64 bits included."""
+    S = nq.NQ_ERR_SHAPE
+    assert L.nq_kv_release(A, 9, A, width, A, 2, 16, None) == S
+    assert L.nq_kv_reserve(A, 9, A, width, A, A, 2, 16, A, A, None) == S
+    assert L.nq_attn_tree(0, A, 1536, A, A, None, None, A, width, A, A, A, 2, 4, 6, 6, 1, 256, 32, 9, 100, 0.1, 1, A, None, None, 0,
+                          None) == S
+    assert L.nq_kv_copy_pages(A, 2, 9 * 4096, 4096, 9, A, width << 4 & (1 << 63) - 1 | 1 << 47, None) == S
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     q, k = torch.zeros((4, 6, 64), dtype=torch.bfloat16), torch.zeros((4, 2, 64), dtype=torch.bfloat16)
     cu, o = torch.tensor([0, 4], dtype=torch.int32), torch.zeros((4, 6, 64))
