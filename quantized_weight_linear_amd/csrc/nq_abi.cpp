@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "nq.h"
+#include "nq_attn_launch.h"
 #include "nq_launch.h"
 
 namespace {

@@ -16,7 +16,7 @@
 
 #include "nq.h"
 #include "nq_attn_keys.h"
-#include "nq_launch.h"
+#include "nq_attn_launch.h"
 
 namespace nq {
 namespace attn {

@@ -11,8 +11,8 @@
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
+#include "nq_attn_launch.h"
 #include "nq_device.h"
-#include "nq_launch.h"
 
 namespace nq {
 namespace {
