@@ -220,7 +220,7 @@ __device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const
 // More than 32 rows: 128 a workgroup.  Bound by the vector ALU and the products,
 // and by the parts it writes: 33 drafts of 24 / 4 heads of 256 over 32768 keys
 // 50 us in an E4M3 cache (10 vector instructions a product, 4 of them the
-// decode; 52 MB of parts, and the join below reads them in 13 us).  With half as
+// decode; 52 MB of parts, and the join below reads them in 12 us).  With half as
 // many parts, one workgroup a CU, 53 + 9 us.
 template <int D, bool FP8, bool BF16OUT>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tree_rows_kernel(TreeArgs a) {
@@ -298,8 +298,9 @@ __global__ __launch_bounds__(256) void attn_tree_keys_kernel(TreeArgs a) {
 
 // The parts of a row, joined in the order of their keys (one result whatever
 // the order in which the parts were made).  WAVES waves a row, each summing
-// every WAVES-th part; then the waves are added.  Bound by the parts' bytes: 52
-// MB in 13 us; 7 us where there is little to join.
+// every WAVES-th part; then the waves are added.  Bound by the parts' bytes, 52
+// MB in 12 us, and by latency where there is little to join, 7 us: the ranges
+// are loaded beside the lengths and the parts beside their references.
 template <int D, int WAVES, bool BF16OUT>
 __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) {
     __shared__ float sum_s[WAVES];
@@ -307,20 +308,26 @@ __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rows = a.max_q * a.group;
     const int row = blockIdx.x % rows, kvh = blockIdx.x / rows % a.hkv, b = blockIdx.x / rows / a.hkv;
-    const Seq s(a, b);
-    if (row >= s.n * a.group) return;
+    // (loaded beside the lengths: a sequence without drafts has left nothing there)
     const int* ranges = reinterpret_cast<const int*>(part_ranges(a, D));
     const int first = uniform(ranges, 2 * b), parts = uniform(ranges, 2 * b + 1);
-    if (parts <= 1) return;
+    const Seq s(a, b);
+    if (row >= s.n * a.group || parts <= 1) return;
     const float2* ml = part_sums(a, D);
     constexpr int W = D / 64, BATCH = 16;               // columns a lane; parts whose loads are in flight together
     typedef float vw __attribute__((ext_vector_type(W)));
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 64) {
-        const float2 p = ml[part_row(a, first + i, kvh, row)];
-        if (p.y != 0.f) top = max2(top, p.x);
-    }
-    float sum = 0.f, x[W];
+    float2 tops[MOST_PARTS / 64];                       // this lane's parts (a part twice does no harm)
+#pragma unroll
+    for (int i = 0; i < MOST_PARTS / 64; ++i)
+        tops[i] = ml[part_row(a, first + (i * 64 + lane < parts ? i * 64 + lane : 0), kvh, row)];
+    auto highest = [&] {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < MOST_PARTS / 64; ++i)
+            if (tops[i].y != 0.f) top = max2(top, tops[i].x);
+        return wave_max(top);
+    };
+    float top = -INFINITY, sum = 0.f, x[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) x[j] = 0.f;
     bool have = false;
@@ -333,7 +340,7 @@ __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) 
             p[e] = ml[at];
             y[e] = *reinterpret_cast<const vw*>(a.parts + at * D + lane * W);
         }
-        if (!have) top = wave_max(top);                 // (beside the first loads)
+        if (!have) top = highest();                     // (beside the first loads)
         have = true;
 #pragma unroll
         for (int e = 0; e < BATCH; ++e) {
@@ -344,7 +351,7 @@ __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) 
             for (int j = 0; j < W; ++j) x[j] += real ? y[e][j] * f : 0.f;
         }
     }
-    if (!have) top = wave_max(top);
+    if (!have) top = highest();
     if constexpr (WAVES > 1) {
 #pragma unroll
         for (int j = 0; j < W; ++j) o_s[wave][lane * W + j] = x[j];
