@@ -22,8 +22,9 @@
  *   - BF16 / FP16 values are passed as their 16-bit patterns (uint16_t), FP32
  *     as float, E4M3 codes as uint8_t (OCP E4M3, "e4m3fn": bias 7, largest
  *     finite 448, S.1111.111 is NaN).
- *   - All data pointers are DEVICE pointers and must be 16-byte aligned.  The
- *     caller owns every buffer; the library allocates nothing and keeps no
+ *   - All data pointers are DEVICE pointers and must be 16-byte aligned (the
+ *     attention and cache calls need less of their small arrays, see there).
+ *     The caller owns every buffer; the library allocates nothing and keeps no
  *     state between calls.  `stream` is a hipStream_t (NULL = the default
  *     stream); every call only enqueues work on it and returns without
  *     synchronizing.  Output buffers must not overlap inputs.
@@ -48,7 +49,7 @@ typedef enum {
     NQ_OK = 0,
     NQ_ERR_NULL = 1,    /* a required pointer is NULL */
     NQ_ERR_SHAPE = 2,   /* a size is negative, a divisibility rule fails, or a grid does not match */
-    NQ_ERR_ALIGN = 3,   /* a pointer is not 16-byte aligned */
+    NQ_ERR_ALIGN = 3,   /* a pointer is not aligned as the call needs (16 bytes where nothing else is said) */
     NQ_ERR_FORMAT = 4,  /* an enum value is unknown */
     NQ_ERR_RANGE = 5,   /* a row range is empty or outside [0, N] */
     NQ_ERR_HIP = 6,     /* the HIP runtime reported an error when enqueuing */
@@ -449,6 +450,9 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
  *   - Logits, softmax statistics and sums are FP32.  The weights of the
  *     softmax are rounded to BF16 for a BF16 output, and to three BF16 terms
  *     (22 bits) for an FP32 output.
+ *   - Rows (q, k, v, o), planes and the workspace are 16-byte aligned, tree
+ *     masks 8, and all other arrays 4 (scales, offsets, lengths, tables, lse,
+ *     page counts and pairs), so that a slice of a longer array can be passed.
  *   - `scale` multiplies the logits; it must lie in [1e-30, 1e30]
  *     (NQ_ERR_RANGE).
  */

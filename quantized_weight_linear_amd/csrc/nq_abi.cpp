@@ -79,7 +79,7 @@ const char* nq_status_string(int status) {
         case NQ_OK: return "ok";
         case NQ_ERR_NULL: return "a required pointer is NULL";
         case NQ_ERR_SHAPE: return "invalid shape";
-        case NQ_ERR_ALIGN: return "pointer not 16-byte aligned";
+        case NQ_ERR_ALIGN: return "a pointer is not aligned as the call needs";
         case NQ_ERR_FORMAT: return "unknown format or output type";
         case NQ_ERR_RANGE: return "row range out of bounds";
         case NQ_ERR_HIP: return "HIP runtime error";
@@ -608,12 +608,16 @@ bool table_ok(int64_t B, int64_t width, int64_t page_size, int64_t pages) {
 }
 bool scale_ok(float scale) { return scale >= 1e-30f && scale <= 1e30f; }       // (false for NaN)
 
-template <class... P>
-nq_status all_there(P... p) {
+// Pointers that may be NULL, aligned to what the kernels read of them at once:
+// 16 bytes of rows, pages and workspace, 8 of masks, 4 of everything else.
+template <int BYTES>
+nq_status at_ok(const void* p) { return reinterpret_cast<uintptr_t>(p) % BYTES == 0 ? NQ_OK : NQ_ERR_ALIGN; }
+
+template <int BYTES, class... P>
+nq_status all_at(P... p) {
     for (const void* x : {(const void*)p...})
         if (x == nullptr) return NQ_ERR_NULL;
-    for (const void* x : {(const void*)p...})
-        if (!aligned16(x)) return NQ_ERR_ALIGN;
+    for (const void* x : {(const void*)p...}) NQ_TRY(at_ok<BYTES>(x));
     return NQ_OK;
 }
 
@@ -630,12 +634,13 @@ nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k,
     if (!out_ok(out_dt)) return NQ_ERR_FORMAT;
     if (!scale_ok(scale)) return NQ_ERR_RANGE;
     if (B == 0 || Tq == 0) return NQ_OK;
-    NQ_TRY(all_there(q, cu_q, cu_k, o));
+    NQ_TRY(all_at<16>(q, o));
+    NQ_TRY(all_at<4>(cu_q, cu_k));
     NQ_TRY(need(k, Tk));
     NQ_TRY(need(v, Tk));
     NQ_TRY(align_ok(k));
     NQ_TRY(align_ok(v));
-    NQ_TRY(align_ok(lse));
+    NQ_TRY(at_ok<4>(lse));
     return from_hip(nq::launch_attn_prompt(q, q_stride, k, k_stride, v, v_stride, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, scale,
                                            out_dt == NQ_OUT_BF16, o, lse, as_stream(stream)));
 }
@@ -649,8 +654,9 @@ nq_status nq_kv_append(int kv_fmt, const uint16_t* k, int64_t k_stride, const ui
     if (!stride_ok(k_stride, Hkv, D) || !stride_ok(v_stride, Hkv, D)) return NQ_ERR_SHAPE;
     if (T * Hkv * D / (8 * 256) >= MOST_BLOCKS) return NQ_ERR_SHAPE;
     if (B == 0 || T == 0 || width == 0 || pages == 0) return NQ_OK;
-    NQ_TRY(all_there(k, v, page_table, lens, cu, k_pages, v_pages));
-    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_there(k_scale, v_scale));
+    NQ_TRY(all_at<16>(k, v, k_pages, v_pages));
+    NQ_TRY(all_at<4>(page_table, lens, cu));
+    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_at<4>(k_scale, v_scale));
     return from_hip(nq::launch_kv_append(kv_fmt == NQ_KV_E4M3, k, k_stride, v, v_stride, k_scale, v_scale, page_table, width,
                                          lens, cu, B, T, Hkv, D, page_size, pages, k_pages, v_pages, as_stream(stream)));
 }
@@ -674,15 +680,17 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
     if (B * Hq * max_q >= MOST_BLOCKS || B * Hq * 4 >= MOST_BLOCKS) return NQ_ERR_SHAPE;
     if (!scale_ok(scale)) return NQ_ERR_RANGE;
     if (B == 0 || T == 0) return NQ_OK;
-    NQ_TRY(all_there(q, lens, cu_q, tree_mask, o));
+    NQ_TRY(all_at<16>(q, o));
+    NQ_TRY(all_at<8>(tree_mask));
+    NQ_TRY(all_at<4>(lens, cu_q));
     NQ_TRY(need(page_table, width));
     NQ_TRY(need(k_pages, pages));
     NQ_TRY(need(v_pages, pages));
-    NQ_TRY(align_ok(page_table));
+    NQ_TRY(at_ok<4>(page_table));
     NQ_TRY(align_ok(k_pages));
     NQ_TRY(align_ok(v_pages));
-    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_there(k_scale, v_scale));
-    NQ_TRY(align_ok(lse));
+    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_at<4>(k_scale, v_scale));
+    NQ_TRY(at_ok<4>(lse));
     NQ_TRY(align_ok(workspace));
     return from_hip(nq::launch_attn_tree(kv_fmt == NQ_KV_E4M3, q, q_stride, k_pages, v_pages, k_scale, v_scale, page_table,
                                          width, lens, cu_q, tree_mask, B, max_q, T, Hq, Hkv, D, page_size, pages, max_len,
@@ -694,9 +702,9 @@ nq_status nq_kv_reserve(int32_t* refs, int64_t pages, int32_t* page_table, int64
                         const int32_t* new_lens, int64_t B, int64_t page_size, int32_t* free_list, int32_t* shortfall,
                         void* stream) {
     if (!table_ok(B, width, page_size, pages) || B > 8192 || B * width >= I31) return NQ_ERR_SHAPE;
-    NQ_TRY(all_there(shortfall));
-    if (B > 0 && width > 0) NQ_TRY(all_there(page_table, lens, new_lens));
-    if (pages > 0) NQ_TRY(all_there(refs, free_list));
+    NQ_TRY(all_at<4>(shortfall));
+    if (B > 0 && width > 0) NQ_TRY(all_at<4>(page_table, lens, new_lens));
+    if (pages > 0) NQ_TRY(all_at<4>(refs, free_list));
     return from_hip(nq::launch_kv_reserve(refs, pages, page_table, width, lens, new_lens, width > 0 ? B : 0, page_size, free_list, shortfall,
                                           as_stream(stream)));
 }
@@ -705,8 +713,8 @@ nq_status nq_kv_release(int32_t* refs, int64_t pages, int32_t* page_table, int64
                         int64_t B, int64_t page_size, void* stream) {
     if (!table_ok(B, width, page_size, pages) || width / 256 >= 65535) return NQ_ERR_SHAPE;
     if (B == 0 || width == 0) return NQ_OK;
-    NQ_TRY(all_there(page_table, keep_lens));
-    if (pages > 0) NQ_TRY(all_there(refs));
+    NQ_TRY(all_at<4>(page_table, keep_lens));
+    if (pages > 0) NQ_TRY(all_at<4>(refs));
     return from_hip(nq::launch_kv_release(refs, pages, page_table, width, keep_lens, B, page_size, as_stream(stream)));
 }
 
@@ -715,11 +723,11 @@ nq_status nq_kv_fork(int32_t* refs, int64_t pages, const int32_t* page_table, in
                      int32_t* free_list, int32_t* shortfall, void* stream) {
     if (!table_ok(B, width, page_size, pages) || width / 256 >= 65535 || children < 0 || children >= MOST_BLOCKS) return NQ_ERR_SHAPE;
     if (children == 0) return NQ_OK;
-    NQ_TRY(all_there(parents, copies, shortfall));
-    if (B > 0) NQ_TRY(all_there(lens));
-    if (width > 0) NQ_TRY(all_there(child_table));
-    if (B > 0 && width > 0) NQ_TRY(all_there(page_table));
-    if (pages > 0) NQ_TRY(all_there(refs, free_list));
+    NQ_TRY(all_at<4>(parents, copies, shortfall));
+    if (B > 0) NQ_TRY(all_at<4>(lens));
+    if (width > 0) NQ_TRY(all_at<4>(child_table));
+    if (B > 0 && width > 0) NQ_TRY(all_at<4>(page_table));
+    if (pages > 0) NQ_TRY(all_at<4>(refs, free_list));
     return from_hip(nq::launch_kv_fork(refs, pages, page_table, width, lens, B, parents, children, page_size, child_table,
                                        copies, free_list, shortfall, as_stream(stream)));
 }
@@ -731,7 +739,8 @@ nq_status nq_kv_copy_pages(void* pool, int64_t planes, int64_t plane_bytes, int6
         n * ((page_bytes + 16383) / 16384) >= MOST_BLOCKS)
         return NQ_ERR_SHAPE;
     if (planes == 0 || page_bytes == 0 || pages == 0 || n == 0) return NQ_OK;
-    NQ_TRY(all_there(pool, copies));
+    NQ_TRY(all_at<16>(pool));
+    NQ_TRY(all_at<4>(copies));
     return from_hip(nq::launch_kv_copy_pages(pool, planes, plane_bytes, page_bytes, pages, copies, n, as_stream(stream)));
 }
 
@@ -743,7 +752,8 @@ nq_status nq_kv_compact(void* pool, int64_t planes, int64_t plane_bytes, int64_t
         (pages > 0 && plane_bytes / pages < Hkv * page_size * row_bytes) || B * Hkv >= MOST_BLOCKS)
         return NQ_ERR_SHAPE;
     if (B == 0 || accepted == 0 || planes == 0 || pages == 0 || width == 0) return NQ_OK;
-    NQ_TRY(all_there(pool, page_table, lens, accept, cu_accept));
+    NQ_TRY(all_at<16>(pool));
+    NQ_TRY(all_at<4>(page_table, lens, accept, cu_accept));
     return from_hip(nq::launch_kv_compact(pool, planes, plane_bytes, Hkv, page_size, row_bytes, pages, page_table, width, lens,
                                           accept, cu_accept, B, accepted, as_stream(stream)));
 }

@@ -134,3 +134,21 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(nq.NQError) as e:
         nq.nq_attn_prompt(q, k, k, cu, cu, 0.0, o)
     assert e.value.status == nq.NQ_ERR_RANGE
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="the addresses are not real: a launch has to fail")
+def test_small_arrays_need_no_more_than_their_elements_alignment(L):
+    """Scales, offsets, lengths, tables, counts and pairs at 4 bytes, masks at 8: the checks pass, the launch fails."""
+    S4, S8, HIP = A + 4, A + 8, nq.NQ_ERR_HIP
+    for x in (S4, S8, A + 12):
+        assert L.nq_attn_prompt(A, 1536, A, 256, A, 256, x, x, 2, 9, 9, 6, 1, 256, 0.1, 0, A, x, None) == HIP
+        assert L.nq_kv_append(1, A, 256, A, 256, x, x, x, 8, x, x, 2, 5, 1, 256, 64, 9, A, A, None) == HIP
+        assert L.nq_attn_tree(1, A, 1536, A, A, x, x, x, 8, x, x, S8, 2, 4, 6, 6, 1, 256, 64, 9, 100, 0.1, 1, A, x, None, 0,
+                              None) == HIP
+        assert L.nq_kv_reserve(x, 9, x, 8, x, x, 2, 16, x, x, None) == HIP
+        assert L.nq_kv_release(x, 9, x, 8, x, 2, 16, None) == HIP
+        assert L.nq_kv_fork(x, 9, x, 8, x, 2, x, 3, 16, x, x, x, x, None) == HIP
+        assert L.nq_kv_copy_pages(A, 2, 9 * 4096, 4096, 9, x, 3, None) == HIP
+        assert L.nq_kv_compact(A, 2, 9 * 16 * 512, 1, 16, 512, 9, x, 8, x, x, x, 2, 4, None) == HIP
+    assert L.nq_attn_tree(1, A, 1536, A, A, A, A, A, 8, A, A, S4, 2, 4, 6, 6, 1, 256, 64, 9, 100, 0.1, 1, A, A, None, 0,
+                          None) == nq.NQ_ERR_ALIGN

@@ -543,3 +543,45 @@ def test_step_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
         assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("hkv", [1, 2, 3])
+def test_e4m3_step_with_slices_of_longer_arrays(hkv, n):
+    """Scales as rows of one tensor, lengths, offsets, tables and masks as parts of longer ones: the step's keys and
+    values appended, then its attention."""
+    d, page, lens, drafts = 64, 16, [37, 5], [n, 3]
+    cache, masks = Cache(lens, drafts, hkv, d, page, True, 80 + hkv, width=13), trees(drafts, 81)
+    q, t = randn((n + 3, 2 * hkv, d), 82), n + 3
+    ref = tree_oracle(q, cache, lens, drafts, masks, 0.125)
+    new = [torch.cat([x[b][lens[b]:] for b in range(2)]).float() for x in (cache.k, cache.v)]
+    scales = torch.stack([cache.ks, cache.vs]).to(DEV)
+    kp, vp, _, _, rows = cache.to_gpu()
+    for pool in (kp, vp):       # the drafted tokens' places start empty
+        for b in range(2):
+            for i in range(lens[b], lens[b] + drafts[b]):
+                pool[int(rows[b, i // page]), :, i % page] = 0
+    table = torch.full((3, 13), -1, dtype=torch.int32, device=DEV)
+    table[1:] = rows
+    ln = torch.tensor([9] + lens, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([9, 0, n, t], dtype=torch.int32, device=DEV)
+    mk = torch.cat([torch.zeros(1, dtype=torch.int64), mask_tensor(masks)]).to(DEV)
+    lse = torch.full((t * 2 * hkv + 1,), 7.0, device=DEV)
+    o = torch.full(q.shape, 7.0, device=DEV)
+    # appended as the codes' own values (exact in BF16) under scales of one, so that the codes are those of the cache
+    k, v = ((x / s.cpu()[:, None]).to(torch.float8_e4m3fn) for x, s in zip(new, scales))
+    one = torch.ones((2, hkv), device=DEV)
+    nq.nq_kv_append(nq.NQ_KV_E4M3, k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), one[0], one[1], table[1:], ln[1:],
+                    cu[1:], kp, vp)
+    nq.nq_attn_tree(nq.NQ_KV_E4M3, q.to(DEV), kp, vp, scales[0], scales[1], table[1:], ln[1:], cu[1:], mk[1:], n if n > 3 else 3,
+                    lens[0] + n, 0.125, o, lse[1:])
+    check(o, lse[1:].view(t, 2 * hkv), *ref, torch.float32)
+    assert lse[0] == 7
+
+
+def test_prompt_offsets_as_parts_of_longer_arrays():
+    q, k, v = randn((40, 2, 64), 83), randn((50, 1, 64), 84), randn((50, 1, 64), 85)
+    cu = torch.tensor([3, 0, 10, 40, 5, 0, 20, 50], dtype=torch.int32, device=DEV)
+    o, lse = torch.zeros((40, 2, 64), device=DEV), torch.zeros(81, device=DEV)
+    nq.nq_attn_prompt(q.to(DEV), k.to(DEV), v.to(DEV), cu[1:4], cu[5:], 0.125, o, lse[1:])
+    check(o, lse[1:].view(40, 2), *prompt_oracle(q, k, v, [10, 30], [20, 30], 0.125), torch.float32)

@@ -220,3 +220,35 @@ def test_compact(dtype, hkv, page, d):
         cu.append(cu[-1] + len(p))
     nq.nq_kv_compact(pool, table, i32(lens), i32(sum(paths, [])), i32(cu))
     assert torch.equal(pool, ref)
+
+
+def test_slices_of_longer_arrays():
+    """Accounting and moves on parts of a table of width 13, of lengths and of lists: no 16-byte boundary anywhere."""
+    page, width, pages = 16, 13, 60
+    m = Model(pages, 3, width, page)
+    refs = torch.zeros(pages + 1, dtype=torch.int32, device=DEV)[1:]
+    whole = torch.full((6, width), -1, dtype=torch.int32, device=DEV)
+    lens, new = i32([99, 0, 0, 0]), i32([99, 40, 7, 64])
+    free, short = torch.empty(pages + 1, dtype=torch.int32, device=DEV)[1:], i32([5, -7])[1:]
+    nq.nq_kv_reserve(refs, whole[1:4], lens[1:], new[1:], page, free, short)
+    assert m.reserve([0, 0, 0], [40, 7, 64]) == int(short)
+    assert whole[1:4].tolist() == m.table and refs.tolist() == m.refs
+    parents, copies = i32([9, 0, 2])[1:], torch.full((5,), 7, dtype=torch.int32, device=DEV)[1:]
+    nq.nq_kv_fork(refs, whole[1:4], new[1:], parents, page, whole[4:6], copies, free, short)
+    child, pairs, missing = m.fork([40, 7, 64], [0, 2])
+    assert whole[4:6].tolist() == child and copies.view(2, 2).tolist() == pairs and int(short) == missing
+    assert refs.tolist() == m.refs and (whole[0] == -1).all()
+    pool = torch.randint(0, 255, (2, pages, 1, page, 64), device=DEV).to(torch.uint8)
+    ref = pool.clone()
+    ref[:, pairs[0][1]] = ref[:, pairs[0][0]]
+    nq.nq_kv_copy_pages(pool, copies)
+    assert torch.equal(pool, ref)
+    at = lambda b, i: (int(whole[1 + b, i // page]), i % page)  # noqa: E731
+    for b, i, a in ((0, 1, 3), (2, 0, 2), (2, 1, 5)):
+        (pd, sd), (ps, ss) = at(b, i + [30, 1, 50][b]), at(b, a + [30, 1, 50][b])
+        ref[:, pd, :, sd] = ref[:, ps, :, ss].clone()
+    nq.nq_kv_compact(pool, whole[1:4], i32([0, 30, 1, 50])[1:], i32([0, 0, 3, 2, 5])[1:], i32([0, 0, 2, 2, 4])[1:])
+    assert torch.equal(pool, ref)
+    nq.nq_kv_release(refs, whole[4:6], i32([4, 0, 0])[1:], page)
+    m.release(child, [0, 0])
+    assert refs.tolist() == m.refs and (whole[4:6] == -1).all()
