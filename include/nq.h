@@ -513,7 +513,10 @@ nq_status nq_kv_append(int kv_fmt, const uint16_t* k, int64_t k_stride, const ui
  *   workspace, workspace_bytes   optional (nq_attn_tree_workspace_bytes): lets
  *            a sequence's keys be split over workgroups.  It needs no
  *            preparation and holds nothing between calls; calls that share it
- *            must be ordered (the same stream)
+ *            must be ordered (the same stream).  The size for the largest B,
+ *            max_q and max_len serves every smaller call with the same heads;
+ *            of a smaller workspace a call uses what there is, with fewer
+ *            and longer parts
  * The result does not depend on timing: parts are joined in the order of
  * their keys.
  */

@@ -419,13 +419,16 @@ struct TreePlan {
     int64_t bytes;
 };
 
+// Workspace of one range: the results and sums of every row.
+int64_t range_bytes(int64_t max_q, int64_t hq, int64_t d) { return max_q * hq * (d * 4 + 8); }
+
 // Ranges of 128 keys (four waves of 32) or, with more rows and so more to
 // write for each part, 256, and up.  Few sequences: as many
 // workgroups as run at once.  Many: about four times as many, short enough
 // that the last ones to run do not leave most CUs idle.
-TreePlan tree_plan(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
+TreePlan tree_plan(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len, int64_t cus) {
     const int64_t rows = max_q * (hq / hkv), tile = attn::tile_rows(rows), tiles = (rows + tile - 1) / tile;
-    const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles, cus = device_cu_count();
+    const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles;
     TreePlan p{0, (int)least, rows <= 32 ? 128 : 32, (int)tiles, 0};
     // Short contexts: one range a sequence and one launch.  (701 keys of 24 / 4
     // heads of 256: 10 + 5 us of kernels and two launches, or 16 us and one;
@@ -437,14 +440,22 @@ TreePlan tree_plan(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t
     if (want > most) want = most;
     if (want < 1) want = 1;
     p.want = (int)want;
-    p.bytes = (want + seqs) * hkv * rows * (d * 4 + 8) + seqs * 8;
+    p.bytes = (want + seqs) * range_bytes(max_q, hq, d) + seqs * 8;
     return p;
 }
 
 }  // namespace
 
+// What any call up to these sizes needs: fewer drafts may need more, since they
+// have fewer row tiles and are split further.
 int64_t attn_tree_workspace_bytes(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len) {
-    return tree_plan(seqs, max_q, hq, hkv, d, max_len).bytes;
+    const int64_t cus = device_cu_count();
+    int64_t most = 0;
+    for (int64_t q = 1; q <= max_q; ++q) {
+        const int64_t bytes = tree_plan(seqs, q, hq, hkv, d, max_len, cus).bytes;
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
@@ -454,8 +465,11 @@ hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const
                             int64_t max_len, float scale, bool bf16_out, void* o, float* lse, void* workspace,
                             int64_t workspace_bytes, hipStream_t stream) {
     using namespace attn;
-    TreePlan p = tree_plan(seqs, max_q, hq, hkv, d, max_len);
-    if (workspace_bytes < p.bytes) p.want = 0;
+    TreePlan p = tree_plan(seqs, max_q, hq, hkv, d, max_len, device_cu_count());
+    if (workspace_bytes < p.bytes) {        // as many ranges as fit, each sequence's last one beside them
+        const int64_t fit = (workspace_bytes - seqs * 8) / range_bytes(max_q, hq, d) - seqs;
+        p.want = fit > 0 ? (int)fit : 0;
+    }
     const TreeArgs a{q, q_stride, k_pages, v_pages, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, table, (int)width, lens,
                      cu_q, masks, (int)seqs, (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size),
                      pages, scale, o, lse, reinterpret_cast<float*>(workspace), p.want, p.least, p.step, p.row_tiles};

@@ -152,3 +152,21 @@ def test_small_arrays_need_no_more_than_their_elements_alignment(L):
         assert L.nq_kv_compact(A, 2, 9 * 16 * 512, 1, 16, 512, 9, x, 8, x, x, x, 2, 4, None) == HIP
     assert L.nq_attn_tree(1, A, 1536, A, A, A, A, A, 8, A, A, S4, 2, 4, 6, 6, 1, 256, 64, 9, 100, 0.1, 1, A, A, None, 0,
                           None) == nq.NQ_ERR_ALIGN
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(24, 4, 256), (32, 8, 128), (40, 8, 128), (8, 1, 256), (14, 2, 64), (20, 20, 64), (128, 1, 64)])
+def test_tree_workspace_of_the_largest_call_serves_smaller_ones(L, hq, hkv, d):
+    """The size never falls as the batch, the drafted tokens or the length grow."""
+    size = lambda b, q, n: L.nq_attn_tree_workspace_bytes(b, q, hq, hkv, d, n)  # noqa: E731
+    batches, lengths = (1, 2, 5, 16, 31, 32, 33, 64, 65, 129, 300), (0, 700, 769, 3000, 32768, 131000, 1 << 20)
+    for n in lengths:
+        for b in batches:
+            sizes = [size(b, q, n) for q in range(1, 65)]
+            assert sizes == sorted(sizes)
+    for q in (1, 4, 17, 33, 64):
+        for n in lengths:
+            sizes = [size(b, q, n) for b in batches]
+            assert sizes == sorted(sizes)
+        for b in batches:
+            sizes = [size(b, q, n) for n in lengths]
+            assert sizes == sorted(sizes)

@@ -585,3 +585,27 @@ def test_prompt_offsets_as_parts_of_longer_arrays():
     o, lse = torch.zeros((40, 2, 64), device=DEV), torch.zeros(81, device=DEV)
     nq.nq_attn_prompt(q.to(DEV), k.to(DEV), v.to(DEV), cu[1:4], cu[5:], 0.125, o, lse[1:])
     check(o, lse[1:].view(40, 2), *prompt_oracle(q, k, v, [10, 30], [20, 30], 0.125), torch.float32)
+
+
+@pytest.mark.parametrize("hq,hkv,d,step,largest", [(24, 4, 256, 21, 33), (8, 1, 64, 16, 17), (4, 1, 128, 3, 3)])
+def test_tree_workspace_of_other_sizes(hq, hkv, d, step, largest):
+    """A step on the largest step's workspace, and on smaller ones: the keys are split as far as it goes, nothing past
+    its end is written, and the result is the same up to rounding."""
+    lens = [5003, 900]
+    cache, masks = Cache(lens, [step, 2], hkv, d, 32, False, 86), trees([step, 2], 87)
+    q = randn((step + 2, hq, d), 88)
+    ref = tree_oracle(q, cache, lens, [step, 2], masks, 1 / math.sqrt(d))
+    kp, vp, _, _, table = cache.to_gpu()
+    ln, cu, mk = torch.tensor(lens, dtype=torch.int32, device=DEV), cu_of([step, 2]).to(DEV), mask_tensor(masks).to(DEV)
+    whole = nq.nq_attn_tree_workspace_bytes(2, largest, hq, hkv, d, 5100)
+    one = step * hq * (d * 4 + 8)                   # a range's results and sums
+    buffer = torch.empty(whole + 4096, dtype=torch.uint8, device=DEV)
+    for size, used in ((whole, True), (whole // 3, True), (5 * one + 16, True), (3 * one + 16, True), (3 * one + 15, False), (16, False),
+                       (1, False)):
+        buffer.fill_(255)
+        o, lse = torch.full(q.shape, 7.0, device=DEV), torch.full(q.shape[:2], 7.0, device=DEV)
+        nq.nq_attn_tree(nq.NQ_KV_BF16, q.to(DEV), kp, vp, None, None, table, ln, cu, mk, step, 5100, 1 / math.sqrt(d), o, lse,
+                        buffer[:size])
+        check(o, lse, *ref, torch.float32)
+        assert bool((buffer[:size] != 255).any()) == used, size
+        assert (buffer[size:] == 255).all()
