@@ -10,13 +10,16 @@
 // operands give them, so V^T is read in the order that S^T's rows come in.
 // V^T comes out of the row-major V tile through the LDS's transposing reads.
 //
-//   x_j = c <q, k_j> (c = scale log2 e),  p_j = 2^(x_j - m),  l = sum p_j,
-//   o = sum p_j v_j / l,  log-sum-exp = (m + log2 l) ln 2
+//   x_j = c <q, k_j> (c = scale log2 e),  p_j = 2^(x_j - r),  l = sum p_j,
+//   o = sum p_j v_j / l,  log-sum-exp = (r + log2 l) ln 2
 //
-// m is a running reference, not the exact maximum: it moves only when a logit
-// passes it by more than RESCALE_LOG2 (p then stays below 2^RESCALE_LOG2, far
-// inside FP32's and BF16's range, and every rounding is relative), so the
-// accumulators are rescaled a few times per row and not once per tile.  Sums, m and l are FP32.  P is rounded once to BF16 (2^-8
+// r = m + RESCALE_LOG2, where m is a running reference, not the exact maximum:
+// it moves only when a logit passes it by more than RESCALE_LOG2, so the
+// accumulators are rescaled a few times per row and not once per tile.  No
+// weight is above 1 (sums of p v stay finite where those of a softmax under the
+// exact maximum do), the largest is at least 2^-RESCALE_LOG2, and every
+// rounding is relative (of values below 2^-118 in size, products may lose bits
+// to FP32's smallest numbers).  Sums, m and l are FP32.  P is rounded once to BF16 (2^-9
 // relative at most, as a BF16 output is); for FP32 outputs SPLITP makes it
 // three BF16 terms (2^-22), for three products with V instead of one.
 #pragma once
@@ -181,7 +184,7 @@ struct Rows {
 
     v8bf q[NS];
     v16f o[ND];
-    float m, l;                                         // reference (unscaled logit units), this lane's half of the sum
+    float m, l;                                         // reference m (unscaled logit units), this lane's half of the sum
     float c;                                            // scale log2 e, made positive
     uint32_t q_and, q_xor;                              // what that makes of the queries' bits
     int ka, va;                                         // byte offsets of this lane's first read in a K and a V tile
@@ -299,6 +302,9 @@ struct Rows {
         for (int i = 0; i < 16; ++i) s[i] = (w >> (8 * (i >> 2) + (i & 3))) & 1u ? s[i] : -INFINITY;
     }
 
+    // r, in log2 units.
+    __device__ __forceinline__ float reference() const { return m * c + RESCALE_LOG2; }
+
     // P^T of the 32 keys at k, with m, l and o brought along.
     template <bool HIDE>
     __device__ __forceinline__ void weights(lds_cptr k, uint64_t seen, v16f& s) {
@@ -318,11 +324,11 @@ struct Rows {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= a;
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
+        const float r = m == -INFINITY ? 0.f : reference();
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
+            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -r));
             sum += s[i];
         }
         l += sum;
@@ -424,8 +430,8 @@ __device__ __forceinline__ void store4(void* out, int64_t at, float a, float b, 
 
 // 1 / sum, or 0 for a row that saw nothing (its outputs are zeros); a NaN sum stays NaN.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
-__device__ __forceinline__ float log_sum_exp(float mc, float l) {
-    return l == 0.f ? -INFINITY : (mc + __builtin_log2f(l)) * LN2;
+__device__ __forceinline__ float log_sum_exp(float r, float l) {
+    return l == 0.f ? -INFINITY : (r + __builtin_log2f(l)) * LN2;
 }
 
 }  // namespace attn

@@ -26,7 +26,7 @@ struct KeysLds {
 };
 
 // Source, Sees and Queries as for attend_rows (keys from key1 on are outside
-// the source's descriptors).  emit(row, column, x, mc, l): four neighbouring
+// the source's descriptors).  emit(row, column, x, r, l): four neighbouring
 // columns of a row's sum of p v, its reference in log2 units and its sum of p;
 // once for each of the first `rows` rows and every fourth column.
 template <int D, bool FP8, bool SPLITP, class Source, class Sees, class Queries, class Emit>
@@ -97,7 +97,7 @@ __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned ch
             *reinterpret_cast<v4f*>(at + R.column(d, e)) =
                 v4f{R.o[d][4 * e], R.o[d][4 * e + 1], R.o[d][4 * e + 2], R.o[d][4 * e + 3]};
     if (lane < 32) {
-        at[D] = R.m == -INFINITY ? -INFINITY : R.m * R.c;
+        at[D] = R.m == -INFINITY ? -INFINITY : R.reference();
         at[D + 1] = l;
     }
     __syncthreads();

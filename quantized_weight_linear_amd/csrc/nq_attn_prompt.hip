@@ -152,11 +152,11 @@ __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     const int keys = t.last + ahead > 0 ? t.last + ahead : 0;
     const PackedRows src = packed_rows<D>(a, t, head / (a.hq / a.hkv), keys);
     auto queries = [&] { R.load_q(row < t.nq ? a.q + (t.q0 + row) * a.qs + head * D : nullptr); };
-    auto emit = [&](int i, int col, const v4f& x, float mc, float l) {
+    auto emit = [&](int i, int col, const v4f& x, float ref, float l) {
         const int64_t out = (t.q0 + t.first + i) * a.hq + head;
         const float f = inverse_sum(l);
         store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
-        if (col == 0 && a.lse) a.lse[out] = log_sum_exp(mc, l);
+        if (col == 0 && a.lse) a.lse[out] = log_sum_exp(ref, l);
     };
     attend_keys(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
 }
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_pro
         for (int e = 0; e < 4; ++e)
             store4<BF16OUT>(a.o, out * D + R.column(d, e), R.o[d][4 * e] * inv, R.o[d][4 * e + 1] * inv,
                             R.o[d][4 * e + 2] * inv, R.o[d][4 * e + 3] * inv);
-    if (a.lse && lane < 32) a.lse[out] = log_sum_exp(l == 0.f ? 0.f : R.m * R.c, l);
+    if (a.lse && lane < 32) a.lse[out] = log_sum_exp(l == 0.f ? 0.f : R.reference(), l);
 }
 
 // Tiles of bm rows at most: every sequence may end in a part of one.

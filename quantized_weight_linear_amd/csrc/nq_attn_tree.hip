@@ -38,7 +38,7 @@ struct TreeArgs {
     float scale;
     void* o;
     float* lse;
-    float* parts;                   // parts' outputs, then their (m c, l) pairs, then each sequence's (first part, parts)
+    float* parts;                   // parts' outputs, then their (r, l) pairs, then each sequence's (first part, parts)
     int want;                       // ranges to split all sequences' keys into, about (0: one a sequence)
     int least, step;                // keys of a range: at least, and a multiple of
     int row_tiles;
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tre
     const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
     auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
     attend_rows(R, (lds_ptr)smem, r.key0, r.key1, src, sees, queries, wave, lane);
-    const float l = halves_sum(R.l), mc = R.m == -INFINITY ? 0.f : R.m * R.c;
+    const float l = halves_sum(R.l), ref = R.m == -INFINITY ? 0.f : R.reference();
     if (row >= s.n * a.group) return;
     const bool only = r.parts == 1;
     const int64_t out = tree_out(a, s, kvh, row), part = part_row(a, range, kvh, row);
@@ -256,8 +256,8 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tre
             else store4<false>(a.parts, part * D + R.column(d, e), x0, x1, x2, x3);
         }
     if (lane < 32) {
-        if (!only) part_sums(a, D)[part] = make_float2(mc, l);
-        else if (a.lse) a.lse[out] = log_sum_exp(mc, l);
+        if (!only) part_sums(a, D)[part] = make_float2(ref, l);
+        else if (a.lse) a.lse[out] = log_sum_exp(ref, l);
     }
 }
 
@@ -281,16 +281,16 @@ __global__ __launch_bounds__(256) void attn_tree_keys_kernel(TreeArgs a) {
     auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
     const bool only = r.parts == 1;
     const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
-    auto emit = [&](int i, int col, const v4f& x, float mc, float l) {
+    auto emit = [&](int i, int col, const v4f& x, float ref, float l) {
         const int64_t out = tree_out(a, s, kvh, i);
         if (only) {
             const float f = inverse_sum(l) * vs;
             store4<BF16OUT>(a.o, out * D + col, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
-            if (col == 0 && a.lse) a.lse[out] = log_sum_exp(mc, l);
+            if (col == 0 && a.lse) a.lse[out] = log_sum_exp(ref, l);
         } else {
             const int64_t part = part_row(a, range, kvh, i);
             store4<false>(a.parts, part * D + col, x[0], x[1], x[2], x[3]);
-            if (col == 0) part_sums(a, D)[part] = make_float2(mc, l);
+            if (col == 0) part_sums(a, D)[part] = make_float2(ref, l);
         }
     };
     attend_keys(R, smem, r.key0, r.key1, s.n * a.group, src, sees, queries, emit, wave, lane);

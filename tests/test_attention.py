@@ -609,3 +609,42 @@ def test_tree_workspace_of_other_sizes(hq, hkv, d, step, largest):
         check(o, lse, *ref, torch.float32)
         assert bool((buffer[:size] != 255).any()) == used, size
         assert (buffer[size:] == 255).all()
+
+
+# ---------------------------------------------------------------------------
+# large values, and rows without a finite logit
+# ---------------------------------------------------------------------------
+
+def rising(n, hq, hkv, d, late, top):
+    """Rows whose logits (scale 1) are 0 but for some late keys at `top`, natural units, with values near 1e37."""
+    q, k = torch.zeros((n, hq, d)), torch.zeros((n, hkv, d))
+    q[:, :, 0] = 1.0
+    for j in late:
+        k[j, :, 0] = top
+    v = (1.0 + torch.rand((n, hkv, d), generator=gen(90))) * 1e37
+    return q.to(torch.bfloat16), k.to(torch.bfloat16), v.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,d", [(4, 64), (4, 256), (132, 64), (68, 256)])        # few tiles, and many
+def test_prompt_large_values_under_rising_logits(hq, d, out):
+    """A key far above the first ones: the sum of weights times values stays finite where the result is."""
+    n = 150
+    q, k, v = rising(n, hq, 2, d, [133], 5.0)
+    o, lse = run_prompt(q, k, v, [n], [n], 1.0, out)
+    check(o, lse, *prompt_oracle(q, k, v, [n], [n], 1.0), out)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("drafts,d", [(2, 256), (40, 128)])
+def test_tree_large_values_under_rising_logits(drafts, d, split, out):
+    lens = [1500]
+    cache, masks = Cache(lens, [drafts], 1, d, 16, False, 91), trees([drafts], 92)
+    q, k, v = rising(1500 + drafts, 2, 1, d, [133, 700, 1400], 5.0)
+    for i in range(1500 + drafts):
+        p = int(cache.table[0, i // 16])
+        cache.kp[p, :, i % 16], cache.vp[p, :, i % 16] = k[i], v[i]
+    cache.k, cache.v = [k.double()], [v.double()]
+    o, lse = run_tree(q[:drafts], cache, lens, [drafts], masks, 1.0, out, split)
+    check(o, lse, *tree_oracle(q[:drafts], cache, lens, [drafts], masks, 1.0), out)
