@@ -380,8 +380,9 @@ struct Rows {
 
     // Values that are not finite, of keys that some rows do not see: a product
     // over 16 keys would give 0 x infinity = NaN there.  They are added to the
-    // rows that see them (a weight is positive, so the sum is infinite or NaN
-    // by them whatever it is), and then count as zeros in the products.
+    // rows that see them (a positive weight makes the sum infinite or NaN by
+    // them whatever it is; one of 0, under a logit far below the others or of
+    // -infinity, is not told apart), and then count as zeros in the products.
     // bad: the keys of the 32 at v that hold such values; seen: as in hide().
     __device__ __forceinline__ void add_not_finite(lds_cptr v, uint32_t bad, uint64_t seen) {
         while (bad) {
@@ -412,6 +413,16 @@ struct Rows {
             x[0] = bf16_bits_to_f32(w[0] & 0xFFFFu), x[1] = bf16_bits_to_f32(w[0] >> 16);
             x[2] = bf16_bits_to_f32(w[1] & 0xFFFFu), x[3] = bf16_bits_to_f32(w[1] >> 16);
         }
+    }
+
+    // A row without weights (sum 0): no outputs either, whatever its values
+    // were (0 x infinity, or a value added by add_not_finite).
+    __device__ __forceinline__ void drop_if_empty(float sum) {
+        if (sum != 0.f) return;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
     }
 
     // o[d][4 e + j] is this lane's output column 32 d + 8 e + 4 h + j.

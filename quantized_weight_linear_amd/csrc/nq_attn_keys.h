@@ -112,12 +112,12 @@ __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned ch
         for (int w = 0; w < KEY_WAVES; ++w) {
             const float* p = join + (w * 32 + i) * L::PITCH;
             const float lw = p[D + 1];
-            // a wave that saw nothing has neither sum nor outputs
+            // a wave without weights has neither sum nor outputs (which may be infinity or NaN there)
             const float f = lw == 0.f ? 0.f : __builtin_amdgcn_exp2f(p[D] == -INFINITY ? 0.f : p[D] - top);
             const v4f y = *reinterpret_cast<const v4f*>(p + col);
             sum += lw * f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] += y[j] * f;
+            for (int j = 0; j < 4; ++j) x[j] += lw == 0.f ? 0.f : y[j] * f;
         }
         emit(i, col, x, top == -INFINITY ? 0.f : top, sum);
     }

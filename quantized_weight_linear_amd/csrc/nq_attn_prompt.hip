@@ -181,6 +181,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_pro
     auto queries = [&] { R.load_q(row < t.nq ? a.q + (t.q0 + row) * a.qs + head * D : nullptr); };
     attend_rows(R, (lds_ptr)smem, 0, t.last + ahead, src, sees, queries, wave, lane);
     const float l = halves_sum(R.l), inv = inverse_sum(l);
+    R.drop_if_empty(l);
     if (row >= t.nq) return;
     const int64_t out = (t.q0 + row) * a.hq + head;
 #pragma unroll

@@ -243,6 +243,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tre
     auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
     attend_rows(R, (lds_ptr)smem, r.key0, r.key1, src, sees, queries, wave, lane);
     const float l = halves_sum(R.l), ref = R.m == -INFINITY ? 0.f : R.reference();
+    R.drop_if_empty(l);
     if (row >= s.n * a.group) return;
     const bool only = r.parts == 1;
     const int64_t out = tree_out(a, s, kvh, row), part = part_row(a, range, kvh, row);

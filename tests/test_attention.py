@@ -648,3 +648,33 @@ def test_tree_large_values_under_rising_logits(drafts, d, split, out):
     cache.k, cache.v = [k.double()], [v.double()]
     o, lse = run_tree(q[:drafts], cache, lens, [drafts], masks, 1.0, out, split)
     check(o, lse, *tree_oracle(q[:drafts], cache, lens, [drafts], masks, 1.0), out)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,d,n", [(2, 64, 40), (2, 256, 70), (132, 128, 150)])     # few tiles, and many
+def test_prompt_rows_of_infinite_negative_logits(hq, d, n, out):
+    """Every logit of the first rows is -infinity: zeros and -infinity, whatever the values hold."""
+    q, k, v = randn((n, hq, d), 93).abs() + 0.01, randn((n, 1, d), 94), randn((n, 1, d), 95)
+    at = n - 5
+    k[:at] = -float("inf")
+    ro, rl = prompt_oracle(q, k[at:], v[at:], [n], [n - at], 0.1)      # as if these keys were not there
+    v[2, 0, 1], v[33, 0, 5], v[at - 3] = float("inf"), float("nan"), -float("inf")
+    o, lse = run_prompt(q, k, v, [n], [n], 0.1, out)
+    check(o[:at], lse[:at], ro[:at], rl[:at], out)
+
+
+@pytest.mark.parametrize("drafts,d", [(2, 256), (40, 64)])
+@pytest.mark.parametrize("len_", [20, 1500])
+def test_tree_rows_of_infinite_negative_logits(len_, drafts, d):
+    cache = Cache([len_], [drafts], 1, d, 16, False, 96)
+    masks = [[0] * drafts]
+    q = randn((drafts, 2, d), 97).abs() + 0.01
+    bad = torch.isnan(cache.kp.float())
+    cache.kp[:] = -float("inf")
+    cache.vp[bad] = float("nan")
+    p = int(cache.table[0, 0])
+    cache.vp[p, 0, 3, 1], cache.vp[p, 0, 7] = float("inf"), float("nan")
+    for out in (torch.float32, torch.bfloat16):
+        o, lse = run_tree(q, cache, [len_], [drafts], masks, 0.1, out)
+        torch.cuda.synchronize()
+        assert (o == 0).all() and (lse == -math.inf).all()
