@@ -464,7 +464,8 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
  * before it too; with n_q > n_k the first rows see nothing).
  *   q [Tq][Hq][D], k / v [Tk][Hkv][D], cu_q / cu_k [B + 1]
  * Query rows outside every sequence are not written.
- * Errors: D, Hq % Hkv, strides -> NQ_ERR_SHAPE.
+ * Errors: D, Hq % Hkv, strides, B, Tq or Tk above 2^31 - 1024, more than
+ * 2^24 workgroups ((Tq / 64 + min(B, Tq)) Hq) -> NQ_ERR_SHAPE.
  */
 nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
                          const uint16_t* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,

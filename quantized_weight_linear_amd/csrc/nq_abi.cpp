@@ -593,6 +593,7 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
 namespace {
 
 constexpr int64_t I31 = (int64_t)1 << 31;
+constexpr int64_t MOST_ROWS = I31 - 1024;                // tiles and searches that reach past the last row stay in 32 bits
 constexpr int64_t MOST_BLOCKS = (int64_t)1 << 24;       // 256 threads each: below 2^32 threads a launch
 
 bool heads_ok(int64_t Hq, int64_t Hkv, int64_t D) {
@@ -628,7 +629,7 @@ extern "C" {
 nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                          int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk,
                          int64_t Hq, int64_t Hkv, int64_t D, float scale, int out_dt, void* o, float* lse, void* stream) {
-    if (B < 0 || Tq < 0 || Tk < 0 || B >= I31 || Tq >= I31 || Tk >= I31 || !heads_ok(Hq, Hkv, D)) return NQ_ERR_SHAPE;
+    if (B < 0 || Tq < 0 || Tk < 0 || B > MOST_ROWS || Tq > MOST_ROWS || Tk > MOST_ROWS || !heads_ok(Hq, Hkv, D)) return NQ_ERR_SHAPE;
     if (!stride_ok(q_stride, Hq, D) || !stride_ok(k_stride, Hkv, D) || !stride_ok(v_stride, Hkv, D)) return NQ_ERR_SHAPE;
     if ((Tq / 64 + (B < Tq ? B : Tq)) * Hq >= MOST_BLOCKS) return NQ_ERR_SHAPE;
     if (!out_ok(out_dt)) return NQ_ERR_FORMAT;

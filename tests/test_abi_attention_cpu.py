@@ -170,3 +170,12 @@ def test_tree_workspace_of_the_largest_call_serves_smaller_ones(L, hq, hkv, d):
         for b in batches:
             sizes = [size(b, q, n) for n in lengths]
             assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("name", ["B", "Tq", "Tk"])
+def test_prompt_sizes_near_32_bits(L, name):
+    """Sizes whose last tile, or last look through the sequences, would pass 32 bits."""
+    good = dict(q=A, qs=64, k=A, ks=64, v=A, vs=64, cu_q=A, cu_k=A, B=1, Tq=1, Tk=1, Hq=1, Hkv=1, D=64, scale=0.1, out=0, o=A, lse=None,
+                stream=None)
+    for n in ((1 << 31) - 1, (1 << 31) - 1023):
+        assert L.nq_attn_prompt(*dict(good, **{name: n}).values()) == nq.NQ_ERR_SHAPE
