@@ -431,6 +431,7 @@ TreePlan tree_plan(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t
     const int64_t rows = max_q * (hq / hkv), tile = attn::tile_rows(rows), tiles = (rows + tile - 1) / tile;
     const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles;
     TreePlan p{0, (int)least, rows <= 32 ? 128 : 32, (int)tiles, 0};
+    if (max_len > (int64_t)1 << 30) max_len = (int64_t)1 << 30;          // the most that a table holds
     // Short contexts: one range a sequence and one launch.  (701 keys of 24 / 4
     // heads of 256: 10 + 5 us of kernels and two launches, or 16 us and one;
     // 19.2 and 17.9 us a step, the cache's append included.)

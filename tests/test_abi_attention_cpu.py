@@ -179,3 +179,12 @@ def test_prompt_sizes_near_32_bits(L, name):
                 stream=None)
     for n in ((1 << 31) - 1, (1 << 31) - 1023):
         assert L.nq_attn_prompt(*dict(good, **{name: n}).values()) == nq.NQ_ERR_SHAPE
+
+
+@pytest.mark.parametrize("b", [1, 5, 300, 100000])
+def test_tree_lengths_beyond_all_tables(L, b):
+    """A length above what a table can hold (2^30 tokens) asks for the workspace of that, not for less."""
+    top = L.nq_attn_tree_workspace_bytes(b, 4, 24, 4, 256, 1 << 30)
+    assert top > 0
+    for n in ((1 << 30) + 1, 1 << 40, 1 << 57, 1 << 62, (1 << 63) - 1):
+        assert L.nq_attn_tree_workspace_bytes(b, 4, 24, 4, 256, n) == top
