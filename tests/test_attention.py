@@ -678,3 +678,61 @@ def test_tree_rows_of_infinite_negative_logits(len_, drafts, d):
         o, lse = run_tree(q, cache, [len_], [drafts], masks, 0.1, out)
         torch.cuda.synchronize()
         assert (o == 0).all() and (lse == -math.inf).all()
+
+
+# ---------------------------------------------------------------------------
+# many sequences, many parts
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("seqs", [300, 600])
+def test_prompt_sequences_past_one_look(seqs):
+    """More sequences than a wave takes in at once (256), empty ones around the boundary."""
+    g = gen(100)
+    ns = torch.randint(1, 20, (seqs,), generator=g).tolist()
+    for i in (0, 254, 255, 256, 257, seqs - 1):
+        ns[i] = 0
+    ns[258] = 200
+    ms = [n + int(e) for n, e in zip(ns, torch.randint(0, 3, (seqs,), generator=g))]
+    q, k, v = randn((sum(ns), 2, 64), 101), randn((sum(ms), 1, 64), 102), randn((sum(ms), 1, 64), 103)
+    o, lse = run_prompt(q, k, v, ns, ms, 0.125, torch.float32)
+    check(o, lse, *prompt_oracle(q, k, v, ns, ms, 0.125), torch.float32)
+
+
+@pytest.mark.parametrize("seqs", [300, 600])
+def test_prompt_few_tokens_of_many_sequences(seqs):
+    """Few query tiles (their waves take different keys) spread over more than 256 sequences, most of them without queries."""
+    ns, ms = [0] * seqs, [70] * seqs
+    for i in (0, 3, 254, 256, 257, 299, seqs - 1):
+        ns[i] = 1 + i % 40
+    q, k, v = randn((sum(ns), 1, 64), 104), randn((sum(ms), 1, 64), 105), randn((sum(ms), 1, 64), 106)
+    o, lse = run_prompt(q, k, v, ns, ms, 0.125, torch.float32)
+    check(o, lse, *prompt_oracle(q, k, v, ns, ms, 0.125), torch.float32)
+
+
+@pytest.mark.parametrize("hq,hkv,d,most", [(4, 2, 64, 3), (40, 1, 64, 2), (8, 1, 128, 2)])
+@pytest.mark.parametrize("seqs", [70, 130])
+def test_tree_many_sequences_split(seqs, hq, hkv, d, most):
+    """More sequences than a wave has lanes, some without drafted tokens or without committed ones, a few long."""
+    g = gen(107)
+    lens = torch.randint(0, 200, (seqs,), generator=g).tolist()
+    drafts = torch.randint(0, most + 1, (seqs,), generator=g).tolist()
+    for i, n in ((0, 0), (3, 1900), (63, 900), (64, 0), (65, 1300), (seqs - 1, 1000)):
+        lens[i] = n
+    drafts[1], drafts[63], drafts[64], drafts[65], drafts[seqs - 1] = 0, most, most, 0, most
+    cache, masks = Cache(lens, drafts, hkv, d, 32, False, 108), trees(drafts, 109)
+    q = randn((sum(drafts), hq, d), 110)
+    assert nq.nq_attn_tree_workspace_bytes(seqs, most, hq, hkv, d, 1903) > 0
+    o, lse = run_tree(q, cache, lens, drafts, masks, 0.1, torch.float32)
+    check(o, lse, *tree_oracle(q, cache, lens, drafts, masks, 0.1), torch.float32)
+
+
+@pytest.mark.parametrize("hq,d,drafts,len_", [(2, 128, 2, 16300), (2, 128, 2, 17000), (3, 64, 1, 40000), (32, 64, 64, 9000),
+                                              (2, 128, 64, 17000)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_many_parts(fp8, hq, d, drafts, len_):
+    """Up to 128 parts of a sequence, joined by one wave a row (2048 rows) or four."""
+    cache, masks = Cache([len_], [drafts], 1, d, 64, fp8, 111), trees([drafts], 112)
+    q = randn((drafts, hq, d), 113)
+    for out in (torch.float32, torch.bfloat16):
+        o, lse = run_tree(q, cache, [len_], [drafts], masks, 1 / math.sqrt(d), out)
+        check(o, lse, *tree_oracle(q, cache, [len_], [drafts], masks, 1 / math.sqrt(d)), out)

@@ -252,3 +252,20 @@ def test_slices_of_longer_arrays():
     nq.nq_kv_release(refs, whole[4:6], i32([4, 0, 0])[1:], page)
     m.release(child, [0, 0])
     assert refs.tolist() == m.refs and (whole[4:6] == -1).all()
+
+
+@pytest.mark.parametrize("planes", [1, 5, 17, 33])
+def test_compact_planes(planes):
+    """Planes past a wave's, a workgroup's and a row of workgroups'."""
+    r = random.Random(planes)
+    lens, hkv, page, d, width = [5, 30, 0], 2, 16, 64, 8
+    paths = [sorted(r.sample(range(64), 20)), list(range(1, 64)), [2]]
+    table = torch.randperm(24, device=DEV).to(torch.int32).view(3, width).contiguous()
+    pool = torch.randint(0, 255, (planes, 24, hkv, page, d), device=DEV).to(torch.uint8)
+    ref, before = pool.clone(), pool.clone()
+    for b, path in enumerate(paths):
+        for i, a in enumerate(path):
+            src, dst = lens[b] + a, lens[b] + i
+            ref[:, int(table[b, dst // page]), :, dst % page] = before[:, int(table[b, src // page]), :, src % page]
+    nq.nq_kv_compact(pool, table, i32(lens), i32(sum(paths, [])), i32([0, 20, 83, 84]))
+    assert torch.equal(pool, ref)
