@@ -445,8 +445,9 @@ nq_status nq_linear_qbits_g64(int fmt, const uint16_t* x, int64_t T, const uint8
  *   - o [Tq][Hq][D] is FP32 or BF16 (out_dt); lse [Tq][Hq] FP32, or NULL:
  *     the natural logarithm of the sum of exp(logits) (it joins this result
  *     with attention over other keys).  A row that sees no key, or whose logits
- *     are all -infinity, gets o = 0 and lse = -infinity.  Keys and values that a row does not see do not touch
- *     its result, whatever they hold, infinities and NaN included.
+ *     are all -infinity, gets o = 0 and lse = -infinity.  Keys and values that a
+ *     row does not see do not touch its result, whatever they hold, infinities
+ *     and NaN included.
  *   - Logits, softmax statistics and sums are FP32.  The weights of the
  *     softmax are rounded to BF16 for a BF16 output, and to three BF16 terms
  *     (22 bits) for an FP32 output.
@@ -540,13 +541,17 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
  * reserve: entries lens[b] / page_size .. ceil(new_lens[b] / page_size) - 1 of
  *   row b that are negative get a page (count 1).  B at most 8192.
  * release: entries from ceil(keep_lens[b] / page_size) on are given back and
- *   become -1 (keep_lens[b] = 0: the whole row).
+ *   become -1 (keep_lens[b] = 0: the whole row).  A row cut back to the middle
+ *   of a page that others share still ends in that page, and its next tokens
+ *   would be written there for all of them: fork it at the shorter length
+ *   instead, and release the old row.
  * fork: child c becomes a copy of row parents[c] up to lens[parents[c]]
  *   tokens: whole pages are shared (counted), a last page that is partly
  *   filled is replaced by a page of the child's own, and copies[c] = (parent's
  *   page, child's page), or (-1, -1) where nothing is to be copied; the other
  *   entries become -1.  What the child's row held before is not given back.
- *   The child's rows may not overlap the parents'.
+ *   The child's rows may not overlap the parents'.  Without children nothing is
+ *   enqueued, and shortfall stays as it was.
  * copy_pages: page copies[i][0] to page copies[i][1] in each of `planes`
  *   planes, plane_bytes apart; pairs with a number outside [0, pages) are
  *   skipped.  No page may be written by one pair and named by another.

@@ -1,10 +1,11 @@
 // Attention tiles on the BF16 matrix cores, shared by the prompt and the tree
 // kernels.
 //
-// A wave holds 32 query rows as the columns of its products.  For 32 keys at a time it forms S^T = K Q^T, so that lane l has
-// the logits of query row l % 32 in its own registers (16 of the 32 keys, the
-// other half in lane l ^ 32): the reference and sum of the softmax are one
-// value per lane, and one exchange between the wave's halves joins the maxima.
+// A wave holds 32 query rows as the columns of its products.  For 32 keys at a
+// time it forms S^T = K Q^T, so that lane l has the logits of query row l % 32
+// in its own registers (16 of the 32 keys, the other half in lane l ^ 32): the
+// reference and sum of the softmax are one value per lane, and one exchange
+// between the wave's halves joins the maxima.
 // P^T, rounded to BF16 in those same registers, is already the right operand
 // of O^T += V^T P^T: the products sum over the keys in whatever order both
 // operands give them, so V^T is read in the order that S^T's rows come in.
@@ -19,9 +20,15 @@
 // weight is above 1 (sums of p v stay finite where those of a softmax under the
 // exact maximum do), the largest is at least 2^-RESCALE_LOG2, and every
 // rounding is relative (of values below 2^-118 in size, products may lose bits
-// to FP32's smallest numbers).  Sums, m and l are FP32.  P is rounded once to BF16 (2^-9
-// relative at most, as a BF16 output is); for FP32 outputs SPLITP makes it
-// three BF16 terms (2^-22), for three products with V instead of one.
+// to FP32's smallest numbers).  Sums, m and l are FP32.
+//
+// P's bits: one BF16 term for BF16 outputs, whose own rounding is as coarse
+// (2^-9 relative at most, each); l sums the weights as they were before it.
+// Against 64 bits the outputs of 16384 tokens of 24 heads of 256 are then
+// 2.0e-3 off (Frobenius), 1.5e-3 with the output's rounding alone.  For FP32
+// outputs SPLITP makes P three BF16 terms (2^-22: 2e-7 off), for three products
+// with V instead of one: 8192 tokens of 32 heads of 128 take 931 us so and 515
+// with one term.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -41,7 +48,8 @@ constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr int BUF_RAW = 0x00027000;      // raw buffer, no format conversion
 
-// Arrays of the call that no kernel of it writes, read at uniform places: by
+// Arrays that the kernel reading them does not write (an earlier one may have:
+// the scalar cache is empty when a kernel starts), read at uniform places: by
 // scalar loads, which no wait for vector loads in flight holds up.
 typedef __attribute__((address_space(4))) const int32_t* uniform_ints;
 __device__ __forceinline__ int uniform(const int32_t* p, int64_t i) { return ((uniform_ints)(uintptr_t)p)[i]; }

@@ -134,7 +134,7 @@ __device__ __forceinline__ PackedRows packed_rows(const PromptArgs& a, const Que
 }
 
 // Few tiles: 32 rows a workgroup, whose four waves take different keys (167
-// tokens of 24 heads of 256: 12 us, latency).
+// tokens of 24 heads of 256: 12.5 us, latency).
 template <int D, bool BF16OUT>
 __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     attend_keys(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
 }
 
-// Many tiles: 128 rows a workgroup (16384 tokens of 24 heads of 256: 1170
+// Many tiles: 128 rows a workgroup (16384 tokens of 24 heads of 256: 1140
 // TFLOP/s).
 template <int D, bool BF16OUT>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_prompt_rows_kernel(PromptArgs a) {
@@ -224,9 +224,12 @@ hipError_t launch_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_
                        scale * LOG2E, o, lse};
     // Few tiles of 128 rows: 32 rows a workgroup, so that more CUs have one and
     // each row's keys are walked four at a time; 512 tokens of 24 heads of 256
-    // take 25 us so and 29 the other way, of 32 heads of 128 11 and 17, 1024 of
-    // 24 of 256 60 and 50.  (With two key tiles there is nothing to share out:
-    // 33 tokens of 24 heads of 256 11 and 8.5 us.)
+    // take 24.5 us so and 35.7 the other way, of 32 heads of 128 11.2 and 17.6,
+    // 2048 of 14 heads of 64 22.4 and 35.7.  With two key tiles there is little to
+    // share out: 33 tokens of 32 heads of 128 6.9 and 5.8 us (of 24 of 256 11.1
+    // and 12.1).  Past the bound for rows of 256 the first form is still the
+    // faster one at 1024 tokens of 24 heads (47.1 and 57.7 us) and at 16 prompts
+    // of up to 300 of 8 heads (20.7 and 27.6).
     const bool few = tiles_of(a, 128) * hq * (d == 256 ? 2 : 1) <= device_cu_count() && tk > 64 * seqs;
     switch (d) {
         case 64: return bf16_out ? go<64, true>(a, few, stream) : go<64, false>(a, few, stream);

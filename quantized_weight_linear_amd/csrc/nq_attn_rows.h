@@ -5,9 +5,9 @@
 // registers), and the matrix work of one wave runs beside the softmax of the
 // others on its SIMD.
 //   Bound by the matrix cores and the vector ALU beside them: 16384 causal
-// tokens of 24 heads of 256 take 2.8 ms, 1170 TFLOP/s; 8192 of 24 of 256 1080
-// TFLOP/s, of 32 of 128 1100, of 32 of 64 920, of 32 of 128 with FP32 outputs
-// 610 (three products with V).  At 16384 tokens eight waves a workgroup are 3 %
+// tokens of 24 heads of 256 take 2.9 ms, 1140 TFLOP/s; 8192 of 24 of 256 1060
+// TFLOP/s, of 32 of 128 1070, of 32 of 64 880, of 32 of 128 with FP32 outputs
+// 590 (three products with V).  At 16384 tokens eight waves a workgroup are 3 %
 // slower, rings of three 2 %; logits of the next tile beside the softmax of
 // this one within a wave, with fewer waves, 30 %.
 //   E4M3 rows become BF16 as operands are read, in every wave: 33 drafts of 24

@@ -8,10 +8,11 @@
 // Either way a sequence's keys are split over workgroups and the parts are
 // joined by a second small kernel, so that one long context uses every CU.
 // Bound by HBM, the cache's bytes once, while the rows are few; from about 64
-// rows a KV head by the products.  24 / 4 heads of 256 in BF16, keys and values a second: one
-// context of 131072 5.3 TB/s, of 32768 4.2 (32 us), 8 of 32768 with 4 drafts
-// 5.6; 64 of 4096, 32 / 8 heads of 128, 5.4, with 16 drafts 5.5; E4M3 5.1, 2.8
-// (24 us), 4.9, 5.1, and 3.0 with 16 drafts.
+// rows a KV head by the products.  First kernel and join, 24 / 4 heads of 256:
+//   one context of 131072 keys, one token   BF16 92.9 + 5.3 us   E4M3 45.3 + 4.9
+//   one of 32768, one token                      26.5 + 4.7           18.0 + 4.6
+//   one of 32768, 33 drafts                      51.1 + 12.0          50.6 + 11.9
+// (the longest: 5.8 and 5.9 TB/s of keys and values).
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
@@ -432,9 +433,16 @@ TreePlan tree_plan(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t
     const int64_t least = rows <= 32 ? 128 : 256, units = seqs * hkv * tiles;
     TreePlan p{0, (int)least, rows <= 32 ? 128 : 32, (int)tiles, 0};
     if (max_len > (int64_t)1 << 30) max_len = (int64_t)1 << 30;          // the most that a table holds
-    // Short contexts: one range a sequence and one launch.  (701 keys of 24 / 4
-    // heads of 256: 10 + 5 us of kernels and two launches, or 16 us and one;
-    // 19.2 and 17.9 us a step, the cache's append included.)
+    // Short contexts: one range a sequence and one launch.  Microseconds in a
+    // graph, one range against several joined, BF16:
+    //                                      200 keys     450          768
+    //   24 / 4 of 256, 1 sequence, 1 token  10.6 13.6    13.4 13.7    16.4 13.8
+    //     8 drafts                          15.6 17.8    23.5 20.2    33.4 22.5
+    //     64 sequences, 1 token             12.2 27.0    15.7 30.1    19.9 36.8
+    //   32 / 8 of 128, 1 sequence, 1 token   7.5 10.3     9.6 10.4    11.8 10.7
+    //     64 sequences, 1 token             10.2 19.7    12.0 21.6    16.0 24.9
+    // One bound for all is a middle: for one sequence the two meet near 450 keys,
+    // for 64 past 768.  (Callers choose through max_len.)
     if (max_len <= 768) return p;
     const int64_t slots = cus * (tile == 32 && d == 256 ? 1 : 2);        // workgroups that run at once
     int64_t want = (2 * units <= slots ? slots : 4 * cus) / (hkv * tiles);
