@@ -44,6 +44,8 @@ typedef __attribute__((address_space(3))) unsigned char* lds_ptr;
 typedef __attribute__((address_space(3))) const unsigned char* lds_cptr;
 
 constexpr float RESCALE_LOG2 = 8.0f;
+constexpr float FAR_LOG2 = 536870912.0f; // references beyond it (2^29): see factor()
+constexpr float FLT_TOP = 3.40282347e38f;
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr int BUF_RAW = 0x00027000;      // raw buffer, no format conversion
@@ -193,6 +195,7 @@ struct Rows {
     v8bf q[NS];
     v16f o[ND];
     float m, l;                                         // reference m (unscaled logit units), this lane's half of the sum
+    bool far;                                           // some row's |m c| is beyond FAR_LOG2 (the same in all lanes)
     float c;                                            // scale log2 e, made positive
     uint32_t q_and, q_xor;                              // what that makes of the queries' bits
     int ka, va;                                         // byte offsets of this lane's first read in a K and a V tile
@@ -217,6 +220,7 @@ struct Rows {
         }
         m = -INFINITY;
         l = 0.f;
+        far = false;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -310,8 +314,22 @@ struct Rows {
         for (int i = 0; i < 16; ++i) s[i] = (w >> (8 * (i >> 2) + (i & 3))) & 1u ? s[i] : -INFINITY;
     }
 
-    // r, in log2 units.
-    __device__ __forceinline__ float reference() const { return m * c + RESCALE_LOG2; }
+    // r, in log2 units, kept finite (-infinity is the reference of a row that
+    // has seen nothing).
+    __device__ __forceinline__ float reference() const {
+        return __builtin_fminf(max2(m * c + RESCALE_LOG2, -FLT_TOP), FLT_TOP);
+    }
+    // The logits' factor in the weights.  fma(s, c, -r) sees s c exactly and r
+    // rounded: one factor for all weights of the row, of 2^32 at most up to |m c|
+    // = 2^29 and beyond FP32's range soon after.  There the logits' own steps are
+    // 32 and more, so that all weights but those of the largest logit vanish
+    // (2^-32), and they still do under the factor that brings |m| to 2^29.
+    __device__ __forceinline__ bool is_far() const { return m > -INFINITY && __builtin_fabsf(m) * c > FAR_LOG2; }
+    __device__ __forceinline__ float factor() const {
+        float f = c;
+        if (far && is_far()) f = FAR_LOG2 / __builtin_fabsf(m);
+        return f;
+    }
 
     // P^T of the 32 keys at k, with m, l and o brought along.
     template <bool HIDE>
@@ -326,17 +344,18 @@ struct Rows {
             const float to = max2(m, top);
             const float a = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - to) * c);
             m = to;
+            far = __ballot(is_far()) != 0;
             l *= a;
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= a;
         }
-        const float r = m == -INFINITY ? 0.f : reference();
+        const float f = factor(), r = m == -INFINITY ? 0.f : m * f + RESCALE_LOG2;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -r));
+            s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], f, -r));
             sum += s[i];
         }
         l += sum;

@@ -736,3 +736,63 @@ def test_tree_many_parts(fp8, hq, d, drafts, len_):
     for out in (torch.float32, torch.bfloat16):
         o, lse = run_tree(q, cache, [len_], [drafts], masks, 1 / math.sqrt(d), out)
         check(o, lse, *tree_oracle(q, cache, [len_], [drafts], masks, 1 / math.sqrt(d)), out)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,d", [(4, 64), (68, 256)])       # few tiles, and many
+@pytest.mark.parametrize("scale", [0.125, 1.0, 30.0])
+def test_prompt_keys_of_the_lowest_value(scale, hq, d, out):
+    """The first keys hold BF16's lowest value: logits of -3.4e38 or, scaled, of -infinity; the later ones are ordinary."""
+    n, at = 150, 70
+    q, k, v = torch.zeros((n, hq, d), dtype=torch.bfloat16), randn((n, 2, d), 98), randn((n, 2, d), 99)
+    q[:, :, 0] = 1.0
+    q[:, :, 1:3] = randn((n, hq, 2), 100, 1 / scale)
+    k[:at, :, 0], k[:at, :, 1:3] = torch.finfo(torch.bfloat16).min, 0
+    o, lse = run_prompt(q, k, v, [n], [n], scale, out)
+    ro, rl = prompt_oracle(q, k[at:], v[at:], [n], [n - at], scale)     # from row `at` on, the first keys weigh nothing
+    check(o[at:], lse[at:], ro[at:], rl[at:], out)
+
+
+@pytest.mark.parametrize("drafts,d", [(2, 256), (40, 64)])
+@pytest.mark.parametrize("split", [False, True])
+def test_tree_keys_of_the_lowest_value(split, drafts, d):
+    lens, at = [1500], 200
+    cache, masks = Cache(lens, [drafts], 1, d, 16, False, 114), trees([drafts], 115)
+    q = torch.zeros((drafts, 2, d), dtype=torch.bfloat16)
+    q[:, :, 0], q[:, :, 1:3] = 1.0, randn((drafts, 2, 2), 116)
+    for i in range(at):
+        cache.kp[int(cache.table[0, i // 16]), :, i % 16] = 0
+        cache.kp[int(cache.table[0, i // 16]), :, i % 16, 0] = torch.finfo(torch.bfloat16).min
+    o, lse = run_tree(q, cache, lens, [drafts], masks, 1.0, torch.float32, split)
+    cache.k, cache.v = [cache.k[0][at:]], [cache.v[0][at:]]
+    check(o, lse, *tree_oracle(q, cache, [lens[0] - at], [drafts], masks, 1.0), torch.float32)
+
+
+@pytest.mark.parametrize("hq,d", [(4, 64), (68, 256)])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e8, 1e9, 1e10, 1e20, 1e30, 1e38])
+def test_prompt_far_logits(size, hq, d):
+    """Logits of any size: the softmax picks the largest ones."""
+    n = 150
+    q, k, v = torch.zeros((n, hq, d), dtype=torch.bfloat16), torch.zeros((n, 2, d), dtype=torch.bfloat16), randn((n, 2, d), 117)
+    q[:, :, 0], q[:, 1::2, 0] = 1.0, -1.0
+    k[:, :, 0] = ((torch.rand((n, 2), generator=gen(118)) * 2 - 1) * size).to(torch.bfloat16)
+    k[140:, 0, 0] = k[:140, 0, 0].max()                 # equal ones share
+    o, lse = run_prompt(q, k, v, [n], [n], 1.0, torch.float32)
+    check(o, lse, *prompt_oracle(q, k, v, [n], [n], 1.0), torch.float32)
+
+
+@pytest.mark.parametrize("drafts,d", [(2, 256), (40, 64)])
+@pytest.mark.parametrize("size", [1e9, 1e20, 1e38])
+def test_tree_far_logits(size, drafts, d):
+    lens = [1500]
+    cache, masks = Cache(lens, [drafts], 1, d, 16, False, 119), trees([drafts], 120)
+    q, n = torch.zeros((drafts, 2, d), dtype=torch.bfloat16), 1500 + drafts
+    q[:, 0, 0], q[:, 1, 0] = 1.0, -1.0
+    k = torch.zeros((n, 1, d), dtype=torch.bfloat16)
+    k[:, 0, 0] = ((torch.rand(n, generator=gen(121)) * 2 - 1) * size).to(torch.bfloat16)
+    for i in range(n):
+        cache.kp[int(cache.table[0, i // 16]), :, i % 16] = k[i]
+    cache.k = [k.double()]
+    for split in (False, True):
+        o, lse = run_tree(q, cache, lens, [drafts], masks, 1.0, torch.float32, split)
+        check(o, lse, *tree_oracle(q, cache, lens, [drafts], masks, 1.0), torch.float32)
