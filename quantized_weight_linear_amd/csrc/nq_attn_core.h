@@ -27,7 +27,7 @@
 // Against 64 bits the outputs of 16384 tokens of 24 heads of 256 are then
 // 2.0e-3 off (Frobenius), 1.5e-3 with the output's rounding alone.  For FP32
 // outputs SPLITP makes P three BF16 terms (2^-22: 2e-7 off), for three products
-// with V instead of one: 8192 tokens of 32 heads of 128 take 931 us so and 515
+// with V instead of one: 8192 tokens of 32 heads of 128 take 927 us so and 520
 // with one term.
 #pragma once
 

@@ -1,9 +1,9 @@
 // The workgroup form with up to 32 query rows: four waves take different keys
 // of the same rows, every fourth tile of 32, each through LDS of its own
 // without barriers, and join at the end.  Bound by HBM: four contexts of
-// 71494 to 131000 keys, 24 / 4 heads of 256, BF16, up to 4 drafts, 282 us, 5.9
+// 71494 to 131000 keys, 24 / 4 heads of 256, BF16, up to 4 drafts, 281 us, 5.9
 // TB/s of keys and values; by latency where they are few: 701 keys 16.5 us, a
-// prompt of 167 tokens 12.5 us.
+// prompt of 167 tokens 12.6 us.
 #pragma once
 
 #include "nq_attn_rows.h"

@@ -6,7 +6,7 @@
 // Bound by the matrix cores: 4 D flops per (row, visible key).  Neighbouring
 // workgroups are heads of one tile, so that one round of them reads the same
 // keys; 1792 tokens on top of 8192 keys, 24 heads of 256, take 0.45 ms (336
-// workgroups for 512 places: 885 TFLOP/s).
+// workgroups for 512 places: 880 TFLOP/s).
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
@@ -134,7 +134,7 @@ __device__ __forceinline__ PackedRows packed_rows(const PromptArgs& a, const Que
 }
 
 // Few tiles: 32 rows a workgroup, whose four waves take different keys (167
-// tokens of 24 heads of 256: 12.5 us, latency).
+// tokens of 24 heads of 256: 12.6 us, latency).
 template <int D, bool BF16OUT>
 __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -161,8 +161,8 @@ __global__ __launch_bounds__(256) void attn_prompt_keys_kernel(PromptArgs a) {
     attend_keys(R, smem, 0, keys, t.last - t.first, src, sees, queries, emit, wave, lane);
 }
 
-// Many tiles: 128 rows a workgroup (16384 tokens of 24 heads of 256: 1140
-// TFLOP/s).
+// Many tiles: 128 rows a workgroup (16384 tokens of 24 heads of 256: 1120
+// to 1140 TFLOP/s).
 template <int D, bool BF16OUT>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_prompt_rows_kernel(PromptArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];

@@ -5,8 +5,8 @@
 // registers), and the matrix work of one wave runs beside the softmax of the
 // others on its SIMD.
 //   Bound by the matrix cores and the vector ALU beside them: 16384 causal
-// tokens of 24 heads of 256 take 2.9 ms, 1140 TFLOP/s; 8192 of 24 of 256 1060
-// TFLOP/s, of 32 of 128 1070, of 32 of 64 880, of 32 of 128 with FP32 outputs
+// tokens of 24 heads of 256 take 2.9 ms, 1120 to 1140 TFLOP/s; 8192 of 24 of 256
+// 1050 TFLOP/s, of 32 of 128 1060, of 32 of 64 880, of 32 of 128 with FP32 outputs
 // 590 (three products with V).  At 16384 tokens eight waves a workgroup are 3 %
 // slower, rings of three 2 %; logits of the next tile beside the softmax of
 // this one within a wave, with fewer waves, 30 %.

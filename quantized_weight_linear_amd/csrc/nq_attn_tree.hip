@@ -9,10 +9,10 @@
 // joined by a second small kernel, so that one long context uses every CU.
 // Bound by HBM, the cache's bytes once, while the rows are few; from about 64
 // rows a KV head by the products.  First kernel and join, 24 / 4 heads of 256:
-//   one context of 131072 keys, one token   BF16 92.9 + 5.3 us   E4M3 45.3 + 4.9
-//   one of 32768, one token                      26.5 + 4.7           18.0 + 4.6
-//   one of 32768, 33 drafts                      51.1 + 12.0          50.6 + 11.9
-// (the longest: 5.8 and 5.9 TB/s of keys and values).
+//   one context of 131072 keys, one token   BF16 93.6 + 5.8 us   E4M3 46.9 + 5.1
+//   one of 32768, one token                      27.1 + 4.5           18.0 + 4.6
+//   one of 32768, 33 drafts                      53.2 + 12.2          50.4 + 12.0
+// (the longest: 5.7 and 5.7 TB/s of keys and values).
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
