@@ -71,6 +71,13 @@ typedef enum {
     NQ_W_Q6G64_F16S = 7   /* (b = 4 would be the Q4 layout); one FP16 scale per 64 elements [N][K/64] */
 } nq_wfmt;
 
+/* What nq_rmsnorm writes: the forms of activations that the products take. */
+typedef enum {
+    NQ_ACT_BF16 = 0,      /* BF16 [T][K] */
+    NQ_ACT_INT8_G64 = 1,  /* int8 [T][K], one FP32 scale per 64 columns [T][K/64] (W8A8, A8) */
+    NQ_ACT_E4M3_B128 = 2  /* E4M3 [T][K], one FP32 scale per 128 columns [T][ceil(K/128)] (nq_gemm_fp8_b128) */
+} nq_act_fmt;
+
 typedef enum { NQ_ROUTE_BF16 = 0, NQ_ROUTE_A8 = 1, NQ_ROUTE_A8_DECODE = 2 } nq_route_kind;
 
 /* Flags of the routed calls (nq_route, nq_linear_*): which steps may run with
@@ -169,6 +176,41 @@ nq_status nq_quantize_act_int8_g64(const uint16_t* x, int64_t T, int64_t K, int8
  */
 nq_status nq_quantize_act_fp8_row(const uint16_t* x, int64_t M, int64_t K, uint8_t* codes, float* scale,
                                   void* stream);
+
+/*
+ * E4M3 activation quantization with a scale per token and 128 columns, for
+ * nq_gemm_fp8_b128: s = fp32(amax / 448) over the block (the last one of a row
+ * may be shorter), codes e4m3_rne_sat(fp32(x / s)).  A block of zeros gets s = 0
+ * and keeps its signed zeros; a block holding a NaN gets s = NaN and NaN codes,
+ * one holding an infinity (but no NaN) s = infinity, and reads as NaN.
+ *   x [T][K] BF16 bits;  codes [T][K];  scale [T][ceil(K/128)] FP32 (4-byte aligned)
+ * Errors: K % 16 != 0, more than 2^28 blocks -> NQ_ERR_SHAPE.
+ */
+nq_status nq_quantize_act_fp8_b128(const uint16_t* x, int64_t T, int64_t K, uint8_t* codes, float* scale,
+                                   void* stream);
+
+/*
+ * RMS norm with the residual's addition, ready for the next projection.  [FP8
+ * card, "Model overview"]: hidden states of 5120 between the projections.
+ *   h = bf16(x + residual) (without a residual: h = x), written to residual_out;
+ *   y = h / sqrt(mean(h^2) + eps) * (weight + weight_bias), in FP32
+ *   x        [T][K] BF16 bits, x_stride elements between rows (at least K, a
+ *            multiple of 8, below 2^24)
+ *   residual, residual_out   [T][K] BF16 bits; residual_out may be residual
+ *            itself; residual NULL: nothing is added and residual_out is not used
+ *   weight   [K] BF16 bits, or NULL for ones; weight_bias is 1 for models whose
+ *            weights are stored as their distance from 1, else 0
+ *   act_fmt, y, y_scale   see nq_act_fmt.  BF16: y rounded once.  8 bits: the
+ *            FP32 y quantized as nq_quantize_act_int8_g64 and
+ *            nq_quantize_act_fp8_b128 quantize theirs (y_scale 4-byte aligned;
+ *            NULL for BF16)
+ * Squares are summed in FP64.
+ * Errors: K not a multiple of 8 (BF16), 64 (int8) or 16 (E4M3), K above 32768,
+ * T of 2^24 or more -> NQ_ERR_SHAPE; eps outside [1e-30, 1e30] -> NQ_ERR_RANGE.
+ */
+nq_status nq_rmsnorm(int act_fmt, const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                     uint16_t* residual_out, const uint16_t* weight, float weight_bias, float eps, int64_t T,
+                     int64_t K, void* y, float* y_scale, void* stream);
 
 /*
  * Decode GEMV on row-scaled FP8 weights, BF16 activations, FP32 accumulation.
@@ -308,6 +350,36 @@ nq_status nq_gemm_w8a8_g64(const int8_t* a_q, const float* a_scale, const int8_t
 nq_status nq_gemm_fp8row(const uint16_t* x, const uint8_t* w, const uint16_t* w_scale, int64_t M,
                          int64_t N, int64_t K, uint8_t* a_codes, float* a_scale, int out_dt, void* y,
                          void* stream);
+
+/*
+ * E4M3 activations times E4M3 weights with block scales, for decode, verify and
+ * prefill alike.  [FP8 card, "Conversion and verification", "Block-wise to
+ * per-row, exactly"]: checkpoints hold E4M3 codes with one FP32 scale per 128x128
+ * block (weight_scale_inv); this product takes them as they are.
+ *   a_codes [M][K], a_scale [M][gc] FP32 (from nq_quantize_act_fp8_b128 or nq_rmsnorm)
+ *   w       [N][K] E4M3 codes
+ *   wsi     [gr][gc] FP32, gr = ceil(N/128), gc = ceil(K/128)
+ *   y       [M][N] FP32 or BF16 bits:
+ *           y[m][n] = sum_g a_scale[m][g] * wsi[n/128][g] * P[m][n][g],
+ *           P the sum over block g's columns of a[m][k] * w[n][k]; the product of
+ *           the two scales is formed in FP32, and the blocks are summed in FP32
+ *   workspace, workspace_bytes   optional device scratch
+ *           (nq_gemm_fp8_b128_workspace_bytes): lets K be split over workgroups
+ *           where M and N give too few.  It needs no preparation and holds nothing
+ *           between calls; calls that share it must be ordered (the same stream).
+ *           A smaller one than asked for is not used.
+ * FP32 outputs: both operands are decoded exactly to BF16 and P is summed in FP32
+ * on the BF16 matrix units, within this library's 1e-5.  BF16 outputs: P comes
+ * from the FP8 matrix units, whose sums are off by 1.3e-5 to 1.8e-5 (Frobenius,
+ * relative), where the output's rounding is off by 1.7e-3.
+ * The result does not depend on timing.  a_scale, wsi: 4-byte aligned.
+ * Errors: K % 16 != 0, K of 2^20 or more, gr / gc mismatch, more than 2^24 tiles
+ * of 64 x 64 -> NQ_ERR_SHAPE.
+ */
+int64_t nq_gemm_fp8_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
+nq_status nq_gemm_fp8_b128(const uint8_t* a_codes, const float* a_scale, const uint8_t* w, const float* wsi,
+                           int64_t M, int64_t N, int64_t K, int64_t gr, int64_t gc, int out_dt, void* y,
+                           void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * Route rule.  [int8 card, "What changes"]: a projection permitted to use
@@ -475,8 +547,17 @@ nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k,
 
 typedef enum {
     NQ_KV_BF16 = 0,  /* BF16 rows */
-    NQ_KV_E4M3 = 1   /* E4M3 codes; a KV head's values are code * scale[head] (FP32 [Hkv], for K and for V) */
+    NQ_KV_E4M3 = 1,  /* E4M3 codes; a KV head's values are code * scale[head] (FP32 [Hkv], for K and for V) */
+    NQ_KV_E4M3_TOKEN = 3  /* (2 stays unknown) E4M3 codes with a scale for each token and head: code * scale[page][head][slot]
+                             (FP32 [pages][Hkv][page_size], a plane beside K's and one beside V's), so that no
+                             range has to be known before the first token, and moving or dropping a row
+                             touches no other one */
 } nq_kv_fmt;
+
+typedef enum {
+    NQ_ROPE_HALVES = 0,  /* pairs are columns (i, i + rot / 2) */
+    NQ_ROPE_PAIRS = 1    /* pairs are columns (2 i, 2 i + 1) */
+} nq_rope;
 
 /*
  * The cache.  A plane holds the keys, or the values, of one layer:
@@ -495,7 +576,8 @@ typedef enum {
 /*
  * The step's keys and values into the cache: token t of sequence b to position
  * lens[b] + (t - cu[b]).  E4M3: e4m3_rne_sat(fp32(x / scale[head])).  Tokens
- * past the table or without a page are dropped.
+ * past the table or without a page are dropped.  (E4M3_TOKEN rows are written by
+ * nq_kv_append_rope.)
  */
 nq_status nq_kv_append(int kv_fmt, const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
                        const float* k_scale, const float* v_scale, const int32_t* page_table, int64_t width,
@@ -503,11 +585,49 @@ nq_status nq_kv_append(int kv_fmt, const uint16_t* k, int64_t k_stride, const ui
                        int64_t page_size, int64_t pages, void* k_pages, void* v_pages, void* stream);
 
 /*
+ * The same with what comes before it in a layer: heads normalised where the
+ * model does that, queries and keys turned by their tokens' positions, keys and
+ * values into the cache.  This is also the call that writes NQ_KV_E4M3_TOKEN
+ * rows (rot = 0 and q NULL: nothing but the append).
+ *   q_weight, k_weight   BF16 bits [D], or NULL: each head of q (k) becomes
+ *            x / sqrt(mean(x^2) + eps) * (weight + weight_bias) first
+ *   positions, inv_freq  int32 [T] and FP32 [rot / 2]: pair i of the first `rot`
+ *            columns (rope: which columns form a pair) is turned by the angle
+ *            positions[t] * inv_freq[i], whose fraction of a turn is worked out in
+ *            FP64; columns from rot on stay as they are
+ *   q_out    BF16 [T][Hq][D], q_out_stride elements between tokens; it may be q
+ *            itself, with its stride.  q NULL: there are no queries (Hq is still
+ *            checked)
+ *   k_out    NULL, or the keys as q_out has the queries (what attention over the
+ *            prompt itself reads); it may be k itself
+ *   k_scale, v_scale     E4M3: read, [Hkv].  E4M3_TOKEN: written, planes of
+ *            [pages][Hkv][page_size]: s = fp32(amax / 448) over the row's finite
+ *            values, so that a scale is always finite; codes are
+ *            e4m3_rne_sat(fp32(x / s)): infinities saturate, NaN stays NaN, a row of
+ *            zeros has s = 0.  BF16: not used.  Keys are rounded once, from FP32
+ * Tokens past the table or without a page are dropped from the cache, but their
+ * queries and k_out are written; tokens of no sequence are not written at all.
+ * Errors: rot not a multiple of 16 in 0 .. D, T of 2^24 or more -> NQ_ERR_SHAPE;
+ * unknown rope or kv_fmt -> NQ_ERR_FORMAT; eps outside [1e-30, 1e30] with a
+ * weight -> NQ_ERR_RANGE.
+ */
+nq_status nq_kv_append_rope(int kv_fmt, const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                            const uint16_t* v, int64_t v_stride, const uint16_t* q_weight, const uint16_t* k_weight,
+                            float weight_bias, float eps, const int32_t* positions, const float* inv_freq,
+                            int64_t rot, int rope, float* k_scale, float* v_scale, const int32_t* page_table,
+                            int64_t width, const int32_t* lens, const int32_t* cu, int64_t B, int64_t T, int64_t Hq,
+                            int64_t Hkv, int64_t D, int64_t page_size, int64_t pages, uint16_t* q_out,
+                            int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride, void* k_pages,
+                            void* v_pages, void* stream);
+
+/*
  * Attention of the drafted tokens, which form a tree: token i of a sequence
  * sees all committed tokens, and drafted token j (0 .. 63, counted from the
  * sequence's first) where bit j of tree_mask[i] is set (uint64 [T]; bit i
  * itself included or not, as given; bits past the sequence's drafted tokens
  * are ignored).  The drafted tokens' keys and values are in the cache already.
+ *   k_scale, v_scale   E4M3: [Hkv].  E4M3_TOKEN: planes of [pages][Hkv][page_size].
+ *            BF16: not used
  *   max_q    the most drafted tokens of a sequence, 1 .. 64; later ones are
  *            neither computed nor written
  *   max_len  about the longest lens[b] + drafted tokens; it only shapes the
@@ -559,7 +679,8 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
  *   sequence b keeps, ascending: accept[cu_accept[b]] ..) are moved together:
  *   row lens[b] + accept[i] to row lens[b] + i, in every plane, for i and
  *   accept[i] below 64.  `accepted` is accept's length; rows without a page
- *   are skipped.
+ *   are skipped.  A row has 16 .. 512 bytes, a multiple of 16, or 4: the planes
+ *   of an E4M3_TOKEN cache's scales move with those of its codes.
  */
 nq_status nq_kv_reserve(int32_t* refs, int64_t pages, int32_t* page_table, int64_t width, const int32_t* lens,
                         const int32_t* new_lens, int64_t B, int64_t page_size, int32_t* free_list,

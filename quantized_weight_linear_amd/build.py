@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libnq.so")
 SOURCES = ["nq_abi.cpp", "nq_convert.hip", "nq_gemv.hip", "nq_gemv_fp8row.hip", "nq_gemv_mxfp8.hip",
            "nq_gemv_bf16.hip", "nq_gemv_q8g64.hip", "nq_gemv_q4g64.hip", "nq_gemv_q8g32.hip", "nq_gemv_a8.hip",
            "nq_gemv_qb.hip", "nq_gemm.hip", "nq_attn_prompt.hip", "nq_attn_tree.hip", "nq_kv_pages.hip",
-           "nq_probe.hip"]
+           "nq_norm.hip", "nq_gemm_b128.hip", "nq_kv_rope.hip", "nq_probe.hip"]
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

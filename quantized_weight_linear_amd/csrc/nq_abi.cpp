@@ -9,6 +9,7 @@
 #include "nq.h"
 #include "nq_attn_launch.h"
 #include "nq_launch.h"
+#include "nq_layer_launch.h"
 
 namespace {
 
@@ -607,6 +608,12 @@ bool table_ok(int64_t B, int64_t width, int64_t page_size, int64_t pages) {
     return B >= 0 && B < MOST_BLOCKS && width >= 0 && pages >= 0 && pages < I31 && page_ok(page_size) &&
            width <= ((int64_t)1 << 30) / page_size;
 }
+bool kv_fmt_ok(int fmt) { return fmt == NQ_KV_BF16 || fmt == NQ_KV_E4M3 || fmt == NQ_KV_E4M3_TOKEN; }
+// Offsets inside a tile are 32-bit (256 rows of K bytes), and so are rows.
+bool b128_shape_ok(int64_t M, int64_t N, int64_t K) {
+    return M >= 0 && N >= 0 && K >= 0 && M <= MOST_ROWS && N <= MOST_ROWS && K < ((int64_t)1 << 20) && K % 16 == 0 &&
+           ((M + 63) / 64) * ((N + 63) / 64) < MOST_BLOCKS;
+}
 bool scale_ok(float scale) { return scale >= 1e-30f && scale <= 1e30f; }       // (false for NaN)
 
 // Pointers that may be NULL, aligned to what the kernels read of them at once:
@@ -625,6 +632,90 @@ nq_status all_at(P... p) {
 }  // namespace
 
 extern "C" {
+
+nq_status nq_quantize_act_fp8_b128(const uint16_t* x, int64_t T, int64_t K, uint8_t* codes, float* scale, void* stream) {
+    if (T < 0 || K < 0 || K % 16 != 0 || T >= I31 || K >= I31 || T * ((K + 127) / 128) >= 16 * MOST_BLOCKS) return NQ_ERR_SHAPE;
+    if (T == 0 || K == 0) return NQ_OK;
+    NQ_TRY(all_at<16>(x, codes));
+    NQ_TRY(all_at<4>(scale));
+    return from_hip(nq::launch_quantize_fp8_b128(x, T, K, codes, scale, as_stream(stream)));
+}
+
+nq_status nq_rmsnorm(int act_fmt, const uint16_t* x, int64_t x_stride, const uint16_t* residual, uint16_t* residual_out,
+                     const uint16_t* weight, float weight_bias, float eps, int64_t T, int64_t K, void* y, float* y_scale,
+                     void* stream) {
+    if (act_fmt != NQ_ACT_BF16 && act_fmt != NQ_ACT_INT8_G64 && act_fmt != NQ_ACT_E4M3_B128) return NQ_ERR_FORMAT;
+    const int64_t unit = act_fmt == NQ_ACT_BF16 ? 8 : act_fmt == NQ_ACT_INT8_G64 ? 64 : 16;
+    if (T < 0 || T >= MOST_BLOCKS || K < 0 || K > 32768 || K % unit != 0 || !stride_ok(x_stride, 1, K)) return NQ_ERR_SHAPE;
+    if (!scale_ok(eps)) return NQ_ERR_RANGE;
+    if (T == 0 || K == 0) return NQ_OK;
+    NQ_TRY(all_at<16>(x, y));
+    if (residual) NQ_TRY(all_at<16>(residual, residual_out));
+    NQ_TRY(at_ok<16>(weight));
+    if (act_fmt != NQ_ACT_BF16) NQ_TRY(all_at<4>(y_scale));
+    return from_hip(nq::launch_rmsnorm(act_fmt, x, x_stride, residual, residual_out, weight, weight_bias, eps, T, K, y, y_scale,
+                                       as_stream(stream)));
+}
+
+int64_t nq_gemm_fp8_b128_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!b128_shape_ok(M, N, K) || M == 0 || N == 0) return 0;
+    return nq::gemm_fp8_b128_workspace_bytes(M, N, K);
+}
+
+nq_status nq_gemm_fp8_b128(const uint8_t* a_codes, const float* a_scale, const uint8_t* w, const float* wsi, int64_t M,
+                           int64_t N, int64_t K, int64_t gr, int64_t gc, int out_dt, void* y, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+    if (!b128_shape_ok(M, N, K) || workspace_bytes < 0) return NQ_ERR_SHAPE;
+    if (gr != (N + 127) / 128 || gc != (K + 127) / 128) return NQ_ERR_SHAPE;
+    if (!out_ok(out_dt)) return NQ_ERR_FORMAT;
+    if (M == 0 || N == 0) return NQ_OK;
+    NQ_TRY(all_at<16>(y));
+    if (K > 0) {
+        NQ_TRY(all_at<16>(a_codes, w));
+        NQ_TRY(all_at<4>(a_scale, wsi));
+    }
+    NQ_TRY(align_ok(workspace));
+    return from_hip(nq::launch_gemm_fp8_b128(a_codes, a_scale, w, wsi, M, N, K, out_dt == NQ_OUT_BF16, y, workspace,
+                                             workspace ? workspace_bytes : 0, as_stream(stream)));
+}
+
+nq_status nq_kv_append_rope(int kv_fmt, const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                            const uint16_t* v, int64_t v_stride, const uint16_t* q_weight, const uint16_t* k_weight,
+                            float weight_bias, float eps, const int32_t* positions, const float* inv_freq, int64_t rot,
+                            int rope, float* k_scale, float* v_scale, const int32_t* page_table, int64_t width,
+                            const int32_t* lens, const int32_t* cu, int64_t B, int64_t T, int64_t Hq, int64_t Hkv,
+                            int64_t D, int64_t page_size, int64_t pages, uint16_t* q_out, int64_t q_out_stride,
+                            uint16_t* k_out, int64_t k_out_stride, void* k_pages, void* v_pages, void* stream) {
+    if (!kv_fmt_ok(kv_fmt) || (rope != NQ_ROPE_HALVES && rope != NQ_ROPE_PAIRS)) return NQ_ERR_FORMAT;
+    if (T < 0 || T >= MOST_BLOCKS || !heads_ok(Hq, Hkv, D) || !table_ok(B, width, page_size, pages) || rot < 0 || rot > D ||
+        rot % 16 != 0)
+        return NQ_ERR_SHAPE;
+    if ((q && (!stride_ok(q_stride, Hq, D) || !stride_ok(q_out_stride, Hq, D))) || !stride_ok(k_stride, Hkv, D) ||
+        !stride_ok(v_stride, Hkv, D) || (k_out && !stride_ok(k_out_stride, Hkv, D)))
+        return NQ_ERR_SHAPE;
+    if (((q && q_weight) || k_weight) && !scale_ok(eps)) return NQ_ERR_RANGE;
+    if (B == 0 || T == 0) return NQ_OK;
+    NQ_TRY(all_at<16>(k, v));
+    NQ_TRY(all_at<4>(lens, cu));
+    if (q) NQ_TRY(all_at<16>(q, q_out));
+    if (rot > 0) NQ_TRY(all_at<4>(positions, inv_freq));
+    for (const void* p : {(const void*)q_weight, (const void*)k_weight, (const void*)k_out}) NQ_TRY(at_ok<16>(p));
+    if (width > 0 && pages > 0) {
+        NQ_TRY(all_at<4>(page_table));
+        NQ_TRY(all_at<16>(k_pages, v_pages));
+        if (kv_fmt != NQ_KV_BF16) NQ_TRY(all_at<4>(k_scale, v_scale));
+    }
+    const bool cached = width > 0 && pages > 0;
+    nq::RopeArgs a{};
+    a.q = q, a.k = k, a.v = v, a.qs = q_stride, a.ks = k_stride, a.vs = v_stride;
+    a.q_weight = q_weight, a.k_weight = k_weight, a.bias = weight_bias, a.eps = eps;
+    a.positions = positions, a.freq = inv_freq, a.rot = (int)rot, a.pairs = rope == NQ_ROPE_PAIRS;
+    a.k_scale = k_scale, a.v_scale = v_scale, a.table = page_table, a.lens = lens, a.cu = cu;
+    a.width = cached ? width : 0, a.pages = cached ? pages : 0, a.t = T;
+    a.seqs = (int)B, a.hq = q ? (int)Hq : 0, a.hkv = (int)Hkv, a.d = (int)D, a.shift = __builtin_ctzll(page_size);
+    a.q_out = q_out, a.k_out = k_out, a.qos = q_out_stride, a.kos = k_out_stride, a.k_pages = k_pages, a.v_pages = v_pages;
+    return from_hip(nq::launch_kv_append_rope(cached ? kv_fmt : (int)NQ_KV_BF16, a, as_stream(stream)));
+}
 
 nq_status nq_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                          int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, int64_t B, int64_t Tq, int64_t Tk,
@@ -673,8 +764,7 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
                        int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t page_size, int64_t pages, int64_t max_len,
                        float scale, int out_dt, void* o, float* lse, void* workspace, int64_t workspace_bytes,
                        void* stream) {
-    if (kv_fmt != NQ_KV_BF16 && kv_fmt != NQ_KV_E4M3) return NQ_ERR_FORMAT;
-    if (!out_ok(out_dt)) return NQ_ERR_FORMAT;
+    if (!kv_fmt_ok(kv_fmt) || !out_ok(out_dt)) return NQ_ERR_FORMAT;
     if (T < 0 || T >= I31 || max_q < 1 || max_q > 64 || max_len < 0 || workspace_bytes < 0 || !heads_ok(Hq, Hkv, D) ||
         !table_ok(B, width, page_size, pages) || !stride_ok(q_stride, Hq, D))
         return NQ_ERR_SHAPE;
@@ -690,10 +780,10 @@ nq_status nq_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const vo
     NQ_TRY(at_ok<4>(page_table));
     NQ_TRY(align_ok(k_pages));
     NQ_TRY(align_ok(v_pages));
-    if (kv_fmt == NQ_KV_E4M3) NQ_TRY(all_at<4>(k_scale, v_scale));
+    if (kv_fmt == NQ_KV_E4M3 || (kv_fmt == NQ_KV_E4M3_TOKEN && pages > 0 && width > 0)) NQ_TRY(all_at<4>(k_scale, v_scale));
     NQ_TRY(at_ok<4>(lse));
     NQ_TRY(align_ok(workspace));
-    return from_hip(nq::launch_attn_tree(kv_fmt == NQ_KV_E4M3, q, q_stride, k_pages, v_pages, k_scale, v_scale, page_table,
+    return from_hip(nq::launch_attn_tree(kv_fmt, q, q_stride, k_pages, v_pages, k_scale, v_scale, page_table,
                                          width, lens, cu_q, tree_mask, B, max_q, T, Hq, Hkv, D, page_size, pages, max_len,
                                          scale, out_dt == NQ_OUT_BF16, o, lse, workspace, workspace ? workspace_bytes : 0,
                                          as_stream(stream)));
@@ -748,8 +838,8 @@ nq_status nq_kv_copy_pages(void* pool, int64_t planes, int64_t plane_bytes, int6
 nq_status nq_kv_compact(void* pool, int64_t planes, int64_t plane_bytes, int64_t Hkv, int64_t page_size, int64_t row_bytes,
                         int64_t pages, const int32_t* page_table, int64_t width, const int32_t* lens, const int32_t* accept,
                         const int32_t* cu_accept, int64_t B, int64_t accepted, void* stream) {
-    if (!table_ok(B, width, page_size, pages) || planes < 0 || planes > 65535 || Hkv < 1 || Hkv >= 65536 || row_bytes < 16 ||
-        row_bytes % 16 != 0 || row_bytes > 512 || accepted < 0 || accepted >= I31 || plane_bytes % 16 != 0 ||
+    if (!table_ok(B, width, page_size, pages) || planes < 0 || planes > 65535 || Hkv < 1 || Hkv >= 65536 ||
+        (row_bytes != 4 && (row_bytes < 16 || row_bytes % 16 != 0 || row_bytes > 512)) || accepted < 0 || accepted >= I31 || plane_bytes % 16 != 0 ||
         (pages > 0 && plane_bytes / pages < Hkv * page_size * row_bytes) || B * Hkv >= MOST_BLOCKS)
         return NQ_ERR_SHAPE;
     if (B == 0 || accepted == 0 || planes == 0 || pages == 0 || width == 0) return NQ_OK;

@@ -92,6 +92,13 @@ __device__ __forceinline__ void load_to_lds(v4i r, int off, lds_ptr dst) {
                  : "memory", "m0");
 }
 
+// The 16 floats of r to LDS at dst, zeros to the 192 bytes behind them.
+__device__ __forceinline__ void load_scales(v4i r, int lane, lds_ptr dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 ::"s"((uint32_t)(uintptr_t)dst), "v"(lane * 4), "s"(r)
+                 : "memory", "m0");
+}
+
 // 16 rows (keys 16-aligned in the tile) from memory into LDS at dst, no
 // registers between; rows past the descriptor's range become zeros.  The wave
 // waits with vmcnt before anyone reads them.
@@ -183,6 +190,32 @@ __device__ __forceinline__ void rows_made_finite(lds_ptr p, int lane) {
         *at = x;
     }
 }
+
+// The scales of 32 staged keys, or of their values, where each row of the cache
+// has one: two groups of 16 floats in LDS, GROUP bytes apart (one load
+// instruction fills GROUP bytes, zeros behind the 16).  They multiply the
+// logits, or the weights, of the keys: a lane's 16 registers are keys
+// 8 (i / 4) + 4 h + i % 4.
+struct NoScales {
+    static constexpr bool ANY = false;
+    template <bool HIDE>
+    __device__ __forceinline__ void apply(v16f&, int) const {}
+};
+struct RowScales {
+    static constexpr bool ANY = true;
+    static constexpr int GROUP = 256;
+    lds_cptr at;
+    // HIDE: what is 0 stays 0 whatever the scale holds (the row may never have been written).
+    template <bool HIDE>
+    __device__ __forceinline__ void apply(v16f& x, int lane) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const v4f f = *(__attribute__((address_space(3))) const v4f*)(at + (e >> 1) * GROUP + (e & 1) * 32 + (lane >> 5) * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * e + j] = HIDE && x[4 * e + j] == 0.f ? 0.f : x[4 * e + j] * f[j];
+        }
+    }
+};
 
 // One wave's 32 rows and their running results; a lane has one row (lane % 32).
 template <int D, bool FP8, bool SPLITP>
@@ -332,9 +365,10 @@ struct Rows {
     }
 
     // P^T of the 32 keys at k, with m, l and o brought along.
-    template <bool HIDE>
-    __device__ __forceinline__ void weights(lds_cptr k, uint64_t seen, v16f& s) {
+    template <bool HIDE, class Scales>
+    __device__ __forceinline__ void weights(lds_cptr k, uint64_t seen, v16f& s, const Scales& scales) {
         logits(k, s);
+        scales.template apply<false>(s, lane);
         if (HIDE) hide(s, seen);
         float top = s[0];
 #pragma unroll

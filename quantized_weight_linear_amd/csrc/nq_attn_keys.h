@@ -15,11 +15,14 @@ namespace attn {
 // and each slot is loaded again as soon as it has been read.
 constexpr int KEY_WAVES = 4;
 
-template <int D, bool FP8>
+// SCALED: each key's and value's row has a scale of its own, staged beside the tiles.
+template <int D, bool FP8, bool SCALED = false>
 struct KeysLds {
     static constexpr int TILE = 32 * Tile<D, FP8>::ROW;
     static constexpr int RING = TILE >= 8192 ? 1 : TILE >= 4096 ? 2 : 4;
-    static constexpr int WAVE = 2 * RING * TILE;                    // 16 KiB (BF16 rows of 256: 32 KiB)
+    static constexpr int SCALES = 2 * RING * TILE;                  // of a slot: K's two groups, then V's
+    static constexpr int SLOT_SCALES = SCALED ? 4 * RowScales::GROUP : 0;
+    static constexpr int WAVE = SCALES + RING * SLOT_SCALES;        // 16 KiB (BF16 rows of 256: 32 KiB) and the scales
     static constexpr int PITCH = D + 4;                             // floats a row of the waves' results at the end
     static constexpr int JOIN = KEY_WAVES * 32 * PITCH * 4;
     static constexpr int BYTES = KEY_WAVES * WAVE > JOIN ? KEY_WAVES * WAVE : JOIN;
@@ -33,17 +36,31 @@ template <int D, bool FP8, bool SPLITP, class Source, class Sees, class Queries,
 __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned char* smem, int key0, int key1, int rows,
                                             const Source& src, const Sees& sees, const Queries& queries, const Emit& emit,
                                             int wave, int lane) {
-    using L = KeysLds<D, FP8>;
-    constexpr int LOADS = 2 * Tile<D, FP8>::LOADS16, LATER = (2 * L::RING - 1) * LOADS, STEP = KEY_WAVES * 32;
+    constexpr bool SCALED = Source::SCALED;
+    using L = KeysLds<D, FP8, SCALED>;
+    constexpr int PIECES = 2 * Tile<D, FP8>::LOADS16, LOADS = PIECES + (SCALED ? 2 : 0), LATER = (2 * L::RING - 1) * LOADS;
+    constexpr int STEP = KEY_WAVES * 32;
     const Stager<D, FP8> st_k(lane, src.k_stride), st_v(lane, src.v_stride);
     const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
     auto load_k = [&](int key, int slot) {
         st_k.rows16(src.k_rows(key), mine + slot * 2 * L::TILE);
         st_k.rows16(src.k_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE / 2);
+        if constexpr (SCALED) {
+            load_scales(src.k_scales(key), lane, mine + L::SCALES + slot * L::SLOT_SCALES);
+            load_scales(src.k_scales(key + 16), lane, mine + L::SCALES + slot * L::SLOT_SCALES + RowScales::GROUP);
+        }
     };
     auto load_v = [&](int key, int slot) {
         st_v.rows16(src.v_rows(key), mine + slot * 2 * L::TILE + L::TILE);
         st_v.rows16(src.v_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
+        if constexpr (SCALED) {
+            load_scales(src.v_scales(key), lane, mine + L::SCALES + slot * L::SLOT_SCALES + 2 * RowScales::GROUP);
+            load_scales(src.v_scales(key + 16), lane, mine + L::SCALES + slot * L::SLOT_SCALES + 3 * RowScales::GROUP);
+        }
+    };
+    auto scales = [&](int slot, int groups) {
+        if constexpr (SCALED) return RowScales{mine + L::SCALES + slot * L::SLOT_SCALES + groups * RowScales::GROUP};
+        else return NoScales{};
     };
     const int from = key0 + wave * 32;
 #pragma unroll
@@ -60,16 +77,17 @@ __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned ch
         uint64_t seen = 0;
         if (PARTLY) seen = sees.seen(key);
         wait_vm<LATER>();
-        R.template weights<PARTLY>(k, seen, x);
+        R.template weights<PARTLY>(k, seen, x, scales(slot, 0));
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
         load_k(key + L::RING * STEP, slot);
         wait_vm<LATER>();
         if (PARTLY) {
-            if (const uint32_t bad = rows_not_finite<D, FP8, LOADS>(v, lane)) {
+            if (const uint32_t bad = rows_not_finite<D, FP8, PIECES>(v, lane)) {
                 R.add_not_finite(v, bad, seen);
-                rows_made_finite<D, FP8, LOADS>(v, lane);
+                rows_made_finite<D, FP8, PIECES>(v, lane);
             }
         }
+        scales(slot, 2).template apply<PARTLY>(x, lane);
         R.values(v, x);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         load_v(key + L::RING * STEP, slot);

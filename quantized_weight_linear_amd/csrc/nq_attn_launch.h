@@ -35,7 +35,7 @@ hipError_t launch_attn_prompt(const uint16_t* q, int64_t q_stride, const uint16_
                               int64_t tk, int64_t hq, int64_t hkv, int64_t d, float scale, bool bf16_out, void* o,
                               float* lse, hipStream_t stream);
 int64_t attn_tree_workspace_bytes(int64_t seqs, int64_t max_q, int64_t hq, int64_t hkv, int64_t d, int64_t max_len);
-hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+hipError_t launch_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
                             const float* k_scale, const float* v_scale, const int32_t* table, int64_t width,
                             const int32_t* lens, const int32_t* cu_q, const uint64_t* masks, int64_t seqs, int64_t max_q,
                             int64_t t, int64_t hq, int64_t hkv, int64_t d, int64_t page_size, int64_t pages,

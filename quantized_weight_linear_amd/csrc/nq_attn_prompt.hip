@@ -32,6 +32,7 @@ struct PromptArgs {
 __device__ __forceinline__ int cut_offset(int x, int64_t total) { return x < 0 ? 0 : x > (int)total ? (int)total : x; }
 
 struct PackedRows {                 // K or V rows of one sequence and KV head
+    static constexpr bool SCALED = false;
     const uint16_t *k, *v;
     int k_stride, v_stride;         // bytes
     int n, row_bytes;

@@ -25,11 +25,12 @@ namespace attn {
 
 constexpr int KEYS = 32;        // keys a step
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SCALED = false>
 struct RowsLds {
     static constexpr int TILE = KEYS * Tile<D, FP8>::ROW;
     static constexpr int FLAGS = 4 * TILE;               // [2] steps x 4 waves: the staged rows that are not finite
-    static constexpr int BYTES = FLAGS + 2 * 4 * 4;
+    static constexpr int SCALES = FLAGS + 2 * 4 * 4;     // [2] slots: K's two groups, then V's, one a wave
+    static constexpr int BYTES = SCALES + (SCALED ? 2 * 4 * RowScales::GROUP : 0);
 };
 
 // Bits below n (0 .. 64 and beyond either end).
@@ -53,7 +54,8 @@ __device__ __forceinline__ void lds_barrier() {
 template <int D, bool FP8, bool SPLITP, class Source, class Sees, class Queries>
 __device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds, int key0, int key1, const Source& src,
                                             const Sees& sees, const Queries& queries, int wave, int lane) {
-    using L = RowsLds<D, FP8>;
+    constexpr bool SCALED = Source::SCALED;
+    using L = RowsLds<D, FP8, SCALED>;
     constexpr int ROW = Tile<D, FP8>::ROW, LOADS = Tile<D, FP8>::LOADS16;
     // waves 0, 1 stage K's rows, 2, 3 V's, 16 each
     const bool is_k = wave < 2;
@@ -64,6 +66,11 @@ __device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds
         const int key = key0 + i * KEYS + part;
         if (is_k) st.rows16(src.k_rows(key), k_ring + slot * L::TILE + part * ROW);
         else st.rows16(src.v_rows(key), v_ring + slot * L::TILE + part * ROW);
+        if constexpr (SCALED) load_scales(is_k ? src.k_scales(key) : src.v_scales(key), lane, lds + L::SCALES + (slot * 4 + wave) * RowScales::GROUP);
+    };
+    auto scales = [&](int slot, int groups) {
+        if constexpr (SCALED) return RowScales{lds + L::SCALES + (slot * 4 + groups) * RowScales::GROUP};
+        else return NoScales{};
     };
     if (key0 >= key1) return;
     const int n = (key1 - key0 + KEYS - 1) / KEYS;
@@ -91,14 +98,17 @@ __device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds
             seen = sees.seen(key);
         }
         v16f s;
-        if (some) R.template weights<PARTLY>(k, seen, s);
+        if (some) R.template weights<PARTLY>(k, seen, s, scales(slot, 0));
         if (PARTLY && bad) {
             if (some) R.add_not_finite(v, bad, seen);
             lds_barrier();
             if (!is_k) rows_made_finite<D, FP8, LOADS>(v + part * ROW, lane);
             lds_barrier();
         }
-        if (some) R.values(v, s);
+        if (some) {
+            scales(slot, 2).template apply<PARTLY>(s, lane);
+            R.values(v, s);
+        }
     };
     const int clean = sees.all_before() - key0 < 0 ? 0 : (sees.all_before() - key0) / KEYS;
     int i = 0;

@@ -27,6 +27,7 @@ struct TreeArgs {
     int64_t qs;                     // elements between tokens
     const void *k_pages, *v_pages;
     const float *k_scale, *v_scale; // per KV head (E4M3 caches), or NULL
+    const float *k_rows, *v_rows;   // per row of the cache (E4M3 caches with a scale a token), or NULL
     const int32_t* table;
     int width;
     const int32_t *lens, *cu;
@@ -146,9 +147,11 @@ struct Range {
 
 // K or V rows of one sequence and KV head in pages of (1 << page_shift) rows.
 // A page number outside the pool gives rows of zeros.
-template <int D, bool FP8>
+template <int D, int FMT>
 struct PagedRows {
+    static constexpr bool FP8 = FMT != NQ_KV_BF16, SCALED = FMT == NQ_KV_E4M3_TOKEN;
     const char *k, *v;
+    const float *ks, *vs;           // planes of the rows' scales (SCALED)
     const int32_t* table;           // this sequence's row
     int64_t pages;
     int64_t page_bytes, head_bytes; // bytes of a page; of the heads before this one
@@ -163,6 +166,16 @@ struct PagedRows {
     }
     __device__ __forceinline__ v4i k_rows(int key) const { return rows(k, key); }
     __device__ __forceinline__ v4i v_rows(int key) const { return rows(v, key); }
+    // The 16 rows' scales (zeros where there is no row), at the same place of their plane.
+    __device__ __forceinline__ v4i scales(const float* base, int key) const {
+        int rows = total - key < 16 ? total - key : 16;
+        const int64_t page = rows > 0 ? uniform(table, key >> page_shift) : -1;
+        if (page < 0 || page >= pages) rows = 0;
+        const int64_t at = rows > 0 ? (page * page_bytes + head_bytes) / k_stride + (key & ((1 << page_shift) - 1)) : 0;
+        return rows_rsrc(base + at, rows, 4, 4);
+    }
+    __device__ __forceinline__ v4i k_scales(int key) const { return scales(ks, key); }
+    __device__ __forceinline__ v4i v_scales(int key) const { return scales(vs, key); }
 };
 
 struct TreeSees {
@@ -204,11 +217,14 @@ __device__ __forceinline__ int64_t tree_out(const TreeArgs& a, const Seq& s, int
     return (s.t0 + row / a.group) * a.hq + kvh * a.group + row % a.group;
 }
 
-template <int D, bool FP8>
-__device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const Seq& s, int b, int kvh) {
-    PagedRows<D, FP8> src;
+template <int D, int FMT>
+__device__ __forceinline__ PagedRows<D, FMT> paged_rows(const TreeArgs& a, const Seq& s, int b, int kvh) {
+    constexpr bool FP8 = FMT != NQ_KV_BF16;
+    PagedRows<D, FMT> src;
     src.k = (const char*)a.k_pages;
     src.v = (const char*)a.v_pages;
+    src.ks = a.k_rows;
+    src.vs = a.v_rows;
     src.table = a.table + (int64_t)b * a.width;
     src.pages = a.pages;
     src.head_bytes = ((int64_t)kvh << a.page_shift) * Tile<D, FP8>::ROW;
@@ -223,8 +239,9 @@ __device__ __forceinline__ PagedRows<D, FP8> paged_rows(const TreeArgs& a, const
 // 50 us in an E4M3 cache (10 vector instructions a product, 4 of them the
 // decode; 52 MB of parts, and the join below reads them in 12 us).  With half as
 // many parts, one workgroup a CU, 53 + 9 us.
-template <int D, bool FP8, bool BF16OUT>
+template <int D, int FMT, bool BF16OUT>
 __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tree_rows_kernel(TreeArgs a) {
+    constexpr bool FP8 = FMT != NQ_KV_BF16;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the row tiles of one range are 8 apart: on the same XCD, whose L2 gives all but the first their keys
@@ -236,11 +253,11 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tre
     if (rt * 128 >= s.n * a.group) return;
     if (r.first == range && kvh == 0 && rt == 0 && threadIdx.x == 0 && a.want > 0) part_ranges(a, D)[r.b] = make_int2(r.first, r.parts);
     Rows<D, FP8, !BF16OUT> R;
-    R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
+    R.init(lane, a.scale * (FMT == NQ_KV_E4M3 ? a.k_scale[kvh] : 1.0f) * LOG2E);
     const int row = (rt * 4 + wave) * 32 + (lane & 31);
     TreeSees sees = tree_sees(a, s, row);
     if ((rt * 4 + wave) * 32 >= s.n * a.group) sees.none = 0;
-    const PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
+    const PagedRows<D, FMT> src = paged_rows<D, FMT>(a, s, r.b, kvh);
     auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
     attend_rows(R, (lds_ptr)smem, r.key0, r.key1, src, sees, queries, wave, lane);
     const float l = halves_sum(R.l), ref = R.m == -INFINITY ? 0.f : R.reference();
@@ -248,7 +265,7 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tre
     if (row >= s.n * a.group) return;
     const bool only = r.parts == 1;
     const int64_t out = tree_out(a, s, kvh, row), part = part_row(a, range, kvh, row);
-    const float f = only ? inverse_sum(l) * (FP8 ? a.v_scale[kvh] : 1.0f) : 1.0f;
+    const float f = only ? inverse_sum(l) * (FMT == NQ_KV_E4M3 ? a.v_scale[kvh] : 1.0f) : 1.0f;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -265,8 +282,9 @@ __global__ __launch_bounds__(256, D == 256 ? 2 : D == 128 ? 3 : 4) void attn_tre
 
 // Up to 32 rows: the waves take different keys.  Bound by HBM; 40 sequences of
 // up to 8191 keys, 32 / 8 heads of 128, 34 us for 120 MB.
-template <int D, bool FP8, bool BF16OUT>
+template <int D, int FMT, bool BF16OUT>
 __global__ __launch_bounds__(256) void attn_tree_keys_kernel(TreeArgs a) {
+    constexpr bool FP8 = FMT != NQ_KV_BF16;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kvh = blockIdx.x % a.hkv, range = blockIdx.x / a.hkv;
@@ -275,14 +293,14 @@ __global__ __launch_bounds__(256) void attn_tree_keys_kernel(TreeArgs a) {
     const Seq s(a, r.b);
     if (r.first == range && kvh == 0 && threadIdx.x == 0 && a.want > 0) part_ranges(a, D)[r.b] = make_int2(r.first, r.parts);
     Rows<D, FP8, !BF16OUT> R;
-    R.init(lane, a.scale * (FP8 ? a.k_scale[kvh] : 1.0f) * LOG2E);
+    R.init(lane, a.scale * (FMT == NQ_KV_E4M3 ? a.k_scale[kvh] : 1.0f) * LOG2E);
     const int row = lane & 31;
     const TreeSees sees = tree_sees(a, s, row);
-    PagedRows<D, FP8> src = paged_rows<D, FP8>(a, s, r.b, kvh);
+    PagedRows<D, FMT> src = paged_rows<D, FMT>(a, s, r.b, kvh);
     src.total = r.key1;                                 // keys past the range: no rows, zeros
     auto queries = [&] { R.load_q(tree_query(a, s, kvh, row, D)); };
     const bool only = r.parts == 1;
-    const float vs = FP8 ? a.v_scale[kvh] : 1.0f;
+    const float vs = FMT == NQ_KV_E4M3 ? a.v_scale[kvh] : 1.0f;
     auto emit = [&](int i, int col, const v4f& x, float ref, float l) {
         const int64_t out = tree_out(a, s, kvh, i);
         if (only) {
@@ -384,19 +402,20 @@ __global__ __launch_bounds__(WAVES * 64) void attn_tree_join_kernel(TreeArgs a) 
 // as two workgroups of four.)
 constexpr int tile_rows(int64_t rows) { return rows <= 32 ? 32 : 128; }
 
-template <int D, bool FP8, bool BF16OUT>
+template <int D, int FMT, bool BF16OUT>
 hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
+    constexpr bool FP8 = FMT != NQ_KV_BF16, SCALED = FMT == NQ_KV_E4M3_TOKEN;
     const unsigned units = (unsigned)(a.want + a.seqs) * a.hkv;
     hipError_t e;
     if (tile_rows(a.max_q * a.group) == 32) {
-        constexpr int LDS = KeysLds<D, FP8>::BYTES;
-        auto kernel = attn_tree_keys_kernel<D, FP8, BF16OUT>;
+        constexpr int LDS = KeysLds<D, FP8, SCALED>::BYTES;
+        auto kernel = attn_tree_keys_kernel<D, FMT, BF16OUT>;
         static LdsLimit limit;
         if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
         kernel<<<units, 256, LDS, stream>>>(a);
     } else {
-        constexpr int LDS = RowsLds<D, FP8>::BYTES;
-        auto kernel = attn_tree_rows_kernel<D, FP8, BF16OUT>;
+        constexpr int LDS = RowsLds<D, FP8, SCALED>::BYTES;
+        auto kernel = attn_tree_rows_kernel<D, FMT, BF16OUT>;
         static LdsLimit limit;
         if ((e = limit.raise((const void*)kernel, LDS)) != hipSuccess) return e;
         kernel<<<(units + 7) / 8 * 8 * a.row_tiles, 256, LDS, stream>>>(a);
@@ -410,6 +429,15 @@ hipError_t go_tree(const TreeArgs& a, hipStream_t stream) {
         return hipGetLastError();
     }
     return hipSuccess;
+}
+
+template <int D>
+hipError_t go_tree(int fmt, bool bf16_out, const TreeArgs& a, hipStream_t stream) {
+    switch (fmt) {
+        case NQ_KV_BF16: return bf16_out ? go_tree<D, NQ_KV_BF16, true>(a, stream) : go_tree<D, NQ_KV_BF16, false>(a, stream);
+        case NQ_KV_E4M3: return bf16_out ? go_tree<D, NQ_KV_E4M3, true>(a, stream) : go_tree<D, NQ_KV_E4M3, false>(a, stream);
+        default: return bf16_out ? go_tree<D, NQ_KV_E4M3_TOKEN, true>(a, stream) : go_tree<D, NQ_KV_E4M3_TOKEN, false>(a, stream);
+    }
 }
 
 }  // namespace attn
@@ -468,7 +496,7 @@ int64_t attn_tree_workspace_bytes(int64_t seqs, int64_t max_q, int64_t hq, int64
     return most;
 }
 
-hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+hipError_t launch_attn_tree(int kv_fmt, const uint16_t* q, int64_t q_stride, const void* k_pages, const void* v_pages,
                             const float* k_scale, const float* v_scale, const int32_t* table, int64_t width,
                             const int32_t* lens, const int32_t* cu_q, const uint64_t* masks, int64_t seqs, int64_t max_q,
                             int64_t t, int64_t hq, int64_t hkv, int64_t d, int64_t page_size, int64_t pages,
@@ -480,19 +508,15 @@ hipError_t launch_attn_tree(bool fp8, const uint16_t* q, int64_t q_stride, const
         const int64_t fit = (workspace_bytes - seqs * 8) / range_bytes(max_q, hq, d) - seqs;
         p.want = fit > 0 ? (int)fit : 0;
     }
-    const TreeArgs a{q, q_stride, k_pages, v_pages, fp8 ? k_scale : nullptr, fp8 ? v_scale : nullptr, table, (int)width, lens,
-                     cu_q, masks, (int)seqs, (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size),
-                     pages, scale, o, lse, reinterpret_cast<float*>(workspace), p.want, p.least, p.step, p.row_tiles};
+    const bool heads = kv_fmt == NQ_KV_E4M3, rows = kv_fmt == NQ_KV_E4M3_TOKEN;
+    const TreeArgs a{q, q_stride, k_pages, v_pages, heads ? k_scale : nullptr, heads ? v_scale : nullptr,
+                     rows ? k_scale : nullptr, rows ? v_scale : nullptr, table, (int)width, lens, cu_q, masks, (int)seqs,
+                     (int)max_q, t, (int)hq, (int)hkv, (int)(hq / hkv), __builtin_ctzll(page_size), pages, scale, o, lse,
+                     reinterpret_cast<float*>(workspace), p.want, p.least, p.step, p.row_tiles};
     switch (d) {
-        case 64:
-            return fp8 ? (bf16_out ? go_tree<64, true, true>(a, stream) : go_tree<64, true, false>(a, stream))
-                       : (bf16_out ? go_tree<64, false, true>(a, stream) : go_tree<64, false, false>(a, stream));
-        case 128:
-            return fp8 ? (bf16_out ? go_tree<128, true, true>(a, stream) : go_tree<128, true, false>(a, stream))
-                       : (bf16_out ? go_tree<128, false, true>(a, stream) : go_tree<128, false, false>(a, stream));
-        default:
-            return fp8 ? (bf16_out ? go_tree<256, true, true>(a, stream) : go_tree<256, true, false>(a, stream))
-                       : (bf16_out ? go_tree<256, false, true>(a, stream) : go_tree<256, false, false>(a, stream));
+        case 64: return go_tree<64>(kv_fmt, bf16_out, a, stream);
+        case 128: return go_tree<128>(kv_fmt, bf16_out, a, stream);
+        default: return go_tree<256>(kv_fmt, bf16_out, a, stream);
     }
 }
 

@@ -13,35 +13,12 @@
 #include "nq.h"
 #include "nq_attn_launch.h"
 #include "nq_device.h"
+#include "nq_pages.h"
 
 namespace nq {
 namespace {
 
 constexpr int POOL_THREADS = 1024;
-
-// The sequence that packed row t belongs to: the last b with cu[b] <= t.
-__device__ __forceinline__ int owner(const int32_t* cu, int seqs, int64_t t) {
-    int lo = 0, hi = seqs;                               // cu[lo] <= t < cu[hi] where cu is in order
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (cu[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-// The page and slot of token `at` of a sequence, or page -1 where the table
-// has none inside the pool.
-__device__ __forceinline__ int64_t page_of(const int32_t* table, int64_t width, int64_t pages, int shift, int64_t at) {
-    if (at < 0 || (at >> shift) >= width) return -1;
-    const int64_t p = table[at >> shift];
-    return p < 0 || p >= pages ? -1 : p;
-}
-
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-    if (fabsf(a) < 448.f && fabsf(b) < 448.f && fabsf(c) < 448.f && fabsf(d) < 448.f) return f32x4_to_e4m3_hw(a, b, c, d);
-    return f32_to_e4m3_sat(a) | f32_to_e4m3_sat(b) << 8 | f32_to_e4m3_sat(c) << 16 | f32_to_e4m3_sat(d) << 24;
-}
 
 struct AppendArgs {
     const uint16_t *k, *v;
@@ -329,6 +306,7 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(char* pool, int64_t plane_
 // row i moves to lies below every row read after it.  100 sequences of up to 64
 // drafts, 32 planes of 4 heads of 256 in BF16: 19 us; one 5 us.
 constexpr int MOVE_ROWS = 64, MOVE_PLANES = 4, MOVE_BATCH = 4;
+template <class Piece>               // 16 bytes, or the 4 of a scale's row
 __global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t plane_bytes, int planes, int hkv, int shift,
                                                          int row_bytes, int64_t pages, const int32_t* table, int64_t width,
                                                          const int32_t* lens, const int32_t* accept, const int32_t* cu,
@@ -339,7 +317,7 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t pla
     int64_t a0 = cu[b], a1 = cu[b + 1];
     a0 = a0 < 0 ? 0 : a0 > accepted ? accepted : a0;
     a1 = a1 < a0 ? a0 : a1 > accepted ? accepted : a1;
-    const int n = (int)(a1 - a0 > MOVE_ROWS ? MOVE_ROWS : a1 - a0), len = lens[b], per = row_bytes / 16;
+    const int n = (int)(a1 - a0 > MOVE_ROWS ? MOVE_ROWS : a1 - a0), len = lens[b], per = row_bytes / (int)sizeof(Piece);
     if (len < 0 || plane0 >= planes) return;
     pool += plane0 * plane_bytes;
     auto place = [&](int64_t at) -> int64_t {
@@ -348,7 +326,7 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t pla
     };
     for (int p0 = 0; p0 < n * per; p0 += 64 * MOVE_BATCH) {
         int64_t src[MOVE_BATCH], dst[MOVE_BATCH];
-        v4u x[MOVE_BATCH][MOVE_PLANES];
+        Piece x[MOVE_BATCH][MOVE_PLANES];
 #pragma unroll
         for (int j = 0; j < MOVE_BATCH; ++j) {
             const int p = p0 + j * 64 + lane, i = p / per;
@@ -358,21 +336,21 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t pla
                 src[j] = place((int64_t)len + from);
                 dst[j] = place((int64_t)len + i);
                 if (src[j] < 0) dst[j] = -1;
-                src[j] += p % per * 16;
-                if (dst[j] >= 0) dst[j] += p % per * 16;
+                src[j] += p % per * (int)sizeof(Piece);
+                if (dst[j] >= 0) dst[j] += p % per * (int)sizeof(Piece);
             }
         }
 #pragma unroll
         for (int j = 0; j < MOVE_BATCH; ++j)
 #pragma unroll
             for (int q = 0; q < MOVE_PLANES; ++q)
-                if (dst[j] >= 0 && plane0 + q < planes) x[j][q] = *reinterpret_cast<const v4u*>(pool + q * plane_bytes + src[j]);
+                if (dst[j] >= 0 && plane0 + q < planes) x[j][q] = *reinterpret_cast<const Piece*>(pool + q * plane_bytes + src[j]);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int j = 0; j < MOVE_BATCH; ++j)
 #pragma unroll
             for (int q = 0; q < MOVE_PLANES; ++q)
-                if (dst[j] >= 0 && plane0 + q < planes) *reinterpret_cast<v4u*>(pool + q * plane_bytes + dst[j]) = x[j][q];
+                if (dst[j] >= 0 && plane0 + q < planes) *reinterpret_cast<Piece*>(pool + q * plane_bytes + dst[j]) = x[j][q];
     }
 }
 
@@ -432,9 +410,10 @@ hipError_t launch_kv_compact(void* pool, int64_t planes, int64_t plane_bytes, in
                              int64_t row_bytes, int64_t pages, const int32_t* table, int64_t width, const int32_t* lens,
                              const int32_t* accept, const int32_t* cu_accept, int64_t seqs, int64_t accepted,
                              hipStream_t stream) {
-    kv_compact_kernel<<<dim3((unsigned)(seqs * hkv), (unsigned)((planes + 4 * MOVE_PLANES - 1) / (4 * MOVE_PLANES))), 256, 0,
-                        stream>>>((char*)pool, plane_bytes, (int)planes, (int)hkv, shift_of(page_size), (int)row_bytes, pages,
-                                  table, width, lens, accept, cu_accept, accepted);
+    const dim3 grid((unsigned)(seqs * hkv), (unsigned)((planes + 4 * MOVE_PLANES - 1) / (4 * MOVE_PLANES)));
+    auto kernel = row_bytes == 4 ? kv_compact_kernel<uint32_t> : kv_compact_kernel<v4u>;
+    kernel<<<grid, 256, 0, stream>>>((char*)pool, plane_bytes, (int)planes, (int)hkv, shift_of(page_size), (int)row_bytes, pages,
+                                     table, width, lens, accept, cu_accept, accepted);
     return hipGetLastError();
 }
 

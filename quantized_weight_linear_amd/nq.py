@@ -22,7 +22,9 @@ NQ_W_Q4G64_F16S, NQ_W_Q8G32_F16S, NQ_W_Q8G64_F16S, NQ_W_MXFP8_G32, NQ_W_BF16 = r
 NQ_W_Q3G64_F16S, NQ_W_Q5G64_F16S, NQ_W_Q6G64_F16S = 5, 6, 7
 NQ_ROUTE_BF16, NQ_ROUTE_A8, NQ_ROUTE_A8_DECODE = 0, 1, 2
 NQ_A8_PREFILL, NQ_A8_DECODE = 1, 2
-NQ_KV_BF16, NQ_KV_E4M3 = 0, 1
+NQ_KV_BF16, NQ_KV_E4M3, NQ_KV_E4M3_TOKEN = 0, 1, 3
+NQ_ACT_BF16, NQ_ACT_INT8_G64, NQ_ACT_E4M3_B128 = 0, 1, 2
+NQ_ROPE_HALVES, NQ_ROPE_PAIRS = 0, 1
 
 # every entry point the header declares: name -> (restype, argtypes)
 _P, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
@@ -56,6 +58,12 @@ SIGNATURES = {
     "nq_linear_q8g64": (_I, [_P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _I, _P, _P, _I64, _P]),
     "nq_unpack_q4_to_int8": (_I, [_P, _I64, _I64, _P, _P]),
     "nq_linear_q4g64": (_I, [_P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _P, _I, _P, _P, _I64, _P]),
+    "nq_quantize_act_fp8_b128": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "nq_rmsnorm": (_I, [_I, _P, _I64, _P, _P, _P, _F, _F, _I64, _I64, _P, _P, _P]),
+    "nq_gemm_fp8_b128_workspace_bytes": (_I64, [_I64] * 3),
+    "nq_gemm_fp8_b128": (_I, [_P] * 4 + [_I64] * 5 + [_I, _P, _P, _I64, _P]),
+    "nq_kv_append_rope": (_I, [_I] + [_P, _I64] * 3 + [_P, _P, _F, _F, _P, _P, _I64, _I, _P, _P, _P, _I64, _P, _P] + [_I64] * 7 +
+                          [_P, _I64, _P, _I64, _P, _P, _P]),
     "nq_attn_prompt": (_I, [_P, _I64] * 3 + [_P, _P] + [_I64] * 6 + [_F, _I, _P, _P, _P]),
     "nq_kv_append": (_I, [_I] + [_P, _I64] * 2 + [_P, _P, _P, _I64, _P, _P] + [_I64] * 6 + [_P, _P, _P]),
     "nq_attn_tree_workspace_bytes": (_I64, [_I64] * 6),
@@ -207,6 +215,34 @@ def _ws(workspace):
     return (_ptr(workspace), workspace.numel()) if workspace is not None else (None, 0)
 
 
+def nq_quantize_act_fp8_b128(x, T, K, codes, scale):
+    _size(x, 2 * T * K, "x"); _size(codes, T * K, "codes"); _size(scale, 4 * T * -(-K // 128), "scale")
+    _check(lib().nq_quantize_act_fp8_b128(_ptr(x), T, K, _ptr(codes), _ptr(scale), _stream(x)), "nq_quantize_act_fp8_b128")
+
+
+_ACT_GROUP = {NQ_ACT_INT8_G64: 64, NQ_ACT_E4M3_B128: 128}
+
+
+def nq_rmsnorm(act_fmt, x, weight, eps, y, y_scale=None, residual=None, residual_out=None, weight_bias=0.0):
+    """x [T][K], rows back to back or a slice of longer ones; residual_out may be residual."""
+    if x.dim() != 2 or x.dtype not in _TWO_BYTES:
+        raise ValueError("x: BF16 rows [T][K] expected")
+    t, k = x.shape
+    stride = x.stride(0) if t > 1 else k
+    if k > 1 and x.stride(1) != 1:
+        raise ValueError("x: a row's columns must be back to back")
+    group = _ACT_GROUP.get(act_fmt)
+    for z, what in ((y, "y"), (residual, "residual"), (residual_out, "residual_out")):
+        if z is not None and (z.shape != x.shape or not z.is_contiguous() or z.dtype not in
+                              (_ONE_BYTE if what == "y" and group else _TWO_BYTES)):
+            raise ValueError(f"{what}: contiguous, the shape of x and the format's type expected")
+    if weight is not None and (weight.dtype not in _TWO_BYTES or weight.numel() != k):
+        raise ValueError("weight: BF16 [K] expected")
+    sp = _floats(y_scale, t * -(-k // group), "y_scale") if group else None
+    _check((_lib or lib()).nq_rmsnorm(act_fmt, x.data_ptr() if x.numel() else None, stride, _ptr(residual), _ptr(residual_out),
+                                      _ptr(weight), weight_bias, eps, t, k, _ptr(y), sp, _stream(x)), "nq_rmsnorm")
+
+
 def nq_gemv_fp8row(w, w_scale, x, T, N, K, y, workspace=None):
     _size(w, N * K, "w"); _size(w_scale, 2 * N, "w_scale"); _size(x, 2 * T * K, "x")
     _size(y, T * N * y.element_size(), "y")
@@ -239,6 +275,28 @@ def nq_gemm_fp8row(x, w, w_scale, M, N, K, a_codes, a_scale, y):
     _size(a_codes, M * K, "a_codes"); _size(a_scale, 4 * M, "a_scale"); _size(y, M * N * y.element_size(), "y")
     _check(lib().nq_gemm_fp8row(_ptr(x), _ptr(w), _ptr(w_scale), M, N, K, _ptr(a_codes), _ptr(a_scale),
                                 _out_dt(y), _ptr(y), _stream(x, w)), "nq_gemm_fp8row")
+
+
+def nq_gemm_fp8_b128_workspace_bytes(M, N, K):
+    return lib().nq_gemm_fp8_b128_workspace_bytes(M, N, K)
+
+
+def alloc_gemm_fp8_b128_workspace(M, N, K, device):
+    """A workspace for nq_gemm_fp8_b128 at these sizes, or None where it needs none."""
+    n = nq_gemm_fp8_b128_workspace_bytes(M, N, K)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def nq_gemm_fp8_b128(a_codes, a_scale, w, wsi, M, N, K, y, workspace=None):
+    """wsi is [ceil(N/128)][ceil(K/128)]; a_scale [M][ceil(K/128)]."""
+    gr, gc = wsi.shape if wsi.dim() == 2 else (-1, -1)
+    _size(a_codes, M * K, "a_codes"); _size(w, N * K, "w"); _size(y, M * N * y.element_size(), "y")
+    _size(a_scale, 4 * M * -(-K // 128), "a_scale")
+    if y.dtype not in _OUT_TYPES:
+        raise ValueError("y: float32 or bfloat16 expected")
+    wp, wb = _ws(workspace)
+    _check((_lib or lib()).nq_gemm_fp8_b128(_ptr(a_codes), _floats(a_scale, 0, "a_scale"), _ptr(w), _floats(wsi, 0, "wsi"), M, N, K,
+                                            gr, gc, _OUT_TYPES[y.dtype], _ptr(y), wp, wb, _stream(a_codes, w)), "nq_gemm_fp8_b128")
 
 
 def nq_linear_q8g64(x, T, w_q, w_scale, N, K, allow_a8, a_q_ws, a_scale_ws, y, workspace=None):
@@ -418,12 +476,18 @@ def _planes(fmt, k_pages, v_pages, hkv, d):
     shape = k_pages.shape
     if len(shape) != 4 or shape != v_pages.shape or shape[1] != hkv or shape[3] != d:
         raise ValueError("pages: [pages][Hkv][page_size][D] expected, the same for keys and values")
-    types = _ONE_BYTE if fmt == NQ_KV_E4M3 else _TWO_BYTES
+    types = _TWO_BYTES if fmt == NQ_KV_BF16 else _ONE_BYTE
     if k_pages.dtype not in types or v_pages.dtype not in types:
         raise ValueError("pages: one byte an element for E4M3, two for BF16")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("pages: tensors must be contiguous")
     return k_pages.data_ptr(), v_pages.data_ptr(), shape[2], shape[0]
+
+
+def _scales(fmt, k_scale, v_scale, pages):
+    """Addresses of the cache's scales: none, one a KV head, or one a row."""
+    n = 0 if fmt == NQ_KV_BF16 else pages.shape[1] if fmt == NQ_KV_E4M3 else pages.numel() // max(1, pages.shape[3])
+    return _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale")
 
 
 def _out(o, shape):
@@ -465,6 +529,41 @@ def nq_kv_append(fmt, k, v, k_scale, v_scale, page_table, lens, cu, k_pages, v_p
                                         kpp, vpp, _stream(k_pages)), "nq_kv_append")
 
 
+def nq_kv_append_rope(fmt, q, k, v, positions, inv_freq, rope, k_scale, v_scale, page_table, lens, cu, q_out, k_pages, v_pages,
+                      q_weight=None, k_weight=None, weight_bias=0.0, eps=1e-6, k_out=None):
+    """q (and q_out) None: keys and values only.  inv_freq None: nothing is turned; else its 2 numel first columns are."""
+    kh = k.shape
+    kp, ks = _rows(k, kh, "k")
+    vp, vs = _rows(v, kh, "v")
+    if v.shape != kh:
+        raise ValueError("k and v must have the same shape")
+    t, hkv, d = kh
+    qp, qs, qop, qos, hq = None, 0, None, 0, hkv
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        if q.shape != (t, hq, d) or q_out is None or q_out.shape != q.shape:
+            raise ValueError("q and q_out: [T][Hq][D] with k's T and D expected")
+        (qp, qs), (qop, qos) = _rows(q, q.shape, "q"), _rows(q_out, q.shape, "q_out")
+    kop, kos = None, 0
+    if k_out is not None:
+        if k_out.shape != kh:
+            raise ValueError("k_out: the shape of k expected")
+        kop, kos = _rows(k_out, kh, "k_out")
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype not in _TWO_BYTES or w.numel() != d):
+            raise ValueError(f"{what}: BF16 [D] expected")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    fp = None if inv_freq is None else _floats(inv_freq, rot // 2, "inv_freq")
+    pp = _ints(positions, t, "positions") if rot else None
+    tp, b, width = _table(page_table)
+    kpp, vpp, ps, pages = _planes(fmt, k_pages, v_pages, hkv, d)
+    ksp, vsp = _scales(fmt, k_scale, v_scale, k_pages)
+    _check((_lib or lib()).nq_kv_append_rope(fmt, qp, qs, kp, ks, vp, vs, _ptr(q_weight), _ptr(k_weight), weight_bias, eps, pp, fp,
+                                             rot, rope, ksp, vsp, tp, width, _ints(lens, b, "lens"), _ints(cu, b + 1, "cu"), b, t,
+                                             hq, hkv, d, ps, pages, qop, qos, kop, kos, kpp, vpp, _stream(k_pages)),
+           "nq_kv_append_rope")
+
+
 def nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len):
     return lib().nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len)
 
@@ -483,12 +582,11 @@ def nq_attn_tree(fmt, q, k_pages, v_pages, k_scale, v_scale, page_table, lens, c
     hkv = k_pages.shape[1] if k_pages.dim() == 4 else 0
     tp, b, width = _table(page_table)
     kpp, vpp, ps, pages = _planes(fmt, k_pages, v_pages, hkv, d)
-    n = hkv if fmt == NQ_KV_E4M3 else 0
+    kp, vp = _scales(fmt, k_scale, v_scale, k_pages)
     wp, wb = _ws(workspace)
     op, out = _out(o, qh)
     lp = None if lse is None else _floats(lse, t * hq, "lse")
-    _check((_lib or lib()).nq_attn_tree(fmt, qp, qs, kpp, vpp, _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale"),
-                                        tp, width, _ints(lens, b, "lens"), _ints(cu_q, b + 1, "cu_q"),
+    _check((_lib or lib()).nq_attn_tree(fmt, qp, qs, kpp, vpp, kp, vp, tp, width, _ints(lens, b, "lens"), _ints(cu_q, b + 1, "cu_q"),
                                         _ints(tree_mask, t, "tree_mask", _INT64), b, max_q, t, hq, hkv, d, ps, pages,
                                         max_len, scale, out, op, lp, wp, wb, _stream(q)), "nq_attn_tree")
 

@@ -1,0 +1,799 @@
+"""The norm, the block-scaled FP8 product, the rotated append and attention over a cache with a scale a row, against plain
+64-bit forms.  Tolerances count roundings: half a step of BF16 is 2^-8 of the value, of E4M3 2^-4 (2^-10 below its
+smallest normal), of FP32 2^-24."""
+
+import math
+
+import pytest
+import torch
+
+from quantized_weight_linear_amd import nq
+
+pytestmark = pytest.mark.gpu
+DEV, BF, F8 = "cuda", torch.bfloat16, torch.float8_e4m3fn
+U32, U16, U8 = 2.0 ** -24, 2.0 ** -8, 2.0 ** -4
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def rand(g, *shape, by=1.0):
+    return (torch.randn(shape, generator=g, device=DEV) * by).to(BF)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def starts(ns):
+    return i32([sum(ns[:i]) for i in range(len(ns) + 1)])
+
+
+def within(got, ref, tol):
+    got, ref = got.double(), ref.double()
+    off = (got - ref).abs()
+    assert bool((off <= tol).all()), (float((off - tol).max()), int((off > tol).sum()), off.numel())
+
+
+def same_bits(a, b):
+    assert a.dtype == b.dtype and a.shape == b.shape
+    assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ---- norm -----------------------------------------------------------------------------------------------------------
+
+def norm64(x, residual, weight, bias, eps):
+    h = x if residual is None else (x.float() + residual.float()).to(BF)
+    d = h.double()
+    w = bias + (weight.double() if weight is not None else 1.0)
+    return h, d / torch.sqrt(d.square().mean(1, keepdim=True) + eps) * w
+
+
+def run_norm(fmt, x, weight, eps=1e-6, residual=None, bias=0.0, in_place=False):
+    t, k = x.shape
+    group = {nq.NQ_ACT_BF16: 0, nq.NQ_ACT_INT8_G64: 64, nq.NQ_ACT_E4M3_B128: 128}[fmt]
+    y = torch.empty((t, k), dtype=torch.uint8 if group else BF, device=DEV)
+    scale = torch.full((t, -(-k // group)), math.nan, device=DEV) if group else None
+    out = None if residual is None else residual if in_place else torch.empty_like(residual)
+    nq.nq_rmsnorm(fmt, x, weight, eps, y, scale, residual=residual, residual_out=out, weight_bias=bias)
+    return y, scale, out
+
+
+def check_norm(fmt, x, weight, residual=None, bias=0.0, eps=1e-6, in_place=False):
+    kept = None if residual is None else residual.clone()
+    y, scale, out = run_norm(fmt, x, weight, eps, residual, bias, in_place)
+    h, ref = norm64(x, kept, weight, bias, eps)
+    if residual is not None:
+        same_bits(out, h)                                   # the FP32 sum rounded once
+    fp32 = 4 * U32 * ref.abs() + 2.0 ** -149                # y in FP32: h r, w + bias and their product, each rounded
+    if fmt == nq.NQ_ACT_BF16:
+        return within(y, ref, U16 * ref.abs() + 2 * fp32)
+    group, top = (64, 127.0) if fmt == nq.NQ_ACT_INT8_G64 else (128, 448.0)
+    for g in range(scale.shape[1]):
+        part = slice(group * g, min(x.shape[1], group * g + group))
+        s = ref[:, part].abs().amax(1, keepdim=True) / top
+        within(scale[:, g:g + 1], s, 6 * U32 * s + 2.0 ** -149)
+        v, by = ref[:, part], scale[:, g:g + 1].double()
+        code = y[:, part].view(torch.int8).double() if group == 64 else y[:, part].view(F8).double()
+        half = 0.5 if group == 64 else (v / by).abs().mul(U8).clamp(min=2.0 ** -10)
+        within(code, v / by, half + (v / by).abs() * 8 * U32)
+
+
+SHAPES = [(1, 64), (1, 128), (3, 192), (5, 448), (4, 512), (9, 576), (2, 1024), (7, 1088), (1, 2048), (3, 2112), (33, 5120), (1, 4160),
+          (2, 6144), (2, 8256), (3, 12288), (2, 12352), (2, 16384), (3, 17408), (1, 24640), (2, 32768), (1000, 256)]
+
+
+@pytest.mark.parametrize("fmt", [nq.NQ_ACT_BF16, nq.NQ_ACT_INT8_G64, nq.NQ_ACT_E4M3_B128])
+@pytest.mark.parametrize("t,k", SHAPES)
+def test_norm(fmt, t, k):
+    g = gen(t * 131 + k)
+    x, w = rand(g, t, k), rand(g, k, by=0.3)
+    check_norm(fmt, x, w, rand(g, t, k, by=3.0), bias=1.0, in_place=k % 128 == 0)
+    check_norm(fmt, x, None if k % 128 else w)
+
+
+@pytest.mark.parametrize("fmt,ks", [(nq.NQ_ACT_BF16, [8, 24, 72, 520, 1000, 5128, 9992]), (nq.NQ_ACT_E4M3_B128, [16, 48, 144, 400, 1040, 2064, 5136])])
+def test_norm_widths_that_end_inside_a_block(fmt, ks):
+    for k in ks:
+        g = gen(k)
+        check_norm(fmt, rand(g, 6, k), rand(g, k), rand(g, 6, k))
+
+
+def test_norm_rows_of_a_wider_matrix():
+    g = gen(5)
+    wide, w = rand(g, 9, 4096), rand(g, 1024)
+    for fmt in (nq.NQ_ACT_BF16, nq.NQ_ACT_E4M3_B128):
+        check_norm(fmt, wide[:, 512:1536], w, rand(g, 9, 1024))
+
+
+@pytest.mark.parametrize("by", [1e-36, 1e-18, 1e18, 1e37])
+def test_norm_of_very_small_and_large_rows(by):
+    """Sums of squares beyond FP32 either way."""
+    g = gen(6)
+    x, w = (rand(g, 3, 2048).float() * by).to(BF), rand(g, 2048)
+    for fmt in (nq.NQ_ACT_BF16, nq.NQ_ACT_INT8_G64, nq.NQ_ACT_E4M3_B128):
+        check_norm(fmt, x, w, eps=1e-30)
+
+
+def test_norm_rows_of_zeros_and_not_finite():
+    x = torch.zeros((4, 512), dtype=BF, device=DEV)
+    x[1, 5], x[2, 200], x[3] = math.nan, math.inf, -0.0
+    w = torch.ones(512, dtype=BF, device=DEV)
+    y, _, _ = run_norm(nq.NQ_ACT_BF16, x, w)
+    assert bool((y[0] == 0).all()) and bool(y[1].isnan().all()) and bool((y[3] == 0).all())
+    assert bool(y[2, 200].isnan()) and int(y[2].isnan().sum()) == 1
+    y, s, _ = run_norm(nq.NQ_ACT_E4M3_B128, x, w)
+    v = y.view(F8).float()
+    assert bool((v[0] == 0).all()) and bool((s[0] == 0).all()) and bool((s[3] == 0).all()) and bool((y[3] == 0x80).all())
+    assert bool(s[1].isnan().all()) and bool(v[1].isnan().all())
+    assert s[2].isnan().tolist() == [False, True, False, False] and bool((v[2, :128] == 0).all())
+    y, s, _ = run_norm(nq.NQ_ACT_INT8_G64, x, w)
+    assert bool(s[1].isnan().all()) and bool((y == 0).all()) and bool((s[0] == 0).all())
+
+
+def test_norm_is_the_norm_of_what_is_kept():
+    """With the residual added before or by the call: the same outputs."""
+    g = gen(8)
+    x, r, w = rand(g, 40, 5120), rand(g, 40, 5120, by=5.0), rand(g, 5120)
+    for fmt in (nq.NQ_ACT_BF16, nq.NQ_ACT_INT8_G64, nq.NQ_ACT_E4M3_B128):
+        y, s, out = run_norm(fmt, x, w, residual=r)
+        y2, s2, _ = run_norm(fmt, out, w)
+        same_bits(y, y2)
+        assert s is None or torch.equal(s, s2)
+
+
+def test_norm_repeats_its_bits():
+    g = gen(9)
+    x, w = rand(g, 300, 5120), rand(g, 5120)
+    first = run_norm(nq.NQ_ACT_E4M3_B128, x, w)
+    for _ in range(3):
+        again = run_norm(nq.NQ_ACT_E4M3_B128, x, w)
+        same_bits(first[0], again[0])
+        same_bits(first[1], again[1])
+
+
+# ---- quantizer ------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("t,k", [(1, 16), (1, 128), (2, 144), (33, 5120), (7, 1040), (5, 17408), (129, 256), (700, 400)])
+def test_quantizer_bit_exact(t, k):
+    g = gen(k + t)
+    x = rand(g, t, k) * torch.exp(3 * torch.randn((t, 1), generator=g, device=DEV)).to(BF)
+    x[t // 2] = 0.0
+    x[t // 2, ::3] = -0.0
+    codes, scale = torch.empty((t, k), dtype=torch.uint8, device=DEV), torch.empty((t, -(-k // 128)), device=DEV)
+    nq.nq_quantize_act_fp8_b128(x, t, k, codes, scale)
+    c = x.float().cpu()
+    for b in range(scale.shape[1]):
+        v = c[:, 128 * b:128 * b + 128]
+        s = v.abs().amax(1) / 448.0
+        assert torch.equal(scale[:, b].cpu(), s)
+        q = torch.where(s[:, None] == 0, v, v / s[:, None]).clamp(-448, 448).to(F8).view(torch.uint8)
+        assert torch.equal(codes[:, 128 * b:128 * b + 128].cpu(), q)
+
+
+def test_quantizer_not_finite():
+    x = torch.ones((3, 256), dtype=BF, device=DEV)
+    x[0, 3], x[1, 200], x[2, 130], x[2, 131] = math.nan, math.inf, math.inf, math.nan
+    codes, scale = torch.empty((3, 256), dtype=torch.uint8, device=DEV), torch.empty((3, 2), device=DEV)
+    nq.nq_quantize_act_fp8_b128(x, 3, 256, codes, scale)
+    v = codes.view(F8).float()
+    assert bool(scale[0, 0].isnan()) and bool(v[0, :128].isnan().all()) and bool((v[0, 128:] == 448).all())
+    assert float(scale[1, 1]) == math.inf and bool((v[1, :128] == 448).all())
+    assert bool(scale[2, 1].isnan()) and not bool(scale[2, 0].isnan())
+
+
+# ---- product --------------------------------------------------------------------------------------------------------
+
+def product_inputs(m, n, k, seed, whole=False):
+    g, gc, gr = gen(seed), -(-k // 128), -(-n // 128)
+    if whole:       # every product and sum is exact in any arithmetic
+        a, w = (torch.randint(-2, 3, s, generator=g, device=DEV).float().to(F8) for s in ((m, k), (n, k)))
+        a_s, w_s = (torch.exp2(torch.randint(-2, 3, s, generator=g, device=DEV).float()) for s in ((m, gc), (gr, gc)))
+    else:
+        a, w = ((torch.randn(s, generator=g, device=DEV) * 110).clamp(-448, 448).to(F8) for s in ((m, k), (n, k)))
+        a_s, w_s = (torch.exp(torch.randn(s, generator=g, device=DEV)) * 0.01 for s in ((m, gc), (gr, gc)))
+    return a, a_s, w, w_s
+
+
+def product64(a, a_s, w, w_s, absolute=False):
+    m, k = a.shape
+    n = w.shape[0]
+    f = (lambda z: z.double().abs()) if absolute else (lambda z: z.double())
+    y = torch.zeros((m, n), dtype=torch.float64, device=DEV)
+    rows = w_s.double().repeat_interleave(128, 0)[:n]
+    for b in range(a_s.shape[1]):
+        part = slice(128 * b, 128 * b + 128)
+        y += (f(a[:, part]) @ f(w[:, part]).t().contiguous()) * a_s[:, b:b + 1].double() * rows[:, b]
+    return y
+
+
+def run_product(a, a_s, w, w_s, out, workspace="own", guard=64):
+    m, k = a.shape
+    n = w.shape[0]
+    buf = torch.full((m * n + guard,), 7.0, dtype=out, device=DEV)
+    y = buf[:m * n].view(m, n)
+    ws = nq.alloc_gemm_fp8_b128_workspace(m, n, k, DEV) if workspace == "own" else workspace
+    nq.nq_gemm_fp8_b128(a.view(torch.uint8), a_s, w.view(torch.uint8), w_s, m, n, k, y, ws)
+    assert bool((buf[m * n:] == 7.0).all())
+    return y
+
+
+def check_product(a, a_s, w, w_s, out, **more):
+    y = run_product(a, a_s, w, w_s, out, **more)
+    ref, size = product64(a, a_s, w, w_s), product64(a, a_s, w, w_s, absolute=True)
+    # FP32: up to 128 sums a block and one a block after them (and the same again where K is split), the scales' product
+    # and the factor, of terms whose sizes add up to `size`; the matrix units may cut instead of rounding: a whole step
+    steps = (128 + 2 * a_s.shape[1] + 4) * 2 * U32
+    if out == torch.float32:
+        within(y, ref, steps * size)
+        assert float((y.double() - ref).norm()) <= 1e-5 * float(ref.norm())
+    else:           # an FP8 instruction keeps 2^-15 of its products' sizes (measured: 1.7e-5 of 3.05e-5)
+        within(y, ref, U16 * ref.abs() + (2.0 ** -15 + steps) * size * (1 + U16))
+    return y
+
+
+MNK = [(1, 1, 16), (1, 16, 128), (1, 17, 144), (2, 128, 256), (3, 129, 400), (15, 300, 1040), (16, 64, 2048), (17, 257, 384), (31, 48, 640),
+       (33, 513, 1152), (48, 130, 272), (49, 40, 5136), (64, 256, 512), (65, 100, 256), (100, 300, 784), (128, 384, 128), (129, 257, 272),
+       (130, 1, 128), (200, 500, 1040), (256, 256, 640), (257, 255, 2064), (300, 700, 400), (511, 130, 16), (640, 1024, 512), (1, 1000, 17408),
+       (40, 33, 17408), (300, 64, 5120), (129, 128, 17408)]
+
+
+@pytest.mark.parametrize("out", [BF, torch.float32])
+@pytest.mark.parametrize("m,n,k", MNK)
+def test_product(m, n, k, out):
+    check_product(*product_inputs(m, n, k, m + n + k), out)
+
+
+@pytest.mark.parametrize("m,n,k", MNK)
+def test_product_of_whole_numbers_is_exact(m, n, k):
+    """Each value stands where it belongs: sums of small whole numbers times powers of two have no rounding at all."""
+    x = product_inputs(m, n, k, m * n + k, whole=True)
+    ref = product64(*x)
+    assert torch.equal(run_product(*x, torch.float32).double(), ref)
+    assert torch.equal(run_product(*x, BF), ref.to(BF))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 2048), (33, 200, 5120), (200, 300, 4096), (600, 260, 1024)])
+def test_product_with_and_without_workspace(m, n, k):
+    """No workspace, a smaller one and one with anything in it; and the same bits each time."""
+    x = product_inputs(m, n, k, 3)
+    need = nq.nq_gemm_fp8_b128_workspace_bytes(m, n, k)
+    for out in (BF, torch.float32):
+        check_product(*x, out, workspace=None)
+        full = torch.full((need + 16,), 255, dtype=torch.uint8, device=DEV)
+        first = check_product(*x, out, workspace=full)
+        for _ in range(3):
+            same_bits(first, run_product(*x, out, workspace=full))
+        if need:
+            small = torch.zeros(max(16, need // 2 // 16 * 16), dtype=torch.uint8, device=DEV)
+            check_product(*x, out, workspace=small)
+
+
+@pytest.mark.parametrize("m", [1, 20, 64, 100, 200, 300])
+@pytest.mark.parametrize("out", [BF, torch.float32])
+def test_product_not_finite_stays_in_its_row_and_column(m, out):
+    a, a_s, w, w_s = product_inputs(m, 300, 656, 4)
+    a.view(torch.uint8)[m // 2, 400] = 0x7F
+    w.view(torch.uint8)[299, 655] = 0xFF
+    a_s[0, 1] = math.inf
+    y = run_product(a, a_s, w, w_s, out)
+    bad = ~y.isfinite()
+    bad[m // 2], bad[:, 299], bad[0] = True, True, True
+    assert bool(y[m // 2].isnan().all()) and bool(y[:, 299].isnan().all()) and not bool(y[0].isfinite().any())
+    assert int(bad.sum()) == int((~y.isfinite()).sum())
+
+
+def test_product_of_nothing():
+    z = torch.empty((0, 0), dtype=torch.uint8, device=DEV)
+    y = torch.full((3, 5), 9.0, device=DEV)
+    nq.nq_gemm_fp8_b128(z, torch.empty((3, 0), device=DEV), z, torch.empty((1, 0), device=DEV), 3, 5, 0, y)
+    assert bool((y == 0).all())
+
+
+def test_product_scales_and_outputs_inside_larger_tensors():
+    """Scale arrays at any 4-byte place."""
+    a, a_s, w, w_s = product_inputs(200, 300, 400, 5)
+    pad = torch.zeros(4096, device=DEV)
+    a2, w2 = pad[1:1 + a_s.numel()].view(a_s.shape), pad[2051:2051 + w_s.numel()].view(w_s.shape)
+    a2.copy_(a_s), w2.copy_(w_s)
+    for m in (1, 40, 200):
+        same_bits(run_product(a[:m], a_s[:m], w, w_s, BF), run_product(a[:m], a2[:m], w, w2, BF))
+
+
+# ---- rotated append -------------------------------------------------------------------------------------------------
+
+def turned64(x, weight, bias, eps, pos, freq, pairs):
+    x = x.double()
+    if weight is not None:
+        x = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps) * (weight.double() + bias)
+    if freq is None:
+        return x
+    rot = 2 * freq.numel()
+    by = (pos.double()[:, None] * freq.double())[:, None]
+    c, s = torch.cos(by), torch.sin(by)
+    out = x.clone()
+    one, two = (slice(0, rot, 2), slice(1, rot, 2)) if pairs else (slice(0, rot // 2), slice(rot // 2, rot))
+    out[..., one] = x[..., one] * c - x[..., two] * s
+    out[..., two] = x[..., one] * s + x[..., two] * c
+    return out
+
+
+class Cache:
+    """Pages of one layer, all of them filled with something that must stay where no token is written."""
+
+    def __init__(self, fmt, hkv, d, page, pages, seed=1):
+        g = gen(seed)
+        self.fmt, self.page = fmt, page
+        shape = (pages, hkv, page, d)
+        self.k, self.v = ((rand(g, *shape) if fmt == nq.NQ_KV_BF16 else torch.randint(0, 120, shape, generator=g, device=DEV, dtype=torch.uint8))
+                          for _ in range(2))
+        n = (hkv,) if fmt == nq.NQ_KV_E4M3 else (pages, hkv, page)
+        self.ks, self.vs = (None, None) if fmt == nq.NQ_KV_BF16 else (0.004 + 0.02 * torch.rand(n, generator=g, device=DEV) for _ in range(2))
+
+    def clone(self):
+        c = object.__new__(Cache)
+        c.fmt, c.page = self.fmt, self.page
+        c.k, c.v, c.ks, c.vs = (None if x is None else x.clone() for x in (self.k, self.v, self.ks, self.vs))
+        return c
+
+    def values(self, pages, scale):
+        if self.fmt == nq.NQ_KV_BF16:
+            return pages.double()
+        s = scale.double()
+        return pages.view(F8).double() * (s[:, None, None] if self.fmt == nq.NQ_KV_E4M3 else s[..., None])
+
+
+def check_rows(cache, before, pages, scale, old, old_scale, page, slot, rows, extra):
+    """The tokens' rows hold `rows` [t][heads][d], off by `extra` before their rounding; everything else is as it was."""
+    touched = torch.zeros(pages.shape[:3], dtype=torch.bool, device=DEV)
+    touched[page, :, slot] = True
+    assert torch.equal(pages[~touched], old[~touched])
+    got = cache.values(pages, scale)[page, :, slot]
+    if cache.fmt == nq.NQ_KV_BF16:
+        within(got, rows, U16 * rows.abs() + extra * 2)
+        return
+    if cache.fmt == nq.NQ_KV_E4M3:
+        s = scale.double()[:, None]
+        rows = rows.clamp(-448 * s, 448 * s)
+        assert torch.equal(scale, old_scale)
+    else:
+        assert torch.equal(scale[~touched], old_scale[~touched])
+        s = scale[page, :, slot].double()[..., None]
+        top = rows.abs().amax(-1, keepdim=True) / 448.0
+        within(s, top, 8 * U32 * top + extra.amax(-1, keepdim=True) / 448.0 + 2.0 ** -149)
+    within(got, rows, (U8 * rows.abs()).clamp(min=0) + s * 2.0 ** -10 + extra * 2 + 2 * U32 * rows.abs())
+
+
+def rope_case(fmt, hq, hkv, d, rot, pairs, normed, page, lens, new, seed, far=0, with_k_out=False, in_place=False, bias=0.0):
+    g, t = gen(seed), sum(new)
+    rows = rand(g, t, hq + 2 * hkv, d)
+    q, k, v = rows[:, :hq], rows[:, hq:-hkv], rows[:, -hkv:]
+    qw, kw = (rand(g, d, by=0.5), rand(g, d, by=0.5)) if normed else (None, None)
+    freq = (1e6 ** (-torch.arange(0, rot, 2, device=DEV, dtype=torch.float64) / max(rot, 1))).float() if rot else None
+    pos = torch.cat([torch.arange(n, n + m, device=DEV) for n, m in zip(lens, new)]).to(torch.int32) + far
+    need = [-(-(n + m) // page) for n, m in zip(lens, new)]
+    pages = sum(need) + 3
+    cache = Cache(fmt, hkv, d, page, pages)
+    before = cache.clone()
+    order = torch.randperm(pages, generator=g, device=DEV).tolist()
+    table = torch.full((len(lens), max(need) + 1), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.tensor(order[at:at + n])
+        at += n
+    table = table.to(DEV)
+    q64, k64 = turned64(q, qw, bias, 1e-5, pos, freq, pairs), turned64(k, kw, bias, 1e-5, pos, freq, pairs)
+    v64 = v.double()
+    q_out = q if in_place else torch.empty((t, hq, d), dtype=BF, device=DEV)
+    k_out = k if in_place else torch.empty((t, hkv, d), dtype=BF, device=DEV) if with_k_out else None
+    # FP32 before the last rounding: the norm's two or three, cos and sin (two steps each), their products and the sum
+    size = turned64(q, qw, bias, 1e-5, pos, None, pairs).abs(), turned64(k, kw, bias, 1e-5, pos, None, pairs).abs()
+    extra = [10 * U32 * s.amax(-1, keepdim=True).expand_as(s) for s in size]
+    nq.nq_kv_append_rope(fmt, q, k, v, pos, freq, nq.NQ_ROPE_PAIRS if pairs else nq.NQ_ROPE_HALVES, cache.ks, cache.vs, table, i32(lens),
+                         starts(new), q_out, cache.k, cache.v, q_weight=qw, k_weight=kw, weight_bias=bias, eps=1e-5, k_out=k_out)
+    within(q_out, q64, U16 * q64.abs() + 2 * extra[0])
+    if k_out is not None:
+        within(k_out, k64, U16 * k64.abs() + 2 * extra[1])
+    place = torch.cat([torch.arange(n, n + m, device=DEV) for n, m in zip(lens, new)])
+    owner = torch.repeat_interleave(torch.arange(len(new), device=DEV), torch.tensor(new, device=DEV))
+    where, slot = table[owner, place // page].long(), place % page
+    check_rows(cache, before, cache.k, cache.ks, before.k, before.ks, where, slot, k64, extra[1])
+    check_rows(cache, before, cache.v, cache.vs, before.v, before.vs, where, slot, v64, torch.zeros_like(v64))
+
+
+FMTS = [nq.NQ_KV_BF16, nq.NQ_KV_E4M3, nq.NQ_KV_E4M3_TOKEN]
+HEADS = [(24, 4, 256), (32, 8, 128), (14, 2, 64), (1, 1, 64), (20, 20, 64), (8, 1, 256), (40, 8, 128)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_append_rope_heads(fmt, hq, hkv, d):
+    for n, (rot, pairs, normed) in enumerate([(d, False, True), (d // 4, True, False), (d // 2, False, False), (0, False, True), (16, True, True)]):
+        rope_case(fmt, hq, hkv, d, rot, pairs, normed, 16, [5, 0, 40], [3, 17, 1], 7 * n + d, bias=float(n % 2))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_append_rope_lengths(fmt):
+    rope_case(fmt, 6, 2, 128, 96, False, True, 64, [701], [1], 1)
+    rope_case(fmt, 6, 2, 128, 48, False, False, 32, [0], [300], 2, with_k_out=True)
+    rope_case(fmt, 24, 4, 256, 64, False, True, 16, list(range(0, 70)), [1 + i % 3 for i in range(70)], 3)
+    rope_case(fmt, 6, 2, 64, 64, True, True, 4096, [4000], [400], 4, in_place=True)
+    rope_case(fmt, 6, 2, 256, 256, False, True, 128, [100, 3], [33, 60], 5, in_place=True)
+    rope_case(fmt, 6, 2, 64, 64, False, True, 16, [3, 9], [130, 140], 6, in_place=True)     # over 256 tokens
+
+
+@pytest.mark.parametrize("far", [131072, 1 << 24, (1 << 31) - 100, -5000, -(1 << 31)])
+def test_append_rope_far_positions(far):
+    """Angles of up to 2^31 radians: an FP32 angle would be off by whole turns there."""
+    rope_case(nq.NQ_KV_BF16, 4, 2, 64, 64, False, False, 16, [10], [40], 9, far=far, with_k_out=True)
+
+
+def test_append_rope_without_rotation_is_the_append():
+    g = gen(11)
+    k, v = rand(g, 37, 4, 128, by=30.0), rand(g, 37, 4, 128, by=30.0)
+    table, lens, cu = i32([[3, 1, -1], [0, 2, 4]]), i32([9, 20]), i32([0, 20, 37])
+    for fmt in FMTS[:2]:
+        one, two = Cache(fmt, 4, 128, 16, 6), Cache(fmt, 4, 128, 16, 6)
+        nq.nq_kv_append(fmt, k, v, one.ks, one.vs, table, lens, cu, one.k, one.v)
+        nq.nq_kv_append_rope(fmt, None, k, v, None, None, nq.NQ_ROPE_HALVES, two.ks, two.vs, table, lens, cu, None, two.k, two.v)
+        same_bits(one.k, two.k)
+        same_bits(one.v, two.v)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_append_rope_drops_what_has_no_place(fmt):
+    """Entries without a page, outside the pool and past the table, a negative length, tokens of no sequence."""
+    g, d = gen(12), 64
+    t, new = 60, [8, 8, 8, 8, 8]
+    q, k, v = rand(g, t, 4, d), rand(g, t, 2, d), rand(g, t, 2, d)
+    pos, freq = torch.arange(t, device=DEV, dtype=torch.int32), torch.full((32,), 0.5, device=DEV)
+    table, lens = i32([[1, -1], [99, 0], [2, 3], [4, 5], [-7, 6]]), i32([12, 12, 28, -3, 12])
+    cu = i32([5, 13, 21, 29, 37, 45])                                   # rows before 5 and from 45 on belong to nobody
+    cache = Cache(fmt, 2, d, 16, 8)
+    before = cache.clone()
+    q_out, k_out = torch.full((t, 4, d), 3.0, dtype=BF, device=DEV), torch.full((t, 2, d), 3.0, dtype=BF, device=DEV)
+    nq.nq_kv_append_rope(fmt, q, k, v, pos, freq, nq.NQ_ROPE_HALVES, cache.ks, cache.vs, table, lens, cu, q_out, cache.k, cache.v, k_out=k_out)
+    for out, x in ((q_out, q), (k_out, k)):
+        ref = turned64(x, None, 0, 0, pos, freq, False)
+        assert bool((out[:5] == 3).all()) and bool((out[45:] == 3).all())
+        within(out[5:45], ref[5:45], U16 * ref[5:45].abs() + 1e-5)
+    keep = [(i, b, lens.tolist()[b] + i) for b in range(5) for i in range(8)]
+    rows = [(5 + 8 * b + i, table.tolist()[b][n // 16], n % 16) for i, b, n in keep
+            if lens.tolist()[b] >= 0 and n // 16 < 2 and 0 <= table.tolist()[b][n // 16] < 8]
+    assert len(rows) == 4 + 4 + 4 + 4
+    at, page, slot = (torch.tensor(x, device=DEV) for x in zip(*rows))
+    k64 = turned64(k, None, 0, 0, pos, freq, False)
+    check_rows(cache, before, cache.k, cache.ks, before.k, before.ks, page, slot, k64[at], torch.full_like(k64[at], 1e-6))
+    check_rows(cache, before, cache.v, cache.vs, before.v, before.vs, page, slot, v.double()[at], torch.zeros_like(k64[at]))
+
+
+def test_append_rope_without_a_cache():
+    """A pool or a table of no size: queries and k_out all the same."""
+    g = gen(13)
+    q, k = rand(g, 5, 4, 64), rand(g, 5, 2, 64)
+    pos, freq = torch.arange(5, device=DEV, dtype=torch.int32), torch.full((8,), 0.25, device=DEV)
+    for table, pages in ((torch.empty((1, 0), dtype=torch.int32, device=DEV), 3), (i32([[0, 1]]), 0)):
+        pool, rows = torch.zeros((pages, 2, 16, 64), dtype=torch.uint8, device=DEV), torch.zeros((pages, 2, 16), device=DEV)
+        q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+        nq.nq_kv_append_rope(nq.NQ_KV_E4M3_TOKEN, q, k, k, pos, freq, nq.NQ_ROPE_HALVES, rows, rows, table, i32([0]), i32([0, 5]), q_out, pool,
+                             pool, k_out=k_out)
+        for out, x in ((q_out, q), (k_out, k)):
+            ref = turned64(x, None, 0, 0, pos, freq, False)
+            within(out, ref, U16 * ref.abs() + 1e-5)
+        assert bool((pool == 0).all()) and bool((rows == 0).all())
+
+
+def test_append_rope_token_rows_of_any_values():
+    """Scales are finite whatever comes: infinities saturate, NaN stays in its place, zeros keep their signs."""
+    k = torch.ones((6, 1, 64), dtype=BF, device=DEV)
+    k[0, 0, 3], k[1, 0, 4], k[1, 0, 5], k[2], k[3], k[3, 0, 9] = math.nan, math.inf, -math.inf, -0.0, 0.0, math.inf
+    k[4], k[5] = 3e38, 1e-38
+    cache = Cache(nq.NQ_KV_E4M3_TOKEN, 1, 64, 16, 1)
+    nq.nq_kv_append_rope(nq.NQ_KV_E4M3_TOKEN, None, k, k, None, None, nq.NQ_ROPE_HALVES, cache.ks, cache.vs, i32([[0]]), i32([0]), i32([0, 6]),
+                         None, cache.k, cache.v)
+    for pages, s in ((cache.k, cache.ks), (cache.v, cache.vs)):
+        c, s = pages[0, 0, :6].view(F8).float(), s[0, 0, :6]
+        assert bool(s.isfinite().all()) and s[2] == 0 and s[3] == 0
+        assert int(c.isnan().sum()) == 1 and bool(c[0, 3].isnan()) and bool((c[0, 4:] == 448).all())
+        assert float(c[1, 4]) == 448 and float(c[1, 5]) == -448 and float(c[1, 6]) == 448
+        assert bool((pages[0, 0, 2] == 0x80).all()) and float(c[3, 9]) == 448 and float(c[3, 0]) == 0
+        assert bool((c[4] == 448).all()) and bool((c[5] == 448).all())
+
+
+# ---- attention over rows with a scale each ----------------------------------------------------------------------------
+
+def attend64(q, cache, table, lens, new, mask, scale):
+    t, hq, d = q.shape
+    hkv, page = cache.k.shape[1], cache.page
+    o, lse = torch.zeros((t, hq, d), dtype=torch.float64, device=DEV), torch.full((t, hq), -math.inf, dtype=torch.float64, device=DEV)
+    size, top = torch.zeros_like(o), torch.zeros_like(lse)          # sizes of the sums: of weights times values, of a logit's products
+    r0 = 0
+    for b, (n, m) in enumerate(zip(lens, new)):
+        total = n + m
+        at = torch.arange(total, device=DEV)
+        ids = table[b].long()[at // page]
+        there = (ids >= 0) & (ids < cache.k.shape[0])
+        ids = ids.clamp(0, cache.k.shape[0] - 1)
+        k, v = (torch.where(there[:, None, None], c.view(F8).double()[ids, :, at % page] * s.double()[ids, :, at % page][..., None], 0.0)
+                for c, s in ((cache.k, cache.ks), (cache.v, cache.vs)))
+        for i in range(m):
+            sees = (at < n) | ((mask[r0 + i] >> (at - n).clamp(0, 63)) & 1).bool()
+            if not bool(sees.any()):
+                continue
+            kk, vv = (x[sees].repeat_interleave(hq // hkv, 1) for x in (k, v))
+            x = (q[r0 + i].double()[None] * kk).sum(-1) * scale
+            p = torch.softmax(x, 0)
+            lse[r0 + i] = torch.logsumexp(x, 0)
+            o[r0 + i] = (p[..., None] * vv).sum(0)
+            size[r0 + i] = (p[..., None] * vv.abs()).sum(0)
+            top[r0 + i] = (q[r0 + i].double()[None].abs() * kk.abs()).sum(-1).amax(0) * scale
+        r0 += m
+    return o, lse, size, top
+
+
+def attend_case(hq, hkv, d, page, lens, new, out, seed, workspace=True, holes=(), tree=True, spread=0.3):
+    g, t = gen(seed), sum(new)
+    need = [-(-(n + m) // page) for n, m in zip(lens, new)]
+    pages = sum(need) + 2
+    cache = Cache(nq.NQ_KV_E4M3_TOKEN, hkv, d, page, pages, seed)
+    cache.k = torch.randint(0, 254, cache.k.shape, generator=g, device=DEV, dtype=torch.uint8)
+    cache.k += (cache.k >= 127).to(torch.uint8)
+    cache.v = torch.randint(0, 254, cache.v.shape, generator=g, device=DEV, dtype=torch.uint8)
+    cache.v += (cache.v >= 127).to(torch.uint8)
+    cache.ks, cache.vs = (torch.exp(spread * torch.randn(cache.ks.shape, generator=g, device=DEV)) / 120 for _ in range(2))
+    order = torch.randperm(pages, generator=g, device=DEV).tolist()
+    table, at = torch.full((len(lens), max(need + [1])), -1, dtype=torch.int32), 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.tensor(order[at:at + n], dtype=torch.int32)
+        at += n
+    for b, i, p in holes:
+        table[b, i] = p
+    # what no sequence holds is never read: NaN there, scales and codes
+    held = torch.zeros(cache.ks.shape, dtype=torch.bool)
+    for b, (n, m) in enumerate(zip(lens, new)):
+        for i in range(n + m):
+            p = int(table[b, i // page])
+            if 0 <= p < pages:
+                held[p, :, i % page] = True
+    held = held.to(DEV)
+    cache.ks[~held], cache.vs[~held], cache.k[~held], cache.v[~held] = math.nan, math.inf, 0x7F, 0xFF
+    table = table.to(DEV)
+    q = rand(g, t, hq, d)
+    masks = []
+    for m in new:
+        for i in range(m):
+            masks.append(int(torch.randint(0, 1 << 62, (1,), generator=torch.Generator().manual_seed(seed + len(masks)))) & ((1 << i) - 1) | 1 << i
+                         if tree else (2 << i) - 1)
+    mask = torch.tensor([x - (1 << 64) if x >> 63 else x for x in masks], dtype=torch.int64, device=DEV)
+    o = torch.full((t, hq, d), 5.0, dtype=out, device=DEV)
+    lse = torch.full((t, hq), 5.0, device=DEV)
+    scale, longest, most = d ** -0.5, max(n + m for n, m in zip(lens, new)), max(new)
+    ws = nq.alloc_attn_tree_workspace(len(lens), most, hq, hkv, d, longest, DEV) if workspace else None
+    nq.nq_attn_tree(nq.NQ_KV_E4M3_TOKEN, q, cache.k, cache.v, cache.ks, cache.vs, table, i32(lens), starts(new), mask, most, longest, scale, o,
+                    lse, ws)
+    ref, ref_lse, size, top = attend64(q, cache, table, lens, new, mask, scale)
+    # a logit: d products (exact) summed in FP32 and scaled; a weight and the sum's logarithm move by as much
+    logit = (d + 8) * U32 * top
+    within(torch.where(lse == -math.inf, 0.0, lse.double()), torch.where(ref_lse == -math.inf, 0.0, ref_lse),
+           logit + 8 * U32 * (1 + ref_lse.abs().nan_to_num(posinf=0.0)))
+    assert torch.equal(lse == -math.inf, ref_lse == -math.inf)
+    half = {BF: U16, torch.float32: U32}[out]
+    weight = {BF: U16, torch.float32: 2.0 ** -21}[out]          # the softmax's weights: one BF16 term, or three
+    sums = (longest + 64) * U32
+    within(o, ref, half * ref.abs() + (weight + 2 * logit[..., None] + sums) * size * 1.01 + 1e-30)
+    if spread < 1:
+        assert float((o.double() - ref).norm()) <= {BF: U16, torch.float32: 1e-5}[out] * float(ref.norm())
+    return cache, q, table, mask, o, lse
+
+
+@pytest.mark.parametrize("out", [BF, torch.float32])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_attend_token_scales(hq, hkv, d, out):
+    attend_case(hq, hkv, d, 16, [37, 0, 100], [3, 9, 1], out, d + hq)
+    attend_case(hq, hkv, d, 64, [300], [1], out, d + hq + 1)
+    attend_case(hq, hkv, d, 32, [1, 900], [33, 40], out, d + hq + 2)
+    attend_case(hq, hkv, d, 128, [1500], [8], out, d + hq + 3)
+    attend_case(hq, hkv, d, 16, [1100], [64], out, d + hq + 4, workspace=False)
+
+
+@pytest.mark.parametrize("n", [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 129])
+def test_attend_token_scales_lengths(n):
+    for new in (1, 2, 33):
+        attend_case(6, 1, 128, 16, [n], [new], torch.float32, n + new)
+        attend_case(6, 1, 256, 32, [n, 5], [new, 3], BF, n + new + 1, tree=False)
+
+
+def test_attend_token_scales_missing_pages():
+    """Rows without a page count as zeros, whatever their place in the planes holds."""
+    for new in (2, 20):
+        attend_case(8, 2, 128, 16, [100, 70], [new, new], torch.float32, 3, holes=[(0, 2, -1), (1, 0, 1 << 30), (1, 3, -5)])
+
+
+def test_attend_token_scales_hidden_rows_hold_anything():
+    """Drafted tokens that a row does not see: NaN and infinite scales and NaN codes do not reach it."""
+    for new, heads in ((4, (4, 2)), (40, (8, 2))):
+        d, (hq, hkv) = 128, heads
+        g = gen(new)
+        cache = Cache(nq.NQ_KV_E4M3_TOKEN, hkv, d, 16, 8)
+        clean = cache.clone()
+        n = 50
+        for j, (ks, vs, code) in enumerate([(math.nan, math.inf, 0x7F), (math.inf, math.nan, 0x01), (-math.inf, -math.inf, 0xFF)]):
+            at = n + 1 + j
+            cache.ks[at // 16, :, at % 16], cache.vs[at // 16, :, at % 16] = ks, vs
+            cache.k[at // 16, :, at % 16], cache.v[at // 16, :, at % 16] = code, code
+        mask = torch.tensor([1 | (0xE if i == 2 else 0) | (1 << i if i > 3 else 0) for i in range(new)], dtype=torch.int64, device=DEV)
+        q, table = rand(g, new, hq, d), torch.arange(8, dtype=torch.int32, device=DEV)[None]
+        res = []
+        for c in (cache, clean):
+            o, lse = torch.empty((new, hq, d), device=DEV), torch.empty((new, hq), device=DEV)
+            nq.nq_attn_tree(c.fmt, q, c.k, c.v, c.ks, c.vs, table, i32([n]), i32([0, new]), mask, new, n + new, d ** -0.5, o, lse)
+            res.append((o, lse))
+        others = [i for i in range(new) if i != 2]
+        # Not the same bits: the softmax's reference moves for all rows of a wave when one row's logits ask for it, and the
+        # row that sees the odd keys asks at other times.  Under another reference each weight is rounded anew (exp2 and its
+        # FP32 argument, at most 8 steps of 2^-24 for logits below 16; three BF16 terms, 2^-21) and each of the under 100
+        # sums (2^-24); all terms are positive, so the outputs move by as much relative to themselves, on either side.
+        off = 2 * (2.0 ** -21 + (100 + 16) * U32)
+        within(res[0][0][others], res[1][0][others], off * res[1][0][others].double().abs())
+        within(res[0][1][others], res[1][1][others], off + 8 * U32 * res[1][1][others].double().abs())
+        assert not bool(res[0][0][2].isfinite().any())
+
+
+def test_attend_token_scales_empty_rows():
+    d, hq, hkv = 64, 4, 2
+    cache = Cache(nq.NQ_KV_E4M3_TOKEN, hkv, d, 16, 4)
+    cache.ks[:], cache.vs[:] = math.nan, math.nan
+    for new in (3, 30):
+        o, lse = torch.full((new, hq, d), 5.0, device=DEV), torch.full((new, hq), 5.0, device=DEV)
+        mask = torch.zeros(new, dtype=torch.int64, device=DEV)
+        nq.nq_attn_tree(cache.fmt, rand(gen(1), new, hq, d), cache.k, cache.v, cache.ks, cache.vs, i32([[0, 1, 2, 3]]), i32([0]), i32([0, new]),
+                        mask, new, new, 0.1, o, lse)
+        assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_attend_token_scales_of_one_value_are_the_heads_scale():
+    """All scales the same power of two: the same logits and weights as under one scale a head, up to the values' product."""
+    g = gen(4)
+    for d, new in ((64, 2), (128, 40), (256, 5)):
+        cache = Cache(nq.NQ_KV_E4M3_TOKEN, 2, d, 16, 40)
+        cache.ks[:], cache.vs[:] = 2.0 ** -7, 2.0 ** -6
+        q, table = rand(g, new, 8, d), torch.arange(40, dtype=torch.int32, device=DEV)[None]
+        mask = torch.tensor([(2 << i) - 1 for i in range(new)], dtype=torch.int64, device=DEV)
+        res = []
+        for fmt, ks, vs in ((cache.fmt, cache.ks, cache.vs), (nq.NQ_KV_E4M3, torch.full((2,), 2.0 ** -7, device=DEV), torch.full((2,), 2.0 ** -6, device=DEV))):
+            o = torch.empty((new, 8, d), dtype=BF, device=DEV)
+            nq.nq_attn_tree(fmt, q, cache.k, cache.v, ks, vs, table, i32([500]), i32([0, new]), mask, new, 600, d ** -0.5, o)
+            res.append(o)
+        within(res[0], res[1], 2 * U16 * res[1].double().abs() + 2e-4)
+
+
+def test_attend_token_scales_far_apart():
+    attend_case(8, 2, 128, 16, [400], [4], torch.float32, 5, spread=3.0)
+    attend_case(8, 2, 64, 16, [400], [20], BF, 6, spread=3.0)
+
+
+# ---- the cache's other calls on scale planes ---------------------------------------------------------------------------
+
+def test_pages_and_rows_of_scales_move_with_their_codes():
+    g = gen(21)
+    planes, pages, hkv, page = 6, 9, 3, 16
+    pool = torch.randn((planes, pages, hkv, page, 1), generator=g, device=DEV)
+    table, lens = i32([[4, 2, 7], [1, 0, -1]]), [14, 30]
+    accept, cu = i32([0, 2, 3, 9, 1, 5]), i32([0, 4, 6])
+    want = pool.clone()
+    for b, paths in enumerate(([0, 2, 3, 9], [1, 5])):
+        for i, a in enumerate(paths):
+            src, dst = lens[b] + a, lens[b] + i
+            if int(table[b, src // page]) >= 0 and int(table[b, dst // page]) >= 0:
+                want[:, int(table[b, dst // page]), :, dst % page] = pool[:, int(table[b, src // page]), :, src % page]
+    nq.nq_kv_compact(pool, table, i32(lens), accept, cu)
+    assert torch.equal(pool, want)
+    nq.nq_kv_copy_pages(pool, i32([[4, 8], [-1, -1]]))
+    want[:, 8] = want[:, 4]
+    assert torch.equal(pool, want)
+
+
+# ---- a layer's step ---------------------------------------------------------------------------------------------------
+
+class Layer:
+    """Norm, projection, rotation and append, attention, quantizer, projection, the next norm: all in 8 bits."""
+    HQ, HKV, D, HIDDEN, PAGE = 6, 2, 64, 512, 16
+
+    def __init__(self, seed, batch, new, most):
+        g = gen(seed)
+        n = (self.HQ + 2 * self.HKV) * self.D
+        self.weights = [product_inputs(1, a, b, seed + a)[2:] for a, b in ((n, self.HIDDEN), (self.HIDDEN, self.HQ * self.D))]
+        self.weights = [(w, s * 0.05) for w, s in self.weights]
+        self.norms = [rand(g, self.HIDDEN, by=0.1) for _ in range(2)]
+        self.qw, self.kw = rand(g, self.D, by=0.1), rand(g, self.D, by=0.1)
+        self.freq = (1e4 ** (-torch.arange(0, 32, 2, device=DEV, dtype=torch.float64) / 32)).float()
+        self.t, self.most = batch * new, most
+        pages = batch * -(-most // self.PAGE)
+        self.cache = Cache(nq.NQ_KV_E4M3_TOKEN, self.HKV, self.D, self.PAGE, pages)
+        self.table = torch.randperm(pages, generator=g, device=DEV).to(torch.int32).view(batch, -1)
+        self.cu, self.new = starts([new] * batch), new
+        self.mask = torch.tensor([(2 << i) - 1 for i in range(new)] * batch, dtype=torch.int64, device=DEV)
+        t, e = self.t, lambda *s, dtype=BF: torch.empty(s, dtype=dtype, device=DEV)  # noqa: E731
+        self.codes = [e(t, self.HIDDEN, dtype=torch.uint8), e(t, self.HQ * self.D, dtype=torch.uint8), e(t, self.HIDDEN, dtype=torch.uint8)]
+        self.scales = [e(t, self.HIDDEN // 128, dtype=torch.float32), e(t, self.HQ * self.D // 128, dtype=torch.float32), e(t, self.HIDDEN // 128, dtype=torch.float32)]
+        self.qkv, self.q_out, self.o, self.out, self.res = e(t, n), e(t, self.HQ, self.D), e(t, self.HQ, self.D), e(t, self.HIDDEN), e(t, self.HIDDEN)
+        self.ws = nq.alloc_attn_tree_workspace(batch, new, self.HQ, self.HKV, self.D, most, DEV)
+        self.gemm_ws = [nq.alloc_gemm_fp8_b128_workspace(t, w.shape[0], w.shape[1], DEV) for w, _ in self.weights]
+
+    def product(self, i, y):
+        w, s = self.weights[i]
+        nq.nq_gemm_fp8_b128(self.codes[i], self.scales[i], w.view(torch.uint8), s, self.t, w.shape[0], w.shape[1], y, self.gemm_ws[i])
+
+    def step(self, x, residual, pos, lens):
+        nq.nq_rmsnorm(nq.NQ_ACT_E4M3_B128, x, self.norms[0], 1e-6, self.codes[0], self.scales[0], residual=residual, residual_out=self.res,
+                      weight_bias=1.0)
+        self.product(0, self.qkv)
+        rows = self.qkv.view(self.t, -1, self.D)
+        q, k, v = rows[:, :self.HQ], rows[:, self.HQ:-self.HKV], rows[:, -self.HKV:]
+        c = self.cache
+        nq.nq_kv_append_rope(c.fmt, q, k, v, pos, self.freq, nq.NQ_ROPE_HALVES, c.ks, c.vs, self.table, lens, self.cu, self.q_out, c.k, c.v,
+                             q_weight=self.qw, k_weight=self.kw, weight_bias=1.0)
+        nq.nq_attn_tree(c.fmt, self.q_out, c.k, c.v, c.ks, c.vs, self.table, lens, self.cu, self.mask, self.new, self.most, self.D ** -0.5,
+                        self.o, workspace=self.ws)
+        nq.nq_quantize_act_fp8_b128(self.o, self.t, self.HQ * self.D, self.codes[1], self.scales[1])
+        self.product(1, self.out)
+        nq.nq_rmsnorm(nq.NQ_ACT_E4M3_B128, self.out, self.norms[1], 1e-6, self.codes[2], self.scales[2], residual=self.res, residual_out=self.res,
+                      weight_bias=1.0)
+        return self.codes[2], self.scales[2], self.res
+
+
+def test_layer_step_against_64_bits():
+    """Each call of a step against the formula on what the call before it gave."""
+    for batch, new, lens in ((1, 1, [0]), (3, 4, [5, 40, 0]), (40, 5, [i for i in range(40)])):
+        L = Layer(31, batch, new, 64)
+        g = gen(32)
+        x, r = rand(g, L.t, L.HIDDEN), rand(g, L.t, L.HIDDEN)
+        L.cache.k[:], L.cache.v[:], L.cache.ks[:], L.cache.vs[:] = 0x38, 0x30, 0.01, 0.5
+        pos = torch.cat([torch.arange(n, n + new, device=DEV) for n in lens]).to(torch.int32)
+        L.step(x, r, pos, i32(lens))
+        h, y = norm64(x, r, L.norms[0], 1.0, 1e-6)
+        deq = L.codes[0].view(F8).double() * L.scales[0].double().repeat_interleave(128, 1)
+        within(deq, y, y.abs() * U8 * 1.001 + L.scales[0].double().repeat_interleave(128, 1) * 2.0 ** -10)
+        a = (L.codes[0].view(F8), L.scales[0])
+        ref, size = product64(*a, *L.weights[0]), product64(*a, *L.weights[0], absolute=True)
+        within(L.qkv, ref, U16 * ref.abs() + 2.0 ** -14 * size)
+        rows = L.qkv.view(L.t, -1, L.D)
+        q = turned64(rows[:, :L.HQ], L.qw, 1.0, 1e-6, pos, L.freq, False)
+        within(L.q_out, q, U16 * q.abs() + 1e-5)
+        o, _, size, _ = attend64(L.q_out, L.cache, L.table, lens, [new] * batch, L.mask, L.D ** -0.5)
+        within(L.o, o, U16 * o.abs() + (U16 + 1e-4) * size)
+        out = product64(L.codes[1].view(F8), L.scales[1], *L.weights[1])
+        size = product64(L.codes[1].view(F8), L.scales[1], *L.weights[1], absolute=True)
+        within(L.out, out, U16 * out.abs() + 2.0 ** -14 * size)
+        same_bits(L.res, (h.float() + L.out.float()).to(BF))
+
+
+def test_layer_step_in_a_graph():
+    """Captured once and replayed with other inputs and lengths between eager steps on another stream's results."""
+    L, E = Layer(41, 4, 3, 128), Layer(41, 4, 3, 128)
+    x, r = torch.zeros((L.t, L.HIDDEN), dtype=BF, device=DEV), torch.zeros((L.t, L.HIDDEN), dtype=BF, device=DEV)
+    pos, lens = torch.zeros(L.t, dtype=torch.int32, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        L.step(x, r, pos, lens)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.step(x, r, pos, lens)
+    for c in (L.cache, E.cache):
+        c.k[:], c.v[:], c.ks[:], c.vs[:] = 0x38, 0x30, 0.01, 0.5
+    for i in range(4):
+        g = gen(50 + i)
+        x.copy_(rand(g, L.t, L.HIDDEN)), r.copy_(rand(g, L.t, L.HIDDEN))
+        lens.copy_(i32([3 * i, 10 + 3 * i, 50 + 3 * i, 100 + 3 * i]))
+        pos.copy_((lens[:, None] + torch.arange(3, device=DEV)).flatten())
+        graph.replay()
+        got = [t.clone() for t in (L.codes[2], L.scales[2], L.res, L.o, L.cache.k, L.cache.ks)]
+        want = E.step(x, r, pos, lens)
+        torch.cuda.synchronize()
+        for a, b in zip(got, (*want, E.o, E.cache.k, E.cache.ks)):
+            same_bits(a, b)
