@@ -15,6 +15,8 @@
 // and go through the BF16 instructions at half the rate.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "nq_attn_launch.h"
 #include "nq_device.h"
 #include "nq_launch.h"
@@ -32,6 +34,7 @@ struct B128Args {
     const uint8_t* w;
     const float* ws;
     int m, n, k, groups;
+    int per;                             // blocks a workgroup, of the tile kernels
     void* y;
 };
 
@@ -42,6 +45,13 @@ __device__ __forceinline__ v8bf eight_bf16(uint32_t x, uint32_t y) {
     return __builtin_bit_cast(v8bf, v4u{e4m3x2_to_bf16x2<false>(x, 1.0f), e4m3x2_to_bf16x2<true>(x, 1.0f),
                                         e4m3x2_to_bf16x2<false>(y, 1.0f), e4m3x2_to_bf16x2<true>(y, 1.0f)});
 }
+
+// p[i], the same in all lanes, by a scalar load (no wait for vector loads in flight).
+typedef __attribute__((address_space(4))) const float* uniform_floats;
+__device__ __forceinline__ float uniform(const float* p, int64_t i) { return ((uniform_floats)(uintptr_t)p)[i]; }
+
+// Two values as BF16, rounded as f32_to_bf16_rne does.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) { return f32_to_bf16_rne(a) | f32_to_bf16_rne(b) << 16; }
 
 template <bool BF16OUT>
 __device__ __forceinline__ void store(void* y, int64_t at, float x) {
@@ -152,18 +162,27 @@ hipError_t go_few(const B128Args& a, hipStream_t stream) {
 
 // ---- many tokens: tiles through LDS ---------------------------------------------------------------------------------
 
-// WR x WT waves of TI x TJ products of 32 x 32: a workgroup has 32 WR TI weight
-// rows and 32 WT TJ tokens.  A stage is one block of 128 columns of both, in two
+// WR x WT waves of FI x FT products of 16 x 16: a workgroup has 16 WR FI weight
+// rows and 16 WT FT tokens.  A stage is one block of 128 columns of both, in two
 // slots: row r of a panel at byte 128 r, its 16-byte piece c in place
-// c ^ (r / 2 % 8), so that operand reads (32 rows, two pieces) spread over all
-// banks; and the tokens' scales of the block.
-template <int WR, int WT, int TI, int TJ>
+// c ^ (r / 2 % 8), so that operand reads (16 rows, one piece each) cover all
+// banks once; and the tokens' scales of the block.
+template <int WR, int WT, int FI, int FT>
 struct Tile {
-    static constexpr int WAVES = WR * WT, ROWS = 32 * WR * TI, TOKENS = 32 * WT * TJ;
+    static constexpr int WAVES = WR * WT, ROWS = 16 * WR * FI, TOKENS = 16 * WT * FT;
     static constexpr int LOADS = (ROWS + TOKENS) / 8 / WAVES;            // of 8 rows, a wave
     static constexpr int SCALES = (ROWS + TOKENS) * BLOCK;               // their place in a stage
-    static constexpr int STAGE = SCALES + TOKENS * 4;
-    static_assert((ROWS + TOKENS) % (8 * WAVES) == 0 && TOKENS % 64 == 0 && TOKENS / 64 <= WAVES && TJ % 2 == 0, "");
+    static constexpr int SINK = SCALES + TOKENS * 4;                     // of the waves that have no scales to load
+    static constexpr int STAGE = SINK + 256;
+    static_assert((ROWS + TOKENS) % (8 * WAVES) == 0 && TOKENS % 64 == 0 && TOKENS / 64 <= WAVES && FT % 2 == 0, "");
+    static_assert(BLOCK % (16 * FI) == 0, "a wave's rows lie in one block of the weights' scales");
+};
+
+// A wave's outputs in LDS on their way out, a row of them a token.
+template <int FI, int FT, bool BF16OUT>
+struct Output {
+    static constexpr int SIZE = BF16OUT ? 2 : 4, EACH = 16 / SIZE, ROWS = 16 * FI, TOKENS = 16 * FT, PIECES = ROWS / EACH;
+    static constexpr int PITCH = ROWS * SIZE + 16, BYTES = TOKENS * PITCH;
 };
 
 typedef __attribute__((address_space(3))) unsigned char* lds_ptr;
@@ -184,9 +203,13 @@ __device__ __forceinline__ void lds_load4(v4i r, int off, lds_ptr dst) {
                  ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r) : "memory", "m0");
 }
 
-template <int WR, int WT, int TI, int TJ, bool BF16OUT>
+// The products run LAG steps ahead of the rescales, so that no rescale waits for
+// its product.  Operands are read one column of products ahead, also across
+// stages: the barrier at which the next stage has arrived (and this one has been
+// read by all) stands before the last column.
+template <int WR, int WT, int FI, int FT, bool BF16OUT>
 __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) {
-    using T = Tile<WR, WT, TI, TJ>;
+    using T = Tile<WR, WT, FI, FT>;
     extern __shared__ __align__(16) unsigned char smem[];
     const lds_ptr lds = (lds_ptr)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -197,113 +220,173 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
     const int tile = xcd * each + min(xcd, more) + blockIdx.x / 8;
     const int m0 = tile % tiles_m * T::TOKENS, n0 = tile / tiles_m * T::ROWS;
     const int rows_w = min(a.n - n0, T::ROWS), rows_a = min(a.m - m0, T::TOKENS);
-    const v4i buf_w = buffer(a.w + (int64_t)n0 * a.k, (int64_t)rows_w * a.k), buf_a = buffer(a.a + (int64_t)m0 * a.k, (int64_t)rows_a * a.k);
-    const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, (int64_t)rows_a * a.groups * 4);
-    const int steps = a.groups;
+    const int from = blockIdx.y * a.per, upto = min(from + a.per, a.groups);     // this workgroup's blocks
 
-    // Load i of this wave: rows 8 q .. 8 q + 7 of the panels (weights first), q = wave LOADS + i.
-    int place[2];                        // the lane's piece for even and odd q, as a column
+    const v4i buf_w = buffer(a.w + (int64_t)n0 * a.k, (int64_t)rows_w * a.k), buf_a = buffer(a.a + (int64_t)m0 * a.k, (int64_t)rows_a * a.k);
+    const bool has_scales = wave < T::TOKENS / 64;
+    const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, has_scales ? (int64_t)rows_a * a.groups * 4 : 0);
+    const int scales_at = has_scales ? T::SCALES + wave * 256 : T::SINK, scales_off = (64 * wave + lane) * a.groups * 4;
+
+    // Load i of this wave: rows 8 q .. 8 q + 7 of the panels (weights first), q =
+    // wave LOADS + i.  No branches: past the last block, and of what lies past the
+    // last column, nothing is read and zeros arrive.
+    int col[2], off[2];                  // the lane's piece, and its place, for even and odd q
 #pragma unroll
-    for (int p = 0; p < 2; ++p) place[p] = 16 * ((lane & 7) ^ ((4 * p + (lane >> 4)) & 7));
-    const int row_off = (lane >> 3) * a.k;
-    auto issue = [&](int s) {
-        const lds_ptr at = lds + (s & 1) * T::STAGE;
-        const int col = s * BLOCK;
+    for (int p = 0; p < 2; ++p) {
+        col[p] = 16 * ((lane & 7) ^ ((4 * p + (lane >> 4)) & 7));
+        off[p] = (lane >> 3) * a.k + col[p];
+    }
+    auto issue = [&](int s, int lo, int hi) {
+        const lds_ptr at = lds + ((s - from) & 1) * T::STAGE;
+        const int left = s < upto ? a.k - s * BLOCK : 0;                 // columns from this block on
+        const int mine[2] = {col[0] < left ? off[0] : PAST, col[1] < left ? off[1] : PAST};
 #pragma unroll
         for (int i = 0; i < T::LOADS; ++i) {
+            if (i < lo || i >= hi) continue;
             const int q = wave * T::LOADS + i;
             const bool is_w = q < T::ROWS / 8;
-            const int mine = col + place[q & 1];
-            int off = row_off + 8 * (is_w ? q : q - T::ROWS / 8) * a.k + mine;
-            if (mine >= a.k) off = PAST;
-            lds_load16(is_w ? buf_w : buf_a, off, at + q * 1024);
+            lds_load16(is_w ? buf_w : buf_a, mine[q & 1] + (8 * (is_w ? q : q - T::ROWS / 8) * a.k + s * BLOCK), at + q * 1024);
         }
-        if (wave < T::TOKENS / 64) lds_load4(buf_s, ((64 * wave + lane) * a.groups + s) * 4, at + T::SCALES + wave * 256);
+        if (lo == 0) lds_load4(buf_s, s < upto ? scales_off + s * 4 : PAST, at + scales_at);
     };
 
-    const int wr = wave % WR * TI * 32, wt = wave / WR * TJ * 32;
-    const int n = lane & 31, h = lane >> 5;
-    const int first = n * BLOCK + ((h ^ ((n >> 1) & 7)) << 4);           // of this lane's pieces h, 2 + h, 4 + h, 6 + h of its row
-    auto read = [&](lds_ptr panel, int row, v4u (&x)[4]) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-            x[p] = *(__attribute__((address_space(3))) const v4u*)(panel + row * BLOCK + (first ^ (p << 5)));
+    const int wr = wave % WR * FI * 16, wt = wave / WR * FT * 16;
+    const int n = lane & 15, g = lane >> 4;
+    const int first = n * BLOCK + ((g ^ (n >> 1)) << 4);                 // of this lane's pieces g and 4 + g of its row
+    auto read = [&](lds_ptr row, v4u (&x)[2]) {
+        x[0] = *(__attribute__((address_space(3))) const v4u*)(row + first);
+        x[1] = *(__attribute__((address_space(3))) const v4u*)(row + (first ^ 64));
     };
-    auto product = [&](const v4u (&w)[4], const v4u (&t)[4]) {
-        v16f p;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = 0.f;
-        if constexpr (BF16OUT) {
-            p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(w[0], w[1]), join(t[0], t[1]), p, 0, 0, 0, ONE_E8M0, 0, ONE_E8M0);
-            p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(w[2], w[3]), join(t[2], t[3]), p, 0, 0, 0, ONE_E8M0, 0, ONE_E8M0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(eight_bf16(w[i >> 1][2 * (i & 1)], w[i >> 1][2 * (i & 1) + 1]),
-                                                            eight_bf16(t[i >> 1][2 * (i & 1)], t[i >> 1][2 * (i & 1) + 1]), p, 0, 0, 0);
-        }
-        return p;
-    };
-    v16f acc[TI][TJ];
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-    auto rescale = [&](v16f& c, const v16f& p, float f) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) c[e] = fmaf(p[e], f, c[e]);
-    };
-    v4u w[TI][4], t[2][4];
-    float f[TJ];
-    const float* ws = a.ws + (int64_t)((n0 + wr) / BLOCK) * a.groups;    // (32 TI rows of a wave lie in one block of 128)
-    const bool busy = n0 + wr < a.n;
-    auto scales = [&](int s, lds_ptr at) {
-        const float by = busy ? ws[s] : 0.f;
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) f[j] = by * *(__attribute__((address_space(3))) const float*)(at + T::SCALES + (wt + 32 * j + n) * 4);
-    };
-
+    auto read_scale = [&](lds_ptr at, int j) { return *(__attribute__((address_space(3))) const float*)(at + T::SCALES + (wt + 16 * j + n) * 4); };
     auto arrived = [&] {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    if (steps > 0) issue(0);
-    for (int s = 0; s < steps; ++s) {
-        const lds_ptr at = lds + (s & 1) * T::STAGE;
+    constexpr int Q = FI * FT, LAG = BF16OUT ? 3 : 1;
+    v4f acc[FI][FT], p[LAG + 1];
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i <= LAG; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    // Operands: codes as they are, or (FP32 outputs) as BF16, a block's 128 columns in four steps.
+    struct Codes {
+        v4u x[2];
+    };
+    struct Wide {
+        v8bf x[4];
+    };
+    using Operand = std::conditional_t<BF16OUT, Codes, Wide>;
+    auto operand = [&](const v4u (&x)[2]) {
+        Operand o;
+        if constexpr (BF16OUT) {
+            o.x[0] = x[0], o.x[1] = x[1];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o.x[e] = eight_bf16(x[e >> 1][2 * (e & 1)], x[e >> 1][2 * (e & 1) + 1]);
+        }
+        return o;
+    };
+    auto product = [&](const Operand& w, const Operand& t) {
+        v4f x = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (BF16OUT) {
+            x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w.x[0], w.x[1]), join(t.x[0], t.x[1]), x, 0, 0, 0, ONE_E8M0, 0, ONE_E8M0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.x[e], t.x[e], x, 0, 0, 0);
+        }
+        return x;
+    };
+    auto rescale = [&](v4f& c, const v4f& x, float by) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = fmaf(x[e], by, c[e]);
+    };
+    const float* ws = a.ws + (int64_t)min((n0 + wr) / BLOCK, (a.n - 1) / BLOCK) * a.groups;
+    Operand w[FI], t;
+    v4u wn[FI][2], tn[2];
+    float raw = 0.f, f = 0.f, f_last = 0.f;
+    if (from < upto) {
+        issue(from, 0, T::LOADS);
         arrived();
-        if (s + 1 < steps) issue(s + 1);
-        scales(s, at);
+        issue(from + 1, 0, T::LOADS);
 #pragma unroll
-        for (int i = 0; i < TI; ++i) read(at, wr + 32 * i, w[i]);
+        for (int i = 0; i < FI; ++i) read(lds + (wr + 16 * i) * BLOCK, wn[i]);
+        read(lds + (T::ROWS + wt) * BLOCK, tn);
+        raw = read_scale(lds, 0);
+    }
+    for (int s = from; s < upto; ++s) {
+        const lds_ptr at = lds + ((s - from) & 1) * T::STAGE, next = lds + ((s - from + 1) & 1) * T::STAGE;
+        const float by = uniform(ws, s);
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            read(at + T::ROWS * BLOCK, wt + 32 * j, t[0]);
-#pragma unroll
-            for (int i = 0; i < TI; ++i) rescale(acc[i][j], product(w[i], t[0]), f[j]);
+        for (int q = 0; q < Q; ++q) {
+            const int i = q % FI, j = q / FI;
+            if (i == 0) {
+                t = operand(tn);
+                if (j + 1 == FT) arrived();
+                f_last = f;
+                f = raw * by;
+                read((j + 1 < FT ? at : next) + (T::ROWS + wt + 16 * ((j + 1) % FT)) * BLOCK, tn);    // (past the last stage: bytes that no one uses)
+                raw = read_scale(j + 1 < FT ? at : next, (j + 1) % FT);
+            }
+            if (j == 0) w[i] = operand(wn[i]);
+            __builtin_amdgcn_sched_barrier(0);
+            p[q % (LAG + 1)] = product(w[i], t);
+            {
+                const int e = (q + Q - LAG) % Q;
+                rescale(acc[e % FI][e / FI], p[(q + 1) % (LAG + 1)], i < LAG ? f_last : f);
+            }
+            if (j + 1 == FT) {
+                read(next + (wr + 16 * i) * BLOCK, wn[i]);
+                issue(s + 2, T::LOADS * i / FI, T::LOADS * (i + 1) / FI);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-        const int m = m0 + wt + 32 * j + n;
-        if (m >= a.m) continue;
+    for (int q = Q - LAG; q < Q; ++q) rescale(acc[q % FI][q / FI], p[q % (LAG + 1)], f);
+    // A lane's outputs lie a token apart: through LDS they become pieces of whole
+    // cache lines.  Each wave has a place of its own there, once all have read
+    // their last stage and nothing is on its way into it.
+    arrived();
+    using Out = Output<FI, FT, BF16OUT>;
+    const lds_ptr mine = lds + wave * Out::BYTES;
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+    for (int j = 0; j < FT; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = n0 + wr + 32 * i + 8 * (e >> 2) + 4 * h + (e & 3);
-                if (row < a.n) store<BF16OUT>(a.y, (int64_t)m * a.n + row, acc[i][j][e]);
-            }
+        for (int i = 0; i < FI; ++i) {
+            const lds_ptr to = mine + (16 * j + n) * Out::PITCH + (16 * i + 4 * g) * Out::SIZE;
+            const v4f& c = acc[i][j];
+            if constexpr (BF16OUT) *(__attribute__((address_space(3))) v2u*)to = v2u{bf16_pair(c[0], c[1]), bf16_pair(c[2], c[3])};
+            else *(__attribute__((address_space(3))) v4f*)to = c;
+        }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (a.n % Out::EACH == 0) {          // whole 16-byte pieces
+#pragma unroll 4
+        for (int b = lane; b < Out::TOKENS * Out::PIECES; b += 64) {
+            const int m = m0 + wt + b / Out::PIECES, row = n0 + wr + b % Out::PIECES * Out::EACH;
+            const v4u x = *(__attribute__((address_space(3))) const v4u*)(mine + b / Out::PIECES * Out::PITCH + b % Out::PIECES * 16);
+            if (m < a.m && row < a.n) *reinterpret_cast<v4u*>((char*)a.y + ((int64_t)m * a.n + row) * Out::SIZE) = x;
+        }
+    } else {
+#pragma unroll 4
+        for (int b = lane; b < Out::TOKENS * Out::ROWS; b += 64) {
+            const int m = m0 + wt + b / Out::ROWS, row = n0 + wr + b % Out::ROWS;
+            const lds_ptr x = mine + b / Out::ROWS * Out::PITCH + b % Out::ROWS * Out::SIZE;
+            if (m >= a.m || row >= a.n) continue;
+            if constexpr (BF16OUT) reinterpret_cast<uint16_t*>(a.y)[(int64_t)m * a.n + row] = *(__attribute__((address_space(3))) const uint16_t*)x;
+            else reinterpret_cast<float*>(a.y)[(int64_t)m * a.n + row] = *(__attribute__((address_space(3))) const float*)x;
+        }
     }
 }
 
-template <int WR, int WT, int TI, int TJ, bool BF16OUT>
+template <int WR, int WT, int FI, int FT, bool BF16OUT>
 hipError_t go_tile(const B128Args& a, hipStream_t stream) {
-    using T = Tile<WR, WT, TI, TJ>;
-    constexpr int LDS = 2 * T::STAGE;
-    auto kernel = b128_tile_kernel<WR, WT, TI, TJ, BF16OUT>;
+    using T = Tile<WR, WT, FI, FT>;
+    constexpr int OUT = T::WAVES * Output<FI, FT, BF16OUT>::BYTES, LDS = OUT > 2 * T::STAGE ? OUT : 2 * T::STAGE;
+    static_assert(LDS <= 160 * 1024, "");
+    auto kernel = b128_tile_kernel<WR, WT, FI, FT, BF16OUT>;
     static LdsLimit limit;
     if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
     const int64_t tiles = ((int64_t)(a.m + T::TOKENS - 1) / T::TOKENS) * ((a.n + T::ROWS - 1) / T::ROWS);
@@ -313,7 +396,10 @@ hipError_t go_tile(const B128Args& a, hipStream_t stream) {
 
 template <bool BF16OUT>
 hipError_t go(const B128Args& a, hipStream_t stream) {
-    if (a.m > 128) return go_tile<4, 2, 2, 4, BF16OUT>(a, stream);
+    if (a.m > 128) {
+        if constexpr (BF16OUT) return go_tile<4, 2, 4, 8, BF16OUT>(a, stream);
+        else return go_tile<4, 2, 4, 4, BF16OUT>(a, stream);
+    }
     if (a.m <= 16) return go_few<1, BF16OUT>(a, stream);
     if (a.m <= 32) return go_few<2, BF16OUT>(a, stream);
     if (a.m <= 48) return go_few<3, BF16OUT>(a, stream);
@@ -326,7 +412,7 @@ int64_t gemm_fp8_b128_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_gemm_fp8_b128(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t m,
                                 int64_t n, int64_t k, bool bf16_out, void* y, void*, int64_t, hipStream_t stream) {
-    const B128Args args{a, a_scale, w, w_scale, (int)m, (int)n, (int)k, (int)((k + BLOCK - 1) / BLOCK), y};
+    const B128Args args{a, a_scale, w, w_scale, (int)m, (int)n, (int)k, (int)((k + BLOCK - 1) / BLOCK), (int)((k + BLOCK - 1) / BLOCK), y};
     return bf16_out ? go<true>(args, stream) : go<false>(args, stream);
 }
 
