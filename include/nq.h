@@ -373,8 +373,8 @@ nq_status nq_gemm_fp8row(const uint16_t* x, const uint8_t* w, const uint16_t* w_
  * from the FP8 matrix units, whose sums are off by 1.3e-5 to 1.8e-5 (Frobenius,
  * relative), where the output's rounding is off by 1.7e-3.
  * The result does not depend on timing.  a_scale, wsi: 4-byte aligned.
- * Errors: K % 16 != 0, K of 2^20 or more, gr / gc mismatch, more than 2^24 tiles
- * of 64 x 64 -> NQ_ERR_SHAPE.
+ * Errors: K % 16 != 0, K of 2^20 or more, gr / gc mismatch, 2^24 or more tiles of
+ * 64 x 64 (up to 64 tokens: N of 2^28 or more) -> NQ_ERR_SHAPE.
  */
 int64_t nq_gemm_fp8_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
 nq_status nq_gemm_fp8_b128(const uint8_t* a_codes, const float* a_scale, const uint8_t* w, const float* wsi,

@@ -612,7 +612,7 @@ bool kv_fmt_ok(int fmt) { return fmt == NQ_KV_BF16 || fmt == NQ_KV_E4M3 || fmt =
 // Offsets inside a tile are 32-bit (256 rows of K bytes), and so are rows.
 bool b128_shape_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 0 && K >= 0 && M <= MOST_ROWS && N <= MOST_ROWS && K < ((int64_t)1 << 20) && K % 16 == 0 &&
-           ((M + 63) / 64) * ((N + 63) / 64) < MOST_BLOCKS;
+           (M <= 64 ? (N + 15) / 16 : ((M + 63) / 64) * ((N + 63) / 64)) < MOST_BLOCKS;
 }
 bool scale_ok(float scale) { return scale >= 1e-30f && scale <= 1e30f; }       // (false for NaN)
 

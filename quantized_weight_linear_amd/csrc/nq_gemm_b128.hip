@@ -59,104 +59,226 @@ __device__ __forceinline__ void store(void* y, int64_t at, float x) {
     else reinterpret_cast<float*>(y)[at] = x;
 }
 
-// ---- few tokens: weights straight from memory into registers --------------------------------------------------------
+typedef __attribute__((address_space(3))) unsigned char* lds_ptr;
+constexpr int PAST = 0x40000000;         // an offset outside every buffer here: reads as zeros
 
-// A workgroup has 16 weight rows and up to 16 NT tokens; its waves take every
-// WAVES-th block of 128 columns and join in LDS, in the order of the waves.
-// Bound by HBM: the weights once.
-constexpr int FEW_TOKENS = 64;
+__device__ __forceinline__ v4i buffer(const void* base, int64_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    return v4i{(int)(uint32_t)at, (int)(uint32_t)(at >> 32) & 0xFFFF, (int)bytes, 0x00027000};
+}
+// 16 (4) bytes a lane into LDS at dst + 16 (4) lane, no registers between;
+// whoever reads them waits for the loads himself.
+__device__ __forceinline__ void lds_load16(v4i r, int off, lds_ptr dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r) : "memory", "m0");
+}
+template <bool STREAM>                   // bytes that are read once: past the caches
+__device__ __forceinline__ void lds_load16_as(v4i r, int off, lds_ptr dst) {
+    if constexpr (STREAM)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                     ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r) : "memory", "m0");
+    else lds_load16(r, off, dst);
+}
+__device__ __forceinline__ void lds_load4(v4i r, int off, lds_ptr dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r) : "memory", "m0");
+}
 
-template <int NT, int WAVES, bool BF16OUT>
-__global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
-    __shared__ __align__(16) v4f part[WAVES][NT][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * FEW_TOKENS;
-    const uint8_t* w = a.w + (int64_t)(n0 + r < a.n ? n0 + r : a.n - 1) * a.k;
-    const float* ws = a.ws + (int64_t)(n0 / BLOCK) * a.groups;
-    const uint8_t* x[NT];
-    const float* xs[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int m = m0 + 16 * t + r < a.m ? m0 + 16 * t + r : a.m - 1;
-        x[t] = a.a + (int64_t)m * a.k;
-        xs[t] = a.as + (int64_t)m * a.groups;
+// Which tile a workgroup takes.  Workgroups go to the 8 XCDs in turn; each XCD
+// takes a contiguous range of tiles, in bands of BAND token tiles, tokens first,
+// so that those that share an L2 read few different rows (8192 x 8192 x 8192:
+// 555 us without bands, 495 with).
+constexpr int BAND = 8;
+struct Place {
+    int m, n;
+    __device__ __forceinline__ Place(int tiles_m, int tiles_n) {
+        const int each = (int)gridDim.x / 8, more = (int)gridDim.x % 8, xcd = blockIdx.x % 8;
+        const int tile = xcd * each + min(xcd, more) + blockIdx.x / 8;
+        const int band = tile / (BAND * tiles_n), high = min(BAND, tiles_m - band * BAND), inside = tile - band * BAND * tiles_n;
+        m = band * BAND + inside % high;
+        n = inside / high;
     }
-    v4f acc[NT];
+};
+
+// ---- few tokens: every wave streams its own blocks ------------------------------------------------------------------
+
+// A workgroup has 16 RF weight rows and up to 8 TL tokens; its waves split the
+// blocks of 128 columns between them and join in LDS, in the order of the waves.
+// Each wave streams its blocks (weights, tokens and the tokens' scales) through a ring of RING
+// slots of its own in LDS, without barriers: from memory straight into LDS, since
+// there eight neighbouring lanes read a row's 128 bytes, where operand order
+// (neighbouring lanes on different rows) asks for four times the requests.
+// Bound by HBM: the weights once; the tokens come from L2, once for 16 RF rows.
+//   The scales of a token's blocks lie side by side: they come four at a time,
+// 16 bytes a token, in windows of four blocks (two slots of their own).
+template <int TL, int RF, int WAVES, int RING>
+struct Few {
+    static constexpr int NT = (TL + 1) / 2;
+    static constexpr int TOKENS = 16 * RF * BLOCK, SLOT = TOKENS + TL * 1024;    // the tokens' place in a slot
+    static constexpr int WINDOWS = RING * SLOT, WAVE = WINDOWS + 2 * 1024;
+    static constexpr int LOADS = 2 * RF + TL;
+    // Loads that may be on their way when block v of a window is needed: those of the RING - 1 blocks after it.
+    static constexpr int later(int v) {
+        int n = LOADS * (RING - 1);
+        for (int d = 1; d < RING; ++d) n += (v + d) % 4 == 0;
+        return n;
+    }
+    static constexpr int JOIN = WAVES * RF * NT * 1024;
+    // (the last 16 tokens' operands may reach 8 rows past the last slot's tokens)
+    static constexpr int STREAM = WAVES * WAVE, LDS = STREAM > JOIN ? STREAM : JOIN;
+    static_assert(TL <= 8 && LOADS * (RING - 1) + 1 < 64 && RING <= 4, "");
+};
+
+template <int TL, int RF, int WAVES, int RING, bool ONCE, bool BF16OUT>
+__global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
+    using L = Few<TL, RF, WAVES, RING>;
+    constexpr int NT = L::NT;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
+    const Place place((a.m + 8 * TL - 1) / (8 * TL), (a.n + 16 * RF - 1) / (16 * RF));
+    const int n0 = place.n * 16 * RF, m0 = place.m * 8 * TL;
+    const int rows_w = min(a.n - n0, 16 * RF), rows_a = min(a.m - m0, 8 * TL);
+    const v4i buf_w = buffer(a.w + (int64_t)n0 * a.k, (int64_t)rows_w * a.k), buf_a = buffer(a.a + (int64_t)m0 * a.k, (int64_t)rows_a * a.k);
+    const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, (int64_t)rows_a * a.groups * 4);
+    const int per = (a.groups + WAVES - 1) / WAVES, from = wave * per, upto = min(from + per, a.groups);
+    // Load i: rows 8 i .. 8 i + 7 of a panel.
+    int col[2], off[2];                  // the lane's piece, and its place, for even and odd i
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-    struct Part {
-        v4u w[2], x[NT][2];
-        float xs[NT], ws;
-    };
-    // The lane's two pieces of a block: columns 16 g and 64 + 16 g on (zeros past the last column).
-    auto load = [&](int b, Part& p) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int col = b * BLOCK + 64 * h + 16 * g;
-            const bool in = col < a.k;
-            p.w[h] = in ? __builtin_nontemporal_load(reinterpret_cast<const v4u*>(w + col)) : v4u{0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) p.x[t][h] = in ? *reinterpret_cast<const v4u*>(x[t] + col) : v4u{0u, 0u, 0u, 0u};
+    for (int p = 0; p < 2; ++p) {
+        col[p] = 16 * ((lane & 7) ^ ((4 * p + (lane >> 4)) & 7));
+        off[p] = (lane >> 3) * a.k + col[p];
+    }
+    // A window never reaches past its row: the last one starts earlier.  Rows of
+    // fewer than four scales (a block a wave) come a scale a token.
+    const bool narrow = a.groups < 4;
+    const int scale_off = lane * a.groups * 4, scale_step = narrow ? 4 : 16;
+    auto window = [&](int s) { return max(0, min(s, a.groups - 4)); };
+    auto issue = [&](int s, int slot, int v) {
+        const lds_ptr at = mine + slot * L::SLOT;
+        const int left = s < upto ? a.k - s * BLOCK : 0;                 // columns from this block on
+        const int here[2] = {col[0] < left ? off[0] + s * BLOCK : PAST, col[1] < left ? off[1] + s * BLOCK : PAST};
+        if (v == 0) {
+            const lds_ptr to = mine + L::WINDOWS + ((s - from) / 4 & 1) * 1024;
+            const int from_row = s < upto ? scale_off + (narrow ? s : window(s)) * 4 : PAST;
+            if (narrow) lds_load4(buf_s, from_row, to);
+            else lds_load16(buf_s, from_row, to);
         }
-        p.ws = ws[b];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) p.xs[t] = xs[t][b];
+        for (int i = 0; i < 2 * RF; ++i) lds_load16_as<ONCE>(buf_w, here[i & 1] + 8 * i * a.k, at + i * 1024);
+#pragma unroll
+        for (int i = 0; i < TL; ++i) lds_load16(buf_a, here[i & 1] + 8 * i * a.k, at + L::TOKENS + i * 1024);
     };
-    auto add = [&](const Part& p) {
-        v4f s[NT];
+    const int n = lane & 15, g = lane >> 4;
+    const int first = n * BLOCK + ((g ^ (n >> 1)) << 4);                 // of this lane's pieces g and 4 + g of its row
+    auto read = [&](lds_ptr row, v4u (&x)[2]) {
+        x[0] = *(__attribute__((address_space(3))) const v4u*)(row + first);
+        x[1] = *(__attribute__((address_space(3))) const v4u*)(row + (first ^ 64));
+    };
+    const float* ws = a.ws + (int64_t)(n0 / BLOCK) * a.groups;           // (16 RF rows lie in one block of 128)
+    v4f acc[RF][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
-        if constexpr (BF16OUT) {
+    for (int i = 0; i < RF; ++i)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                s[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(p.w[0], p.w[1]), join(p.x[t][0], p.x[t][1]), s[t], 0, 0, 0,
-                                                                        ONE_E8M0, 0, ONE_E8M0);
-        } else {
+        for (int t = 0; t < NT; ++t) acc[i][t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const v8bf wf = eight_bf16(p.w[h >> 1][2 * (h & 1)], p.w[h >> 1][2 * (h & 1) + 1]);
+    for (int d = 0; d < RING; ++d) issue(from + d, d, d % 4);
+    int slot = 0;
+    auto block = [&](int s, auto nth) {
+        constexpr int V = decltype(nth)::value;                          // its number in the window
+        const lds_ptr at = mine + slot * L::SLOT;
+        const lds_ptr scales = mine + L::WINDOWS + ((s - from) / 4 & 1) * 1024 + (narrow ? 0 : s - window(s - V)) * 4;
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L::later(V)) : "memory");
+        v4u w[RF][2], x[NT][2];
+        float f[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        wf, eight_bf16(p.x[t][h >> 1][2 * (h & 1)], p.x[t][h >> 1][2 * (h & 1) + 1]), s[t], 0, 0, 0);
-            }
+        for (int i = 0; i < RF; ++i) read(at + 16 * i * BLOCK, w[i]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            read(at + L::TOKENS + 16 * t * BLOCK, x[t]);
+            f[t] = *(__attribute__((address_space(3))) const float*)(scales + (16 * t + n) * scale_step);
+        }
+        const float by = uniform(ws, s);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");               // the slot is read
+        issue(s + RING, slot, (V + RING) % 4);
+        slot = slot + 1 == RING ? 0 : slot + 1;
+        v8bf wide[RF][BF16OUT ? 1 : 4];
+        if constexpr (!BF16OUT) {
+#pragma unroll
+            for (int i = 0; i < RF; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) wide[i][h] = eight_bf16(w[i][h >> 1][2 * (h & 1)], w[i][h >> 1][2 * (h & 1) + 1]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float f = p.xs[t] * p.ws;
+            v4f p[RF];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(s[t][e], f, acc[t][e]);
+            for (int i = 0; i < RF; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
+            if constexpr (BF16OUT) {
+#pragma unroll
+                for (int i = 0; i < RF; ++i)
+                    p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w[i][0], w[i][1]), join(x[t][0], x[t][1]), p[i], 0, 0, 0,
+                                                                            ONE_E8M0, 0, ONE_E8M0);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const v8bf y = eight_bf16(x[t][h >> 1][2 * (h & 1)], x[t][h >> 1][2 * (h & 1) + 1]);
+#pragma unroll
+                    for (int i = 0; i < RF; ++i) p[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide[i][h], y, p[i], 0, 0, 0);
+                }
+            }
+            const float to = f[t] * by;
+#pragma unroll
+            for (int i = 0; i < RF; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][t][e] = fmaf(p[i][e], to, acc[i][t][e]);
         }
     };
-    for (int b = wave; b < a.groups; b += WAVES) {
-        Part p;
-        load(b, p);
-        add(p);
+    for (int s = from; s < upto; s += 4) {
+        block(s, std::integral_constant<int, 0>{});
+        if (s + 1 < upto) block(s + 1, std::integral_constant<int, 1>{});
+        if (s + 2 < upto) block(s + 2, std::integral_constant<int, 2>{});
+        if (s + 3 < upto) block(s + 3, std::integral_constant<int, 3>{});
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) part[wave][t][lane] = acc[t];
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                     // nothing is on its way into LDS any more
     __syncthreads();
-    for (int i = threadIdx.x; i < NT * 64; i += WAVES * 64) {
-        v4f sum = part[0][i / 64][i % 64];
+    auto* part = (__attribute__((address_space(3))) v4f*)smem;           // [WAVES][RF NT][64]
+#pragma unroll
+    for (int i = 0; i < RF; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[(wave * RF * NT + i * NT + t) * 64 + lane] = acc[i][t];
+    __syncthreads();
+    for (int c = wave; c < RF * NT; c += WAVES) {
+        v4f sum = part[c * 64 + lane];
 #pragma unroll
         for (int v = 1; v < WAVES; ++v) {
-            const v4f z = part[v][i / 64][i % 64];
+            const v4f z = part[(v * RF * NT + c) * 64 + lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] += z[e];
         }
-        const int m = m0 + i / 64 * 16 + i % 16, n = n0 + i % 64 / 16 * 4;
-        if (m >= a.m) continue;
+        const int t = c % NT * 16 + n, row = n0 + c / NT * 16 + 4 * g;
+        if (t >= rows_a) continue;
+        const int64_t to = (int64_t)(m0 + t) * a.n + row;
+        if (a.n % 4 == 0) {
+            if (row >= a.n) continue;
+            if constexpr (BF16OUT) *reinterpret_cast<v2u*>((uint16_t*)a.y + to) = v2u{bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+            else *reinterpret_cast<v4f*>((float*)a.y + to) = sum;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < a.n) store<BF16OUT>(a.y, (int64_t)m * a.n + n + e, sum[e]);
+            for (int e = 0; e < 4; ++e)
+                if (row + e < a.n) store<BF16OUT>(a.y, to + e, sum[e]);
+        }
     }
 }
 
-template <int NT, bool BF16OUT>
+template <int TL, int RF, int WAVES, int RING, bool ONCE, bool BF16OUT>
 hipError_t go_few(const B128Args& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.n + 15) / 16), (unsigned)((a.m + FEW_TOKENS - 1) / FEW_TOKENS));
-    b128_few_kernel<NT, 8, BF16OUT><<<grid, 512, 0, stream>>>(a);
+    using L = Few<TL, RF, WAVES, RING>;
+    auto kernel = b128_few_kernel<TL, RF, WAVES, RING, ONCE, BF16OUT>;
+    static LdsLimit limit;
+    if (hipError_t e = limit.raise((const void*)kernel, L::LDS); e != hipSuccess) return e;
+    const int64_t tiles = ((int64_t)(a.n + 16 * RF - 1) / (16 * RF)) * ((a.m + 8 * TL - 1) / (8 * TL));
+    kernel<<<(unsigned)tiles, WAVES * 64, L::LDS, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -185,40 +307,18 @@ struct Output {
     static constexpr int PITCH = ROWS * SIZE + 16, BYTES = TOKENS * PITCH;
 };
 
-typedef __attribute__((address_space(3))) unsigned char* lds_ptr;
-constexpr int PAST = 0x40000000;         // an offset outside every buffer here: reads as zeros
-
-__device__ __forceinline__ v4i buffer(const void* base, int64_t bytes) {
-    const uint64_t at = reinterpret_cast<uint64_t>(base);
-    return v4i{(int)(uint32_t)at, (int)(uint32_t)(at >> 32) & 0xFFFF, (int)bytes, 0x00027000};
-}
-// 16 (4) bytes a lane into LDS at dst + 16 (4) lane, no registers between;
-// whoever reads them waits for the loads himself.
-__device__ __forceinline__ void lds_load16(v4i r, int off, lds_ptr dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r) : "memory", "m0");
-}
-__device__ __forceinline__ void lds_load4(v4i r, int off, lds_ptr dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 ::"s"((uint32_t)(uintptr_t)dst), "v"(off), "s"(r) : "memory", "m0");
-}
-
-// The products run LAG steps ahead of the rescales, so that no rescale waits for
-// its product.  Operands are read one column of products ahead, also across
+// The products run some steps ahead of the rescales, so that no rescale waits for
+// its product.  Operands are read a column of products ahead, also across
 // stages: the barrier at which the next stage has arrived (and this one has been
-// read by all) stands before the last column.
-template <int WR, int WT, int FI, int FT, bool BF16OUT>
+// read by all) stands before the end of a stage.
+template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT>
 __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) {
     using T = Tile<WR, WT, FI, FT>;
     extern __shared__ __align__(16) unsigned char smem[];
     const lds_ptr lds = (lds_ptr)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous range of
-    // tiles, tokens first, so that those that share an L2 read the same rows.
-    const int tiles_m = (a.m + T::TOKENS - 1) / T::TOKENS;
-    const int each = (int)gridDim.x / 8, more = (int)gridDim.x % 8, xcd = blockIdx.x % 8;
-    const int tile = xcd * each + min(xcd, more) + blockIdx.x / 8;
-    const int m0 = tile % tiles_m * T::TOKENS, n0 = tile / tiles_m * T::ROWS;
+    const Place place((a.m + T::TOKENS - 1) / T::TOKENS, (a.n + T::ROWS - 1) / T::ROWS);
+    const int m0 = place.m * T::TOKENS, n0 = place.n * T::ROWS;
     const int rows_w = min(a.n - n0, T::ROWS), rows_a = min(a.m - m0, T::TOKENS);
     const int from = blockIdx.y * a.per, upto = min(from + a.per, a.groups);     // this workgroup's blocks
 
@@ -247,7 +347,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
             const bool is_w = q < T::ROWS / 8;
             lds_load16(is_w ? buf_w : buf_a, mine[q & 1] + (8 * (is_w ? q : q - T::ROWS / 8) * a.k + s * BLOCK), at + q * 1024);
         }
-        if (lo == 0) lds_load4(buf_s, s < upto ? scales_off + s * 4 : PAST, at + scales_at);
+        if (lo == 0 && hi > 0) lds_load4(buf_s, s < upto ? scales_off + s * 4 : PAST, at + scales_at);
     };
 
     const int wr = wave % WR * FI * 16, wt = wave / WR * FT * 16;
@@ -263,93 +363,138 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    constexpr int Q = FI * FT, LAG = BF16OUT ? 3 : 1;
-    v4f acc[FI][FT], p[LAG + 1];
+    v4f acc[FI][FT];
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
         for (int j = 0; j < FT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i <= LAG; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    // Operands: codes as they are, or (FP32 outputs) as BF16, a block's 128 columns in four steps.
-    struct Codes {
-        v4u x[2];
-    };
-    struct Wide {
-        v8bf x[4];
-    };
-    using Operand = std::conditional_t<BF16OUT, Codes, Wide>;
-    auto operand = [&](const v4u (&x)[2]) {
-        Operand o;
-        if constexpr (BF16OUT) {
-            o.x[0] = x[0], o.x[1] = x[1];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o.x[e] = eight_bf16(x[e >> 1][2 * (e & 1)], x[e >> 1][2 * (e & 1) + 1]);
-        }
-        return o;
-    };
-    auto product = [&](const Operand& w, const Operand& t) {
-        v4f x = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (BF16OUT) {
-            x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w.x[0], w.x[1]), join(t.x[0], t.x[1]), x, 0, 0, 0, ONE_E8M0, 0, ONE_E8M0);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.x[e], t.x[e], x, 0, 0, 0);
-        }
-        return x;
-    };
     auto rescale = [&](v4f& c, const v4f& x, float by) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] = fmaf(x[e], by, c[e]);
     };
     const float* ws = a.ws + (int64_t)min((n0 + wr) / BLOCK, (a.n - 1) / BLOCK) * a.groups;
-    Operand w[FI], t;
-    v4u wn[FI][2], tn[2];
-    float raw = 0.f, f = 0.f, f_last = 0.f;
+    // A stage has Q steps of one product; its barrier stands before step TURN.
+    // From there on the loads of the stage after the next go out, one in GAP steps
+    // (all at once, the waves would queue at the address unit with no products on
+    // their way: 182 us instead of 171 for 1792 x 17408 x 5120): the first ones in
+    // this stage, the others in the next.
+    constexpr int Q = FI * FT, TURN = Q - (FP8 ? FI : 2 * FI), GAP = FP8 ? 2 : 1;
+    auto issue_at = [&](int s, int q) {
+#pragma unroll
+        for (int l = 0; l < T::LOADS; ++l) {
+            const int at = TURN + l * GAP;
+            if (at < Q ? q == at : q == at - Q) issue(at < Q ? s + 2 : s + 1, l, l + 1);
+        }
+    };
+    static_assert(TURN + (T::LOADS - 1) * GAP - Q < TURN, "all loads of a stage before its barrier");
+    constexpr int SOONER = (Q - TURN + GAP - 1) / GAP < T::LOADS ? (Q - TURN + GAP - 1) / GAP : T::LOADS;     // of them, those before the stage ends
     if (from < upto) {
         issue(from, 0, T::LOADS);
         arrived();
-        issue(from + 1, 0, T::LOADS);
-#pragma unroll
-        for (int i = 0; i < FI; ++i) read(lds + (wr + 16 * i) * BLOCK, wn[i]);
-        read(lds + (T::ROWS + wt) * BLOCK, tn);
-        raw = read_scale(lds, 0);
+        issue(from + 1, 0, SOONER);
     }
-    for (int s = from; s < upto; ++s) {
-        const lds_ptr at = lds + ((s - from) & 1) * T::STAGE, next = lds + ((s - from + 1) & 1) * T::STAGE;
-        const float by = uniform(ws, s);
+    const lds_ptr tokens = lds + (T::ROWS + wt) * BLOCK, rows = lds + wr * BLOCK;
+    if constexpr (FP8) {
+        constexpr int LAG = 3;
+        v4f p[LAG + 1];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int i = q % FI, j = q / FI;
-            if (i == 0) {
-                t = operand(tn);
-                if (j + 1 == FT) arrived();
-                f_last = f;
-                f = raw * by;
-                read((j + 1 < FT ? at : next) + (T::ROWS + wt + 16 * ((j + 1) % FT)) * BLOCK, tn);    // (past the last stage: bytes that no one uses)
-                raw = read_scale(j + 1 < FT ? at : next, (j + 1) % FT);
-            }
-            if (j == 0) w[i] = operand(wn[i]);
-            __builtin_amdgcn_sched_barrier(0);
-            p[q % (LAG + 1)] = product(w[i], t);
-            {
+        for (int i = 0; i <= LAG; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
+        v4u w[FI][2], t[2], tn[2];
+        float raw = 0.f, f = 0.f, f_last = 0.f;
+        if (from < upto) {
+#pragma unroll
+            for (int i = 0; i < FI; ++i) read(rows + 16 * i * BLOCK, w[i]);
+            read(tokens, tn);
+            raw = read_scale(lds, 0);
+        }
+        for (int s = from; s < upto; ++s) {
+            const int here = ((s - from) & 1) * T::STAGE, next = T::STAGE - here;
+            const float by = uniform(ws, s);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = q % FI, j = q / FI;
+                if (i == 0) {
+                    t[0] = tn[0], t[1] = tn[1];
+                    if (q == TURN) arrived();
+                    f_last = f;
+                    f = raw * by;
+                    const int slot = j + 1 < FT ? here : next;           // (past the last stage: bytes that no one uses)
+                    read(tokens + slot + 16 * ((j + 1) % FT) * BLOCK, tn);
+                    raw = read_scale(lds + slot, (j + 1) % FT);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                p[q % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w[i][0], w[i][1]), join(t[0], t[1]), v4f{0.f, 0.f, 0.f, 0.f},
+                                                                                    0, 0, 0, ONE_E8M0, 0, ONE_E8M0);
                 const int e = (q + Q - LAG) % Q;
                 rescale(acc[e % FI][e / FI], p[(q + 1) % (LAG + 1)], i < LAG ? f_last : f);
+                if (j + 1 == FT) read(rows + next + 16 * i * BLOCK, w[i]);
+                issue_at(s, q);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (j + 1 == FT) {
-                read(next + (wr + 16 * i) * BLOCK, wn[i]);
-                issue(s + 2, T::LOADS * i / FI, T::LOADS * (i + 1) / FI);
-            }
-            __builtin_amdgcn_sched_barrier(0);
         }
-    }
 #pragma unroll
-    for (int q = Q - LAG; q < Q; ++q) rescale(acc[q % FI][q / FI], p[q % (LAG + 1)], f);
+        for (int q = Q - LAG; q < Q; ++q) rescale(acc[q % FI][q / FI], p[q % (LAG + 1)], f);
+    } else {
+        // Codes become BF16 a column ahead of their products, a quarter a step, and
+        // are read another column before that; a weight row's right after its last
+        // use in the stage.
+        static_assert(FI == 4 && FT % 2 == 0, "");
+        auto wide = [&](const v4u (&x)[2], int e) { return eight_bf16(x[e >> 1][2 * (e & 1)], x[e >> 1][2 * (e & 1) + 1]); };
+        v8bf w[FI][4], t[2][4];
+        v4u wn[FI][2], tn[2][2];
+        v4f last = {0.f, 0.f, 0.f, 0.f};
+        float raw[2], f = 0.f, f_last = 0.f;
+        if (from < upto) {
+#pragma unroll
+            for (int i = 0; i < FI; ++i) {
+                read(rows + 16 * i * BLOCK, wn[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[i][e] = wide(wn[i], e);
+            }
+            read(tokens, tn[0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[0][e] = wide(tn[0], e);
+            read(tokens + 16 * BLOCK, tn[1]);
+            raw[0] = read_scale(lds, 0);
+            raw[1] = read_scale(lds, 1);
+        }
+        for (int s = from; s < upto; ++s) {
+            const int here = ((s - from) & 1) * T::STAGE, next = T::STAGE - here;
+            const float by = uniform(ws, s);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = q % FI, j = q / FI;
+                if (i == 0) {
+                    if (q == TURN) arrived();
+                    f_last = f;
+                    f = raw[j & 1] * by;
+                    const int slot = j + 2 < FT ? here : next;
+                    read(tokens + slot + 16 * ((j + 2) % FT) * BLOCK, tn[j & 1]);
+                    raw[j & 1] = read_scale(lds + slot, (j + 2) % FT);
+                }
+                if (q >= Q - 2 * FI && q < Q - FI) read(rows + next + 16 * i * BLOCK, wn[i]);
+                __builtin_amdgcn_sched_barrier(0);
+                v4f x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i][e], t[j & 1][e], x, 0, 0, 0);
+                    if (j + 1 == FT) w[i][e] = wide(wn[i], e);
+                }
+                t[(j + 1) & 1][i] = wide(tn[(j + 1) & 1], i);
+                const int e = (q + Q - 1) % Q;
+                rescale(acc[e % FI][e / FI], last, i < 1 ? f_last : f);
+                last = x;
+                issue_at(s, q);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        rescale(acc[FI - 1][FT - 1], last, f);
+    }
     // A lane's outputs lie a token apart: through LDS they become pieces of whole
     // cache lines.  Each wave has a place of its own there, once all have read
     // their last stage and nothing is on its way into it.
     arrived();
+    char* const y = (char*)a.y + (int64_t)blockIdx.y * a.m * a.n * 4;    // (several workgroups a tile: FP32 parts, one after another)
     using Out = Output<FI, FT, BF16OUT>;
     const lds_ptr mine = lds + wave * Out::BYTES;
 #pragma unroll
@@ -367,7 +512,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         for (int b = lane; b < Out::TOKENS * Out::PIECES; b += 64) {
             const int m = m0 + wt + b / Out::PIECES, row = n0 + wr + b % Out::PIECES * Out::EACH;
             const v4u x = *(__attribute__((address_space(3))) const v4u*)(mine + b / Out::PIECES * Out::PITCH + b % Out::PIECES * 16);
-            if (m < a.m && row < a.n) *reinterpret_cast<v4u*>((char*)a.y + ((int64_t)m * a.n + row) * Out::SIZE) = x;
+            if (m < a.m && row < a.n) *reinterpret_cast<v4u*>(y + ((int64_t)m * a.n + row) * Out::SIZE) = x;
         }
     } else {
 #pragma unroll 4
@@ -375,45 +520,150 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
             const int m = m0 + wt + b / Out::ROWS, row = n0 + wr + b % Out::ROWS;
             const lds_ptr x = mine + b / Out::ROWS * Out::PITCH + b % Out::ROWS * Out::SIZE;
             if (m >= a.m || row >= a.n) continue;
-            if constexpr (BF16OUT) reinterpret_cast<uint16_t*>(a.y)[(int64_t)m * a.n + row] = *(__attribute__((address_space(3))) const uint16_t*)x;
-            else reinterpret_cast<float*>(a.y)[(int64_t)m * a.n + row] = *(__attribute__((address_space(3))) const float*)x;
+            if constexpr (BF16OUT) reinterpret_cast<uint16_t*>(y)[(int64_t)m * a.n + row] = *(__attribute__((address_space(3))) const uint16_t*)x;
+            else reinterpret_cast<float*>(y)[(int64_t)m * a.n + row] = *(__attribute__((address_space(3))) const float*)x;
         }
     }
 }
 
-template <int WR, int WT, int FI, int FT, bool BF16OUT>
-hipError_t go_tile(const B128Args& a, hipStream_t stream) {
+// The parts of each output, added in their order.
+template <bool BF16OUT>
+__global__ __launch_bounds__(256) void b128_join_kernel(const float* parts, int count, int64_t outputs, void* y) {
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at + 4 <= outputs && outputs % 4 == 0) {         // (parts stay 16-byte aligned)
+        v4f sum = *reinterpret_cast<const v4f*>(parts + at);
+        for (int i = 1; i < count; ++i) {
+            const v4f z = *reinterpret_cast<const v4f*>(parts + i * outputs + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += z[e];
+        }
+        if constexpr (BF16OUT) *reinterpret_cast<v2u*>((uint16_t*)y + at) = v2u{bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+        else *reinterpret_cast<v4f*>((float*)y + at) = sum;
+        return;
+    }
+    for (int64_t e = at; e < outputs && e < at + 4; ++e) {
+        float sum = parts[e];
+        for (int i = 1; i < count; ++i) sum += parts[i * outputs + e];
+        store<BF16OUT>(y, e, sum);
+    }
+}
+
+template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT>
+hipError_t go_tile(const B128Args& a, int splits, hipStream_t stream) {
     using T = Tile<WR, WT, FI, FT>;
     constexpr int OUT = T::WAVES * Output<FI, FT, BF16OUT>::BYTES, LDS = OUT > 2 * T::STAGE ? OUT : 2 * T::STAGE;
     static_assert(LDS <= 160 * 1024, "");
-    auto kernel = b128_tile_kernel<WR, WT, FI, FT, BF16OUT>;
+    auto kernel = b128_tile_kernel<WR, WT, FI, FT, FP8, BF16OUT>;
     static LdsLimit limit;
     if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
     const int64_t tiles = ((int64_t)(a.m + T::TOKENS - 1) / T::TOKENS) * ((a.n + T::ROWS - 1) / T::ROWS);
-    kernel<<<(unsigned)tiles, T::WAVES * 64, LDS, stream>>>(a);
+    kernel<<<dim3((unsigned)tiles, (unsigned)splits), T::WAVES * 64, LDS, stream>>>(a);
     return hipGetLastError();
 }
 
-template <bool BF16OUT>
-hipError_t go(const B128Args& a, hipStream_t stream) {
-    if (a.m > 128) {
-        if constexpr (BF16OUT) return go_tile<4, 2, 4, 8, BF16OUT>(a, stream);
-        else return go_tile<4, 2, 4, 4, BF16OUT>(a, stream);
+struct Plan {
+    enum { FEW, SMALL, MID, BIG } form;
+    int rows;                            // FEW: blocks of 16 weight rows a workgroup
+    int splits;                          // SMALL: workgroups a tile
+};
+
+// Up to 64 tokens: FEW, with 16 rows a workgroup while that gives no more
+// workgroups than CUs (or for up to 4 tokens, where the tokens' bytes do not
+// count), else 32.  Microseconds with 16 / 32 rows, K = 5120: 33 tokens, N = 1024
+// 5.9 / 7.2, 2048 6.3 / 7.6, 7168 14.2 / 11.4, 17408 31.8 / 27.7; one token, N =
+// 17408 16.8 / 17.9.
+//   More tokens: the form with the least time by what a block of 128 columns
+// takes each (nanoseconds, measured over 65 .. 8192 tokens, N 100 .. 17408, K 512
+// .. 17408), times the rounds in which its workgroups fill the CUs.  Measured
+// against each other (us):
+//                             FEW 16   32    64   SMALL (splits)    MID    BIG
+//   256 x 1024 x 2048          5.0   5.8   7.8   17.6              20.9   28.6
+//   128 x 7168 x 5120         33.1  22.2  16.9   49.5              61.5   65.4
+//   512 x 5120 x 17408         232   140   111    165, 91 (3)       202    258
+//   4800 x 600 x 2896         60.8  40.6  31.6   27.6              33.8   44.6
+//   1024 x 7168 x 5120         206   128    94   65.0              63.1   81.7
+//   2048 x 7168 x 5120         412   254   185    121               125   84.9
+//   2048 x 1024 x 2048, FP32  32.8  22.5  17.2   21.5
+Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus) {
+    auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+    const int64_t groups = up(k, BLOCK);
+#ifdef FORCE
+    FORCE
+#endif
+    if (m <= 64) return {Plan::FEW, up(n, 16) <= cus || m <= 4 ? 1 : 2, 1};
+    Plan best{Plan::FEW, 1, 1};
+    int64_t least = INT64_MAX;
+    auto consider = [&](const Plan& p, int64_t ns) {
+        if (ns < least) least = ns, best = p;
+    };
+    const int64_t few[3] = {165, 200, 350};
+    for (int i = 0; i < 3; ++i) consider({Plan::FEW, 1 << i, 1}, groups * few[i] * up(up(n, 16 << i) * up(m, 64), cus));
+    const int64_t tiles = up(n, 128) * up(m, 128);
+    for (int64_t z = 1; z <= 8 && (z == 1 || 4 * z <= groups); ++z) {
+        const int64_t one = bf16_out ? 1050 : 1100, two = bf16_out ? 1550 : 1900;           // workgroups on a CU
+        const int64_t join = z == 1 ? 0 : 2500 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
+        consider({Plan::SMALL, 0, (int)z}, up(groups, z) * (tiles * z <= cus ? one : two * up(tiles * z, 2 * cus)) + join);
     }
-    if (a.m <= 16) return go_few<1, BF16OUT>(a, stream);
-    if (a.m <= 32) return go_few<2, BF16OUT>(a, stream);
-    if (a.m <= 48) return go_few<3, BF16OUT>(a, stream);
-    return go_few<4, BF16OUT>(a, stream);
+    if (bf16_out) {
+        consider({Plan::MID, 0, 1}, groups * 1500 * up(up(n, 256) * up(m, 128), cus));
+        consider({Plan::BIG, 0, 1}, groups * 2100 * up(up(n, 256) * up(m, 256), cus));
+    }
+    return best;
+}
+
+template <int TL, bool BF16OUT>
+hipError_t go_few(const B128Args& a, int rows, hipStream_t stream) {
+    // Weights that are read once, and fill a good part of the caches, go past them (one token, 17408 x 5120: 19.9 -> 18.1 us with 32
+    // rows; 5120 x 6144, which stays in the last cache from call to call, 7.0 -> 8.0).
+    const bool once = a.m <= 8 * TL && (int64_t)a.n * a.k >= (64 << 20);
+    if constexpr (TL == 8) {
+        if (rows == 4) return go_few<TL, 4, 4, 2, false, BF16OUT>(a, stream);
+    }
+    if (rows == 2) return once ? go_few<TL, 2, 4, 2, true, BF16OUT>(a, stream) : go_few<TL, 2, 4, 2, false, BF16OUT>(a, stream);
+    return once ? go_few<TL, 1, 4, 2, true, BF16OUT>(a, stream) : go_few<TL, 1, 4, 2, false, BF16OUT>(a, stream);
+}
+
+template <bool BF16OUT>
+hipError_t go(B128Args a, const Plan& p, float* parts, hipStream_t stream) {
+    if (p.form == Plan::FEW) {
+        if (a.m <= 8) return go_few<1, BF16OUT>(a, p.rows, stream);
+        if (a.m <= 16) return go_few<2, BF16OUT>(a, p.rows, stream);
+        if (a.m <= 24) return go_few<3, BF16OUT>(a, p.rows, stream);
+        if (a.m <= 32) return go_few<4, BF16OUT>(a, p.rows, stream);
+        if (a.m <= 40) return go_few<5, BF16OUT>(a, p.rows, stream);
+        if (a.m <= 48) return go_few<6, BF16OUT>(a, p.rows, stream);
+        return go_few<8, BF16OUT>(a, p.rows, stream);
+    }
+    if constexpr (BF16OUT) {
+        if (p.form == Plan::BIG) return go_tile<4, 2, 4, 8, true, true>(a, 1, stream);
+        if (p.form == Plan::MID) return go_tile<4, 2, 4, 4, true, true>(a, 1, stream);
+    }
+    if (p.splits == 1) return go_tile<2, 2, 4, 4, BF16OUT, BF16OUT>(a, 1, stream);
+    void* y = a.y;
+    a.y = parts;
+    a.per = (a.groups + p.splits - 1) / p.splits;
+    if (hipError_t e = go_tile<2, 2, 4, 4, BF16OUT, false>(a, p.splits, stream); e != hipSuccess) return e;
+    const int64_t outputs = (int64_t)a.m * a.n;
+    b128_join_kernel<BF16OUT><<<(unsigned)((outputs + 1023) / 1024), 256, 0, stream>>>(parts, p.splits, outputs, y);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gemm_fp8_b128_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+int64_t gemm_fp8_b128_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    const int64_t cus = device_cu_count();
+    const int splits = max(plan(m, n, k, true, cus).splits, plan(m, n, k, false, cus).splits);
+    return splits > 1 ? splits * m * n * 4 : 0;
+}
 
 hipError_t launch_gemm_fp8_b128(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t m,
-                                int64_t n, int64_t k, bool bf16_out, void* y, void*, int64_t, hipStream_t stream) {
-    const B128Args args{a, a_scale, w, w_scale, (int)m, (int)n, (int)k, (int)((k + BLOCK - 1) / BLOCK), (int)((k + BLOCK - 1) / BLOCK), y};
-    return bf16_out ? go<true>(args, stream) : go<false>(args, stream);
+                                int64_t n, int64_t k, bool bf16_out, void* y, void* workspace, int64_t workspace_bytes,
+                                hipStream_t stream) {
+    const int groups = (int)((k + BLOCK - 1) / BLOCK);
+    const B128Args args{a, a_scale, w, w_scale, (int)m, (int)n, (int)k, groups, groups, y};
+    Plan p = plan(m, n, k, bf16_out, device_cu_count());
+    if (p.splits > 1 && workspace_bytes < p.splits * m * n * 4) p.splits = 1;
+    return bf16_out ? go<true>(args, p, (float*)workspace, stream) : go<false>(args, p, (float*)workspace, stream);
 }
 
 }  // namespace nq

@@ -58,7 +58,7 @@ def test_product_refusals(L):
                          ("gr", 2, S), ("gr", 4, S), ("gc", 8, S), ("gc", 10, S), ("wb", -1, S), ("out", 2, F), ("a", None, N),
                          ("a_scale", None, N), ("w", None, N), ("wsi", None, N), ("y", None, N), ("a", MIS, AL), ("w", A + 8, AL),
                          ("a_scale", MIS, AL), ("wsi", MIS, AL), ("y", MIS, AL), ("ws", A + 4, AL)])
-    for m, n in ((1 << 29, 1 << 29), (1 << 17, 1 << 19), ((1 << 31) - 1024, (1 << 31) - 1024)):
+    for m, n in ((1, 1 << 28), (64, 1 << 28), (1 << 29, 1 << 29), (1 << 17, 1 << 19), ((1 << 31) - 1024, (1 << 31) - 1024)):
         assert f(*dict(PRODUCT, M=m, N=n, gr=-(-n // 128)).values()) == S          # more tiles than a launch has
         assert L.nq_gemm_fp8_b128_workspace_bytes(m, n, 1040) == 0
     assert f(*dict(PRODUCT, M=0, a=None, y=None).values()) == nq.NQ_OK
