@@ -94,6 +94,8 @@ __device__ __forceinline__ void load_to_lds(v4i r, int off, lds_ptr dst) {
 
 // The 16 floats of r to LDS at dst, zeros to the 192 bytes behind them.
 __device__ __forceinline__ void load_scales(v4i r, int lane, lds_ptr dst) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);    // (the compiler may have it in vector registers)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  ::"s"((uint32_t)(uintptr_t)dst), "v"(lane * 4), "s"(r)
                  : "memory", "m0");
@@ -191,29 +193,21 @@ __device__ __forceinline__ void rows_made_finite(lds_ptr p, int lane) {
     }
 }
 
-// The scales of 32 staged keys, or of their values, where each row of the cache
-// has one: two groups of 16 floats in LDS, GROUP bytes apart (one load
+// The scales of 32 staged keys and of their values, where each row of the cache
+// has one: two groups of 16 floats each in LDS, GROUP bytes apart (one load
 // instruction fills GROUP bytes, zeros behind the 16).  They multiply the
-// logits, or the weights, of the keys: a lane's 16 registers are keys
+// logits, and the weights, of the keys: a lane's 16 registers are keys
 // 8 (i / 4) + 4 h + i % 4.
 struct NoScales {
     static constexpr bool ANY = false;
-    template <bool HIDE>
-    __device__ __forceinline__ void apply(v16f&, int) const {}
 };
 struct RowScales {
     static constexpr bool ANY = true;
     static constexpr int GROUP = 256;
-    lds_cptr at;
-    // HIDE: what is 0 stays 0 whatever the scale holds (the row may never have been written).
-    template <bool HIDE>
-    __device__ __forceinline__ void apply(v16f& x, int lane) const {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const v4f f = *(__attribute__((address_space(3))) const v4f*)(at + (e >> 1) * GROUP + (e & 1) * 32 + (lane >> 5) * 16);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[4 * e + j] = HIDE && x[4 * e + j] == 0.f ? 0.f : x[4 * e + j] * f[j];
-        }
+    lds_cptr k, v;
+    // Those of registers 4 e .. 4 e + 3.
+    __device__ __forceinline__ static v4f four(lds_cptr at, int e, int lane) {
+        return *(__attribute__((address_space(3))) const v4f*)(at + (e >> 1) * GROUP + (e & 1) * 32 + (lane >> 5) * 16);
     }
 };
 
@@ -314,8 +308,10 @@ struct Rows {
     // registers bear beside the rest.
     __device__ __forceinline__ static void in_order() { __builtin_amdgcn_sched_barrier(0x406); }
 
-    // S^T of the 32 keys at k.
-    __device__ __forceinline__ void logits(lds_cptr k, v16f& s) const {
+    // S^T of the 32 keys at k.  Their scales are read beside the last products.
+    template <class Scales>
+    __device__ __forceinline__ void logits(lds_cptr k, v16f& s, const Scales& scales) const {
+        v4f by[Scales::ANY ? 4 : 1];
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = 0.f;
         const int at = fresh(ka);
@@ -335,7 +331,18 @@ struct Rows {
                 s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(w), q[i], s, 0, 0, 0);
             }
             if (i + AHEAD < READS) x[i % AHEAD] = read(i + AHEAD);
+            else if constexpr (Scales::ANY) {
+                constexpr int LAST = AHEAD < READS ? AHEAD : READS;
+                const int d = i - (READS - LAST);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e >= 4 * d / LAST && e < 4 * (d + 1) / LAST) by[e] = RowScales::four(scales.k, e, lane);
+            }
             in_order();
+        }
+        if constexpr (Scales::ANY) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] *= by[i >> 2][i & 3];
         }
     }
 
@@ -367,8 +374,7 @@ struct Rows {
     // P^T of the 32 keys at k, with m, l and o brought along.
     template <bool HIDE, class Scales>
     __device__ __forceinline__ void weights(lds_cptr k, uint64_t seen, v16f& s, const Scales& scales) {
-        logits(k, s);
-        scales.template apply<false>(s, lane);
+        logits(k, s, scales);
         if (HIDE) hide(s, seen);
         float top = s[0];
 #pragma unroll
@@ -398,11 +404,17 @@ struct Rows {
     // The operand of 16 keys: registers i0 .. i0 + 7 of S^T, as BF16.  SPLITP:
     // as three BF16 terms, each but the last rounded from (1 - 2^-8) of what
     // is left, so that it stays below it and all terms are positive: an
-    // infinite value times them gives infinity, not infinity - infinity.
-    __device__ __forceinline__ static void p_frag(const v16f& p, int i0, v8bf (&out)[TERMS]) {
+    // infinite value times them gives infinity, not infinity - infinity.  by: the
+    // values' scales, which multiply the weights; HIDE: what is 0 because its key
+    // is hidden stays 0 whatever they hold (the row may never have been written).
+    template <bool HIDE, class Scales>
+    __device__ __forceinline__ static void p_frag(const v16f& p, int i0, const v4f* by, v8bf (&out)[TERMS]) {
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = p[i0 + j];
+        for (int j = 0; j < 8; ++j) {
+            x[j] = p[i0 + j];
+            if constexpr (Scales::ANY) x[j] = HIDE && x[j] == 0.f ? 0.f : x[j] * by[j >> 2][j & 3];
+        }
 #pragma unroll
         for (int e = 0; e < TERMS; ++e) {
             const float f = e + 1 < TERMS ? 0.99609375f : 1.0f;
@@ -420,9 +432,15 @@ struct Rows {
     }
 
     // O^T += V^T P^T over the 32 keys at v.
-    __device__ __forceinline__ void values(lds_cptr v, const v16f& p) {
+    template <bool HIDE, class Scales>
+    __device__ __forceinline__ void values(lds_cptr v, const v16f& p, const Scales& scales) {
         const int at = fresh(va);
         constexpr int AHEAD = FP8 ? 4 : 2;
+        v4f by[2];                                      // of 16 keys
+        if constexpr (Scales::ANY) {
+            by[0] = RowScales::four(scales.v, 0, lane);
+            by[1] = RowScales::four(scales.v, 1, lane);
+        }
         v4u x[AHEAD];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) x[i] = read_v(v, at, i / ND, i % ND);
@@ -430,7 +448,13 @@ struct Rows {
         v8bf pf[TERMS];
 #pragma unroll
         for (int i = 0; i < 2 * ND; ++i) {
-            if (i % ND == 0) p_frag(p, 8 * (i / ND), pf);
+            if (i % ND == 0) p_frag<HIDE, Scales>(p, 8 * (i / ND), by, pf);
+            if constexpr (Scales::ANY) {
+                if (i == ND - 2) {                      // the other 16 keys' scales
+                    by[0] = RowScales::four(scales.v, 2, lane);
+                    by[1] = RowScales::four(scales.v, 3, lane);
+                }
+            }
             const v8bf f = v_frag(x[i % AHEAD]);
 #pragma unroll
             for (int e = 0; e < TERMS; ++e) o[i % ND] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[e], o[i % ND], 0, 0, 0);

@@ -42,31 +42,44 @@ __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned ch
     constexpr int STEP = KEY_WAVES * 32;
     const Stager<D, FP8> st_k(lane, src.k_stride), st_v(lane, src.v_stride);
     const lds_ptr mine = (lds_ptr)smem + wave * L::WAVE;
-    auto load_k = [&](int key, int slot) {
-        st_k.rows16(src.k_rows(key), mine + slot * 2 * L::TILE);
-        st_k.rows16(src.k_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE / 2);
+    // A tile's rows are found once, for its K and its V loads.
+    typedef decltype(src.find(0)) At;
+    struct Tile32 {
+        At lo, hi;
+    };
+    auto find = [&](int key) { return Tile32{src.find(key), src.find(key + 16)}; };
+    auto load_k = [&](const Tile32& t, int slot) {
+        st_k.rows16(src.k_rows(t.lo), mine + slot * 2 * L::TILE);
+        st_k.rows16(src.k_rows(t.hi), mine + slot * 2 * L::TILE + L::TILE / 2);
         if constexpr (SCALED) {
-            load_scales(src.k_scales(key), lane, mine + L::SCALES + slot * L::SLOT_SCALES);
-            load_scales(src.k_scales(key + 16), lane, mine + L::SCALES + slot * L::SLOT_SCALES + RowScales::GROUP);
+            const lds_ptr to = mine + L::SCALES + slot * L::SLOT_SCALES;
+            load_scales(src.scales(src.ks, t.lo), lane, to);
+            load_scales(src.scales(src.ks, t.hi), lane, to + RowScales::GROUP);
         }
     };
-    auto load_v = [&](int key, int slot) {
-        st_v.rows16(src.v_rows(key), mine + slot * 2 * L::TILE + L::TILE);
-        st_v.rows16(src.v_rows(key + 16), mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
+    auto load_v = [&](const Tile32& t, int slot) {
+        st_v.rows16(src.v_rows(t.lo), mine + slot * 2 * L::TILE + L::TILE);
+        st_v.rows16(src.v_rows(t.hi), mine + slot * 2 * L::TILE + L::TILE + L::TILE / 2);
         if constexpr (SCALED) {
-            load_scales(src.v_scales(key), lane, mine + L::SCALES + slot * L::SLOT_SCALES + 2 * RowScales::GROUP);
-            load_scales(src.v_scales(key + 16), lane, mine + L::SCALES + slot * L::SLOT_SCALES + 3 * RowScales::GROUP);
+            const lds_ptr to = mine + L::SCALES + slot * L::SLOT_SCALES + 2 * RowScales::GROUP;
+            load_scales(src.scales(src.vs, t.lo), lane, to);
+            load_scales(src.scales(src.vs, t.hi), lane, to + RowScales::GROUP);
         }
     };
-    auto scales = [&](int slot, int groups) {
-        if constexpr (SCALED) return RowScales{mine + L::SCALES + slot * L::SLOT_SCALES + groups * RowScales::GROUP};
-        else return NoScales{};
+    auto scales = [&](int slot) {
+        if constexpr (SCALED) {
+            const lds_ptr at = mine + L::SCALES + slot * L::SLOT_SCALES;
+            return RowScales{at, at + 2 * RowScales::GROUP};
+        } else {
+            return NoScales{};
+        }
     };
     const int from = key0 + wave * 32;
 #pragma unroll
     for (int i = 0; i < L::RING; ++i) {
-        load_k(from + i * STEP, i);
-        load_v(from + i * STEP, i);
+        const Tile32 t = find(from + i * STEP);
+        load_k(t, i);
+        load_v(t, i);
     }
     queries();
     R.queries_ready();
@@ -76,10 +89,11 @@ __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned ch
         v16f x;
         uint64_t seen = 0;
         if (PARTLY) seen = sees.seen(key);
+        const Tile32 then = find(key + L::RING * STEP);             // (its loads are back by the time that they are needed)
         wait_vm<LATER>();
-        R.template weights<PARTLY>(k, seen, x, scales(slot, 0));
+        R.template weights<PARTLY>(k, seen, x, scales(slot));
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");          // K is read: its slot is free
-        load_k(key + L::RING * STEP, slot);
+        load_k(then, slot);
         wait_vm<LATER>();
         if (PARTLY) {
             if (const uint32_t bad = rows_not_finite<D, FP8, PIECES>(v, lane)) {
@@ -87,10 +101,9 @@ __device__ __forceinline__ void attend_keys(Rows<D, FP8, SPLITP>& R, unsigned ch
                 rows_made_finite<D, FP8, PIECES>(v, lane);
             }
         }
-        scales(slot, 2).template apply<PARTLY>(x, lane);
-        R.values(v, x);
+        R.template values<PARTLY>(v, x, scales(slot));
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        load_v(key + L::RING * STEP, slot);
+        load_v(then, slot);
     };
     const int clean = (sees.all_before() < key1 ? sees.all_before() : key1) - 32;
     int key = from, slot = 0;

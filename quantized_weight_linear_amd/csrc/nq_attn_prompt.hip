@@ -36,14 +36,15 @@ struct PackedRows {                 // K or V rows of one sequence and KV head
     const uint16_t *k, *v;
     int k_stride, v_stride;         // bytes
     int n, row_bytes;
-    __device__ __forceinline__ v4i k_rows(int key) const {
-        const int rows = n - key < 16 ? n - key : 16;
-        return rows_rsrc((const char*)k + (rows > 0 ? (int64_t)key * k_stride : 0), rows, k_stride, row_bytes);
+    struct At {
+        int key, rows;
+    };
+    __device__ __forceinline__ At find(int key) const { return At{key, n - key < 16 ? n - key : 16}; }
+    __device__ __forceinline__ v4i rows(const uint16_t* base, int stride, const At& at) const {
+        return rows_rsrc((const char*)base + (at.rows > 0 ? (int64_t)at.key * stride : 0), at.rows, stride, row_bytes);
     }
-    __device__ __forceinline__ v4i v_rows(int key) const {
-        const int rows = n - key < 16 ? n - key : 16;
-        return rows_rsrc((const char*)v + (rows > 0 ? (int64_t)key * v_stride : 0), rows, v_stride, row_bytes);
-    }
+    __device__ __forceinline__ v4i k_rows(const At& at) const { return rows(k, k_stride, at); }
+    __device__ __forceinline__ v4i v_rows(const At& at) const { return rows(v, v_stride, at); }
 };
 
 struct CausalSees {

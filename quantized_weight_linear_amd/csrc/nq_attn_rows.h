@@ -44,9 +44,10 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Source: k_rows(key) / v_rows(key) give the descriptor of 16 keys from a
-// 16-aligned key on (keys past the last one are outside it), k_stride /
-// v_stride the bytes between rows.
+// Source: find(key) finds 16 keys from a 16-aligned key on, k_rows / v_rows give
+// their descriptors (keys past the last one are outside them), scales(ks, ..)
+// and scales(vs, ..) those of their scales (SCALED), k_stride / v_stride the
+// bytes between rows.
 // Sees: all_before() = every row of the workgroup sees all keys below it;
 // none_from() = no row of this wave sees keys from it on; seen(key) = the
 // 64 keys from `key` on as bits, for this lane's row.
@@ -62,19 +63,31 @@ __device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds
     const int part = (wave & 1) * 16;
     const Stager<D, FP8> st(lane, is_k ? src.k_stride : src.v_stride);
     const lds_ptr k_ring = lds, v_ring = lds + 2 * L::TILE;
-    auto stage = [&](int i, int slot) {
-        const int key = key0 + i * KEYS + part;
-        if (is_k) st.rows16(src.k_rows(key), k_ring + slot * L::TILE + part * ROW);
-        else st.rows16(src.v_rows(key), v_ring + slot * L::TILE + part * ROW);
-        if constexpr (SCALED) load_scales(is_k ? src.k_scales(key) : src.v_scales(key), lane, lds + L::SCALES + (slot * 4 + wave) * RowScales::GROUP);
+    // The plane of this wave's scales, in scalar registers (chosen as a pointer, the compiler kept both planes in memory).
+    uint64_t plane = 0;
+    if constexpr (SCALED) {
+        plane = is_k ? (uint64_t)src.ks : (uint64_t)src.vs;
+        plane = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(plane >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)plane);
+    }
+    auto find = [&](int i) { return src.find(key0 + i * KEYS + part); };
+    typedef decltype(src.find(0)) At;
+    auto stage = [&](const At& at, int slot) {
+        if (is_k) st.rows16(src.k_rows(at), k_ring + slot * L::TILE + part * ROW);
+        else st.rows16(src.v_rows(at), v_ring + slot * L::TILE + part * ROW);
+        if constexpr (SCALED) load_scales(src.scales((const float*)plane, at), lane, lds + L::SCALES + (slot * 4 + wave) * RowScales::GROUP);
     };
-    auto scales = [&](int slot, int groups) {
-        if constexpr (SCALED) return RowScales{lds + L::SCALES + (slot * 4 + groups) * RowScales::GROUP};
-        else return NoScales{};
+    auto scales = [&](int slot) {
+        if constexpr (SCALED) {
+            const lds_ptr at = lds + L::SCALES + slot * 4 * RowScales::GROUP;
+            return RowScales{at, at + 2 * RowScales::GROUP};
+        } else {
+            return NoScales{};
+        }
     };
     if (key0 >= key1) return;
     const int n = (key1 - key0 + KEYS - 1) / KEYS;
-    stage(0, 0);
+    stage(find(0), 0);
+    At then = find(1);
     queries();
     R.queries_ready();
     auto step = [&](int i, int slot, auto partly) {
@@ -88,7 +101,8 @@ __device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds
             if (lane == 0) flags[wave] = rows;
         }
         lds_barrier();
-        stage(i + 1, slot ^ 1);
+        stage(then, slot ^ 1);
+        then = find(i + 2);                              // (a step ahead of its use)
         uint32_t bad = 0;
         bool some = true;
         uint64_t seen = 0;
@@ -98,17 +112,14 @@ __device__ __forceinline__ void attend_rows(Rows<D, FP8, SPLITP>& R, lds_ptr lds
             seen = sees.seen(key);
         }
         v16f s;
-        if (some) R.template weights<PARTLY>(k, seen, s, scales(slot, 0));
+        if (some) R.template weights<PARTLY>(k, seen, s, scales(slot));
         if (PARTLY && bad) {
             if (some) R.add_not_finite(v, bad, seen);
             lds_barrier();
             if (!is_k) rows_made_finite<D, FP8, LOADS>(v + part * ROW, lane);
             lds_barrier();
         }
-        if (some) {
-            scales(slot, 2).template apply<PARTLY>(s, lane);
-            R.values(v, s);
-        }
+        if (some) R.template values<PARTLY>(v, s, scales(slot));
     };
     const int clean = sees.all_before() - key0 < 0 ? 0 : (sees.all_before() - key0) / KEYS;
     int i = 0;

@@ -157,25 +157,22 @@ struct PagedRows {
     int64_t page_bytes, head_bytes; // bytes of a page; of the heads before this one
     int page_shift, total;
     static constexpr int k_stride = Tile<D, FP8>::ROW, v_stride = Tile<D, FP8>::ROW;
-    __device__ __forceinline__ v4i rows(const char* base, int key) const {
+    struct At {
+        int64_t bytes;              // place in a plane of the first row
+        int rows;
+    };
+    __device__ __forceinline__ At find(int key) const {
         int rows = total - key < 16 ? total - key : 16;
         const int64_t page = rows > 0 ? uniform(table, key >> page_shift) : -1;
         if (page < 0 || page >= pages) rows = 0;
-        const int64_t at = rows > 0 ? page * page_bytes + head_bytes + (int64_t)(key & ((1 << page_shift) - 1)) * k_stride : 0;
-        return rows_rsrc(base + at, rows, k_stride, k_stride);
+        return At{rows > 0 ? page * page_bytes + head_bytes + (int64_t)(key & ((1 << page_shift) - 1)) * k_stride : 0, rows};
     }
-    __device__ __forceinline__ v4i k_rows(int key) const { return rows(k, key); }
-    __device__ __forceinline__ v4i v_rows(int key) const { return rows(v, key); }
-    // The 16 rows' scales (zeros where there is no row), at the same place of their plane.
-    __device__ __forceinline__ v4i scales(const float* base, int key) const {
-        int rows = total - key < 16 ? total - key : 16;
-        const int64_t page = rows > 0 ? uniform(table, key >> page_shift) : -1;
-        if (page < 0 || page >= pages) rows = 0;
-        const int64_t at = rows > 0 ? (page * page_bytes + head_bytes) / k_stride + (key & ((1 << page_shift) - 1)) : 0;
-        return rows_rsrc(base + at, rows, 4, 4);
+    __device__ __forceinline__ v4i k_rows(const At& at) const { return rows_rsrc(k + at.bytes, at.rows, k_stride, k_stride); }
+    __device__ __forceinline__ v4i v_rows(const At& at) const { return rows_rsrc(v + at.bytes, at.rows, k_stride, k_stride); }
+    // The rows' scales, at the same place of their plane (ks or vs).
+    __device__ __forceinline__ v4i scales(const float* plane, const At& at) const {
+        return rows_rsrc((const char*)plane + ((uint64_t)at.bytes / k_stride * 4), at.rows, 4, 4);
     }
-    __device__ __forceinline__ v4i k_scales(int key) const { return scales(ks, key); }
-    __device__ __forceinline__ v4i v_scales(int key) const { return scales(vs, key); }
 };
 
 struct TreeSees {

@@ -225,22 +225,25 @@ _ACT_GROUP = {NQ_ACT_INT8_G64: 64, NQ_ACT_E4M3_B128: 128}
 
 def nq_rmsnorm(act_fmt, x, weight, eps, y, y_scale=None, residual=None, residual_out=None, weight_bias=0.0):
     """x [T][K], rows back to back or a slice of longer ones; residual_out may be residual."""
-    if x.dim() != 2 or x.dtype not in _TWO_BYTES:
+    shape = x.shape
+    if len(shape) != 2 or x.dtype not in _TWO_BYTES:
         raise ValueError("x: BF16 rows [T][K] expected")
-    t, k = x.shape
-    stride = x.stride(0) if t > 1 else k
-    if k > 1 and x.stride(1) != 1:
+    t, k = shape
+    stride, step = x.stride()
+    if step != 1 and k > 1:
         raise ValueError("x: a row's columns must be back to back")
     group = _ACT_GROUP.get(act_fmt)
-    for z, what in ((y, "y"), (residual, "residual"), (residual_out, "residual_out")):
-        if z is not None and (z.shape != x.shape or not z.is_contiguous() or z.dtype not in
-                              (_ONE_BYTE if what == "y" and group else _TWO_BYTES)):
-            raise ValueError(f"{what}: contiguous, the shape of x and the format's type expected")
-    if weight is not None and (weight.dtype not in _TWO_BYTES or weight.numel() != k):
-        raise ValueError("weight: BF16 [K] expected")
+    if y.shape != shape or y.dtype not in (_ONE_BYTE if group else _TWO_BYTES) or not y.is_contiguous():
+        raise ValueError("y: contiguous, the shape of x and the format's type expected")
+    rp = op = wp = None
+    if residual is not None:
+        rp = _like(residual, shape, "residual")
+        op = rp if residual_out is residual else None if residual_out is None else _like(residual_out, shape, "residual_out")
+    if weight is not None:
+        wp = _like(weight, (k,), "weight")
     sp = _floats(y_scale, t * -(-k // group), "y_scale") if group else None
-    _check((_lib or lib()).nq_rmsnorm(act_fmt, x.data_ptr() if x.numel() else None, stride, _ptr(residual), _ptr(residual_out),
-                                      _ptr(weight), weight_bias, eps, t, k, _ptr(y), sp, _stream(x)), "nq_rmsnorm")
+    _check((_lib or lib()).nq_rmsnorm(act_fmt, x.data_ptr(), stride if t > 1 else k, rp, op, wp, weight_bias, eps, t, k,
+                                      y.data_ptr(), sp, _stream(x)), "nq_rmsnorm")
 
 
 def nq_gemv_fp8row(w, w_scale, x, T, N, K, y, workspace=None):
@@ -448,6 +451,13 @@ def _rows(t, shape, what):
     return t.data_ptr(), s0 if n > 1 else h * d
 
 
+def _like(t, shape, what):
+    """Address of contiguous BF16 values of this shape."""
+    if t.shape != shape or t.dtype not in _TWO_BYTES or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous BF16 {list(shape)} expected")
+    return t.data_ptr()
+
+
 def _ints(t, n, what, types=_INT32):
     """Address of at least n integers."""
     if t.dtype not in types or t.numel() < n or not t.is_contiguous():
@@ -486,7 +496,10 @@ def _planes(fmt, k_pages, v_pages, hkv, d):
 
 def _scales(fmt, k_scale, v_scale, pages):
     """Addresses of the cache's scales: none, one a KV head, or one a row."""
-    n = 0 if fmt == NQ_KV_BF16 else pages.shape[1] if fmt == NQ_KV_E4M3 else pages.numel() // max(1, pages.shape[3])
+    if fmt == NQ_KV_BF16:
+        return None, None
+    p, h, ps, _ = pages.shape
+    n = h if fmt == NQ_KV_E4M3 else p * h * ps
     return _floats(k_scale, n, "k_scale"), _floats(v_scale, n, "v_scale")
 
 
@@ -538,30 +551,33 @@ def nq_kv_append_rope(fmt, q, k, v, positions, inv_freq, rope, k_scale, v_scale,
     if v.shape != kh:
         raise ValueError("k and v must have the same shape")
     t, hkv, d = kh
-    qp, qs, qop, qos, hq = None, 0, None, 0, hkv
+    qp = qop = kop = qwp = kwp = fp = pp = None
+    qs = qos = kos = rot = 0
+    hq = hkv
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        if q.shape != (t, hq, d) or q_out is None or q_out.shape != q.shape:
+        qh = q.shape
+        if len(qh) != 3 or qh[0] != t or qh[2] != d or q_out is None or q_out.shape != qh:
             raise ValueError("q and q_out: [T][Hq][D] with k's T and D expected")
-        (qp, qs), (qop, qos) = _rows(q, q.shape, "q"), _rows(q_out, q.shape, "q_out")
-    kop, kos = None, 0
+        hq = qh[1]
+        qp, qs = _rows(q, qh, "q")
+        qop, qos = (qp, qs) if q_out is q else _rows(q_out, qh, "q_out")
     if k_out is not None:
         if k_out.shape != kh:
             raise ValueError("k_out: the shape of k expected")
         kop, kos = _rows(k_out, kh, "k_out")
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype not in _TWO_BYTES or w.numel() != d):
-            raise ValueError(f"{what}: BF16 [D] expected")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    fp = None if inv_freq is None else _floats(inv_freq, rot // 2, "inv_freq")
-    pp = _ints(positions, t, "positions") if rot else None
+    if q_weight is not None:
+        qwp = _like(q_weight, (d,), "q_weight")
+    if k_weight is not None:
+        kwp = _like(k_weight, (d,), "k_weight")
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        fp, pp = _floats(inv_freq, 0, "inv_freq"), _ints(positions, t, "positions")
     tp, b, width = _table(page_table)
     kpp, vpp, ps, pages = _planes(fmt, k_pages, v_pages, hkv, d)
     ksp, vsp = _scales(fmt, k_scale, v_scale, k_pages)
-    _check((_lib or lib()).nq_kv_append_rope(fmt, qp, qs, kp, ks, vp, vs, _ptr(q_weight), _ptr(k_weight), weight_bias, eps, pp, fp,
-                                             rot, rope, ksp, vsp, tp, width, _ints(lens, b, "lens"), _ints(cu, b + 1, "cu"), b, t,
-                                             hq, hkv, d, ps, pages, qop, qos, kop, kos, kpp, vpp, _stream(k_pages)),
-           "nq_kv_append_rope")
+    _check((_lib or lib()).nq_kv_append_rope(fmt, qp, qs, kp, ks, vp, vs, qwp, kwp, weight_bias, eps, pp, fp, rot, rope, ksp, vsp, tp,
+                                             width, _ints(lens, b, "lens"), _ints(cu, b + 1, "cu"), b, t, hq, hkv, d, ps, pages,
+                                             qop, qos, kop, kos, kpp, vpp, _stream(k_pages)), "nq_kv_append_rope")
 
 
 def nq_attn_tree_workspace_bytes(B, max_q, Hq, Hkv, D, max_len):
