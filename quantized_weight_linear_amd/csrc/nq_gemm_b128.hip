@@ -26,7 +26,6 @@ namespace nq {
 namespace {
 
 constexpr int BLOCK = 128;               // columns of a scale
-constexpr int ONE_E8M0 = 0x7F7F7F7F;     // the instructions' own block scales: 1
 
 struct B128Args {
     const uint8_t* a;
@@ -218,7 +217,7 @@ __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
 #pragma unroll
                 for (int i = 0; i < RF; ++i)
                     p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w[i][0], w[i][1]), join(x[t][0], x[t][1]), p[i], 0, 0, 0,
-                                                                            ONE_E8M0, 0, ONE_E8M0);
+                                                                            0, 0, 0);
             } else {
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -288,14 +287,15 @@ hipError_t go_few(const B128Args& a, hipStream_t stream) {
 // rows and 16 WT FT tokens.  A stage is one block of 128 columns of both, in two
 // slots: row r of a panel at byte 128 r, its 16-byte piece c in place
 // c ^ (r / 2 % 8), so that operand reads (16 rows, one piece each) cover all
-// banks once; and the tokens' scales of the block.
+// banks once.  The tokens' scales come in windows of four blocks, 16 bytes a
+// token (one at a time, each load asks for 64 lines: 173 us instead of 160 for
+// 1792 x 17408 x 5120), in two slots of their own.
 template <int WR, int WT, int FI, int FT>
 struct Tile {
     static constexpr int WAVES = WR * WT, ROWS = 16 * WR * FI, TOKENS = 16 * WT * FT;
     static constexpr int LOADS = (ROWS + TOKENS) / 8 / WAVES;            // of 8 rows, a wave
-    static constexpr int SCALES = (ROWS + TOKENS) * BLOCK;               // their place in a stage
-    static constexpr int SINK = SCALES + TOKENS * 4;                     // of the waves that have no scales to load
-    static constexpr int STAGE = SINK + 256;
+    static constexpr int STAGE = (ROWS + TOKENS) * BLOCK;
+    static constexpr int WINDOWS = 2 * STAGE, WINDOW = TOKENS * 16, LDS = WINDOWS + 2 * WINDOW;
     static_assert((ROWS + TOKENS) % (8 * WAVES) == 0 && TOKENS % 64 == 0 && TOKENS / 64 <= WAVES && FT % 2 == 0, "");
     static_assert(BLOCK % (16 * FI) == 0, "a wave's rows lie in one block of the weights' scales");
 };
@@ -323,9 +323,14 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
     const int from = blockIdx.y * a.per, upto = min(from + a.per, a.groups);     // this workgroup's blocks
 
     const v4i buf_w = buffer(a.w + (int64_t)n0 * a.k, (int64_t)rows_w * a.k), buf_a = buffer(a.a + (int64_t)m0 * a.k, (int64_t)rows_a * a.k);
-    const bool has_scales = wave < T::TOKENS / 64;
-    const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, has_scales ? (int64_t)rows_a * a.groups * 4 : 0);
-    const int scales_at = has_scales ? T::SCALES + wave * 256 : T::SINK, scales_off = (64 * wave + lane) * a.groups * 4;
+    const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, (int64_t)rows_a * a.groups * 4);
+    // A window never reaches past its row: the last one starts earlier.
+    auto window = [&](int s) { return min(s - ((s - from) & 3), a.groups - 4); };
+    auto issue_window = [&](int s) {     // that of blocks s .. s + 3
+        if (wave < T::TOKENS / 64 && s < upto)
+            lds_load16(buf_s, ((64 * wave + lane) * a.groups + window(s)) * 4, lds + T::WINDOWS + ((s - from) / 4 & 1) * T::WINDOW + wave * 1024);
+    };
+    auto scales_of = [&](int s) { return T::WINDOWS + ((s - from) / 4 & 1) * T::WINDOW + (s - window(s)) * 4; };
 
     // Load i of this wave: rows 8 q .. 8 q + 7 of the panels (weights first), q =
     // wave LOADS + i.  No branches: past the last block, and of what lies past the
@@ -347,7 +352,6 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
             const bool is_w = q < T::ROWS / 8;
             lds_load16(is_w ? buf_w : buf_a, mine[q & 1] + (8 * (is_w ? q : q - T::ROWS / 8) * a.k + s * BLOCK), at + q * 1024);
         }
-        if (lo == 0 && hi > 0) lds_load4(buf_s, s < upto ? scales_off + s * 4 : PAST, at + scales_at);
     };
 
     const int wr = wave % WR * FI * 16, wt = wave / WR * FT * 16;
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         x[0] = *(__attribute__((address_space(3))) const v4u*)(row + first);
         x[1] = *(__attribute__((address_space(3))) const v4u*)(row + (first ^ 64));
     };
-    auto read_scale = [&](lds_ptr at, int j) { return *(__attribute__((address_space(3))) const float*)(at + T::SCALES + (wt + 16 * j + n) * 4); };
+    auto read_scale = [&](int at, int j) { return *(__attribute__((address_space(3))) const float*)(lds + at + (wt + 16 * j + n) * 16); };
     auto arrived = [&] {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -378,7 +382,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
     // (all at once, the waves would queue at the address unit with no products on
     // their way: 182 us instead of 171 for 1792 x 17408 x 5120): the first ones in
     // this stage, the others in the next.
-    constexpr int Q = FI * FT, TURN = Q - (FP8 ? FI : 2 * FI), GAP = FP8 ? 2 : 1;
+    constexpr int Q = FI * FT, TURN = Q - 2 * FI, GAP = FP8 && FT > 4 ? 2 : 1;
     auto issue_at = [&](int s, int q) {
 #pragma unroll
         for (int l = 0; l < T::LOADS; ++l) {
@@ -389,6 +393,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
     static_assert(TURN + (T::LOADS - 1) * GAP - Q < TURN, "all loads of a stage before its barrier");
     constexpr int SOONER = (Q - TURN + GAP - 1) / GAP < T::LOADS ? (Q - TURN + GAP - 1) / GAP : T::LOADS;     // of them, those before the stage ends
     if (from < upto) {
+        issue_window(from);
         issue(from, 0, T::LOADS);
         arrived();
         issue(from + 1, 0, SOONER);
@@ -399,38 +404,47 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         v4f p[LAG + 1];
 #pragma unroll
         for (int i = 0; i <= LAG; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
-        v4u w[FI][2], t[2], tn[2];
+        v4u w[2][FI][2], t[2][2];                                        // of even and odd stages; of even and odd columns
         float raw = 0.f, f = 0.f, f_last = 0.f;
         if (from < upto) {
 #pragma unroll
-            for (int i = 0; i < FI; ++i) read(rows + 16 * i * BLOCK, w[i]);
-            read(tokens, tn);
-            raw = read_scale(lds, 0);
+            for (int i = 0; i < FI; ++i) read(rows + 16 * i * BLOCK, w[0][i]);
+            read(tokens, t[0]);
+            raw = read_scale(scales_of(from), 0);
         }
-        for (int s = from; s < upto; ++s) {
-            const int here = ((s - from) & 1) * T::STAGE, next = T::STAGE - here;
+        auto stage = [&](int s, auto odd) {
+            constexpr int ODD = decltype(odd)::value;
+            int here = ODD * T::STAGE, next = T::STAGE - here;
+            asm volatile("" : "+s"(here), "+s"(next));                   // (addresses are formed as they are needed, not all kept in registers)
             const float by = uniform(ws, s);
+            const int scales = scales_of(s), scales_next = scales_of(min(s + 1, upto - 1));
+            if (((s + 2 - from) & 3) == 0) issue_window(s + 2);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 const int i = q % FI, j = q / FI;
+                if (q == TURN) arrived();
                 if (i == 0) {
-                    t[0] = tn[0], t[1] = tn[1];
-                    if (q == TURN) arrived();
                     f_last = f;
                     f = raw * by;
                     const int slot = j + 1 < FT ? here : next;           // (past the last stage: bytes that no one uses)
-                    read(tokens + slot + 16 * ((j + 1) % FT) * BLOCK, tn);
-                    raw = read_scale(lds + slot, (j + 1) % FT);
+                    read(tokens + slot + 16 * ((j + 1) % FT) * BLOCK, t[(j + 1) & 1]);
+                    raw = read_scale(j + 1 < FT ? scales : scales_next, (j + 1) % FT);
                 }
+                if (q >= TURN && (q - TURN) % 2 == 0) read(rows + next + 16 * ((q - TURN) / 2) * BLOCK, w[1 - ODD][(q - TURN) / 2]);
                 __builtin_amdgcn_sched_barrier(0);
-                p[q % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w[i][0], w[i][1]), join(t[0], t[1]), v4f{0.f, 0.f, 0.f, 0.f},
-                                                                                    0, 0, 0, ONE_E8M0, 0, ONE_E8M0);
+                p[q % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    join(w[ODD][i][0], w[ODD][i][1]), join(t[j & 1][0], t[j & 1][1]), v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
                 const int e = (q + Q - LAG) % Q;
                 rescale(acc[e % FI][e / FI], p[(q + 1) % (LAG + 1)], i < LAG ? f_last : f);
-                if (j + 1 == FT) read(rows + next + 16 * i * BLOCK, w[i]);
+                asm volatile("" : "+v"(acc[e % FI][e / FI]));            // (here, not beside its next use)
                 issue_at(s, q);
                 __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        static_assert(FI == 4 && FT % 2 == 0, "");
+        for (int s = from; s < upto; s += 2) {
+            stage(s, std::integral_constant<int, 0>{});
+            if (s + 1 < upto) stage(s + 1, std::integral_constant<int, 1>{});
         }
 #pragma unroll
         for (int q = Q - LAG; q < Q; ++q) rescale(acc[q % FI][q / FI], p[q % (LAG + 1)], f);
@@ -455,12 +469,14 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) t[0][e] = wide(tn[0], e);
             read(tokens + 16 * BLOCK, tn[1]);
-            raw[0] = read_scale(lds, 0);
-            raw[1] = read_scale(lds, 1);
+            raw[0] = read_scale(scales_of(from), 0);
+            raw[1] = read_scale(scales_of(from), 1);
         }
         for (int s = from; s < upto; ++s) {
             const int here = ((s - from) & 1) * T::STAGE, next = T::STAGE - here;
             const float by = uniform(ws, s);
+            const int scales = scales_of(s), scales_next = scales_of(min(s + 1, upto - 1));
+            if (((s + 2 - from) & 3) == 0) issue_window(s + 2);
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 const int i = q % FI, j = q / FI;
@@ -470,7 +486,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
                     f = raw[j & 1] * by;
                     const int slot = j + 2 < FT ? here : next;
                     read(tokens + slot + 16 * ((j + 2) % FT) * BLOCK, tn[j & 1]);
-                    raw[j & 1] = read_scale(lds + slot, (j + 2) % FT);
+                    raw[j & 1] = read_scale(j + 2 < FT ? scales : scales_next, (j + 2) % FT);
                 }
                 if (q >= Q - 2 * FI && q < Q - FI) read(rows + next + 16 * i * BLOCK, wn[i]);
                 __builtin_amdgcn_sched_barrier(0);
@@ -551,7 +567,7 @@ __global__ __launch_bounds__(256) void b128_join_kernel(const float* parts, int 
 template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT>
 hipError_t go_tile(const B128Args& a, int splits, hipStream_t stream) {
     using T = Tile<WR, WT, FI, FT>;
-    constexpr int OUT = T::WAVES * Output<FI, FT, BF16OUT>::BYTES, LDS = OUT > 2 * T::STAGE ? OUT : 2 * T::STAGE;
+    constexpr int OUT = T::WAVES * Output<FI, FT, BF16OUT>::BYTES, LDS = OUT > T::LDS ? OUT : T::LDS;
     static_assert(LDS <= 160 * 1024, "");
     auto kernel = b128_tile_kernel<WR, WT, FI, FT, FP8, BF16OUT>;
     static LdsLimit limit;
@@ -577,36 +593,34 @@ struct Plan {
 // .. 17408), times the rounds in which its workgroups fill the CUs.  Measured
 // against each other (us):
 //                             FEW 16   32    64   SMALL (splits)    MID    BIG
-//   256 x 1024 x 2048          5.0   5.8   7.8   17.6              20.9   28.6
-//   128 x 7168 x 5120         33.1  22.2  16.9   49.5              61.5   65.4
-//   512 x 5120 x 17408         232   140   111    165, 91 (3)       202    258
-//   4800 x 600 x 2896         60.8  40.6  31.6   27.6              33.8   44.6
-//   1024 x 7168 x 5120         206   128    94   65.0              63.1   81.7
-//   2048 x 7168 x 5120         412   254   185    121               125   84.9
-//   2048 x 1024 x 2048, FP32  32.8  22.5  17.2   21.5
+//   256 x 1024 x 2048          5.0   5.7   7.8   14.8              18.5   28.1
+//   96 x 7168 x 5120          29.1  19.7  16.0   41.3, 19.8 (4)    52.1   62.9
+//   512 x 5120 x 17408         234   140   111    138, 78 (3)       182    224
+//   4800 x 600 x 2896         62.0  40.5  31.7   25.4              32.1   42.0
+//   1024 x 7168 x 5120         206   127    95   57.8              57.7   70.3
+//   2048 x 7168 x 5120         414   251    186   107               114   75.9
+//   512 x 5120 x 5120, FP32   74.9  49.5  43.1   47.6, 41.7 (3)
 Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus) {
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t groups = up(k, BLOCK);
-#ifdef FORCE
-    FORCE
-#endif
     if (m <= 64) return {Plan::FEW, up(n, 16) <= cus || m <= 4 ? 1 : 2, 1};
     Plan best{Plan::FEW, 1, 1};
     int64_t least = INT64_MAX;
     auto consider = [&](const Plan& p, int64_t ns) {
         if (ns < least) least = ns, best = p;
     };
-    const int64_t few[3] = {165, 200, 350};
+    const int64_t few[3] = {150, 245, 360};
     for (int i = 0; i < 3; ++i) consider({Plan::FEW, 1 << i, 1}, groups * few[i] * up(up(n, 16 << i) * up(m, 64), cus));
+    if (groups < 4) return best;         // (the tiles' windows of scales need four)
     const int64_t tiles = up(n, 128) * up(m, 128);
     for (int64_t z = 1; z <= 8 && (z == 1 || 4 * z <= groups); ++z) {
-        const int64_t one = bf16_out ? 1050 : 1100, two = bf16_out ? 1550 : 1900;           // workgroups on a CU
-        const int64_t join = z == 1 ? 0 : 2500 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
+        const int64_t one = bf16_out ? 1050 : 1100, two = bf16_out ? 1350 : 1950;           // workgroups on a CU
+        const int64_t join = z == 1 ? 0 : 2300 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
         consider({Plan::SMALL, 0, (int)z}, up(groups, z) * (tiles * z <= cus ? one : two * up(tiles * z, 2 * cus)) + join);
     }
     if (bf16_out) {
-        consider({Plan::MID, 0, 1}, groups * 1500 * up(up(n, 256) * up(m, 128), cus));
-        consider({Plan::BIG, 0, 1}, groups * 2100 * up(up(n, 256) * up(m, 256), cus));
+        consider({Plan::MID, 0, 1}, groups * 1400 * up(up(n, 256) * up(m, 128), cus));
+        consider({Plan::BIG, 0, 1}, groups * 2000 * up(up(n, 256) * up(m, 256), cus));
     }
     return best;
 }
