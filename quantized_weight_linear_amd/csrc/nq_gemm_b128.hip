@@ -293,10 +293,10 @@ hipError_t go_few(const B128Args& a, hipStream_t stream) {
 template <int WR, int WT, int FI, int FT>
 struct Tile {
     static constexpr int WAVES = WR * WT, ROWS = 16 * WR * FI, TOKENS = 16 * WT * FT;
-    static constexpr int LOADS = (ROWS + TOKENS) / 8 / WAVES;            // of 8 rows, a wave
+    static constexpr int LOADS_W = ROWS / 8 / WAVES, LOADS_T = TOKENS / 8 / WAVES;          // of 8 rows, a wave
     static constexpr int STAGE = (ROWS + TOKENS) * BLOCK;
     static constexpr int WINDOWS = 2 * STAGE, WINDOW = TOKENS * 16, LDS = WINDOWS + 2 * WINDOW;
-    static_assert((ROWS + TOKENS) % (8 * WAVES) == 0 && TOKENS % 64 == 0 && TOKENS / 64 <= WAVES && FT % 2 == 0, "");
+    static_assert(ROWS % (8 * WAVES) == 0 && TOKENS % (8 * WAVES) == 0 && TOKENS % 64 == 0 && TOKENS / 64 <= WAVES && FT % 2 == 0, "");
     static_assert(BLOCK % (16 * FI) == 0, "a wave's rows lie in one block of the weights' scales");
 };
 
@@ -308,9 +308,7 @@ struct Output {
 };
 
 // The products run some steps ahead of the rescales, so that no rescale waits for
-// its product.  Operands are read a column of products ahead, also across
-// stages: the barrier at which the next stage has arrived (and this one has been
-// read by all) stands before the end of a stage.
+// its product.  Operands are read a column of products ahead, also across stages.
 template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT>
 __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) {
     using T = Tile<WR, WT, FI, FT>;
@@ -332,27 +330,16 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
     };
     auto scales_of = [&](int s) { return T::WINDOWS + ((s - from) / 4 & 1) * T::WINDOW + (s - window(s)) * 4; };
 
-    // Load i of this wave: rows 8 q .. 8 q + 7 of the panels (weights first), q =
-    // wave LOADS + i.  No branches: past the last block, and of what lies past the
-    // last column, nothing is read and zeros arrive.
-    int col[2], off[2];                  // the lane's piece, and its place, for even and odd q
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        col[p] = 16 * ((lane & 7) ^ ((4 * p + (lane >> 4)) & 7));
-        off[p] = (lane >> 3) * a.k + col[p];
-    }
-    auto issue = [&](int s, int lo, int hi) {
-        const lds_ptr at = lds + ((s - from) & 1) * T::STAGE;
-        const int left = s < upto ? a.k - s * BLOCK : 0;                 // columns from this block on
-        const int mine[2] = {col[0] < left ? off[0] : PAST, col[1] < left ? off[1] : PAST};
-#pragma unroll
-        for (int i = 0; i < T::LOADS; ++i) {
-            if (i < lo || i >= hi) continue;
-            const int q = wave * T::LOADS + i;
-            const bool is_w = q < T::ROWS / 8;
-            lds_load16(is_w ? buf_w : buf_a, mine[q & 1] + (8 * (is_w ? q : q - T::ROWS / 8) * a.k + s * BLOCK), at + q * 1024);
-        }
+    // Load i of this wave: rows 8 q .. 8 q + 7 of a panel, q = i WAVES + wave.  No
+    // branches: past the last block, and of what lies past the last column, nothing
+    // is read and zeros arrive.
+    const int col = 16 * ((lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7)), off = (8 * wave + (lane >> 3)) * a.k + col;
+    auto issue = [&](v4i buf, int panel, int s, int i) {
+        const int at = s < upto && col < a.k - s * BLOCK ? off : PAST;
+        lds_load16(buf, at + (8 * T::WAVES * i * a.k + s * BLOCK), lds + ((s - from) & 1) * T::STAGE + panel + (i * T::WAVES + wave) * 1024);
     };
+    auto issue_w = [&](int s, int i) { issue(buf_w, 0, s, i); };
+    auto issue_t = [&](int s, int i) { issue(buf_a, T::ROWS * BLOCK, s, i); };
 
     const int wr = wave % WR * FI * 16, wt = wave / WR * FT * 16;
     const int n = lane & 15, g = lane >> 4;
@@ -377,26 +364,48 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         for (int e = 0; e < 4; ++e) c[e] = fmaf(x[e], by, c[e]);
     };
     const float* ws = a.ws + (int64_t)min((n0 + wr) / BLOCK, (a.n - 1) / BLOCK) * a.groups;
-    // A stage has Q steps of one product; its barrier stands before step TURN.
-    // From there on the loads of the stage after the next go out, one in GAP steps
-    // (all at once, the waves would queue at the address unit with no products on
-    // their way: 182 us instead of 171 for 1792 x 17408 x 5120): the first ones in
-    // this stage, the others in the next.
-    constexpr int Q = FI * FT, TURN = Q - 2 * FI, GAP = FP8 && FT > 4 ? 2 : 1;
-    auto issue_at = [&](int s, int q) {
-#pragma unroll
-        for (int l = 0; l < T::LOADS; ++l) {
-            const int at = TURN + l * GAP;
-            if (at < Q ? q == at : q == at - Q) issue(at < Q ? s + 2 : s + 1, l, l + 1);
+    // A stage has Q steps of one product.  Its weight rows are in registers once
+    // the first FI steps are done: from a barrier there on the weights of the stage
+    // after the next go out, with almost two stages to arrive (weights come from
+    // memory more often than tokens do; with all loads after step TURN 1792 x 17408 x
+    // 5120 took 171 us instead of 151, 1024 x 7168 x 5120 57 instead of 48, and half
+    // the tokens' loads from a third barrier on gained nothing).  The reads of its last
+    // tokens are out before step TURN (they are read one column ahead, two for FP32
+    // outputs): at the barrier there they are done, the next stage has arrived, and
+    // the tokens of the one after it go out.  One load in GAP steps (all at once, the
+    // waves would queue at the address unit with no products on their way).
+    constexpr int Q = FI * FT, TURN = FP8 ? Q - FI - 2 : Q - 2 * FI, GAP = FP8 && FT > 4 ? 2 : 1;
+    static_assert(FI + (T::LOADS_W - 1) * GAP < TURN && TURN + T::LOADS_T <= Q, "");
+    auto barriers = [&](int q) {
+        if (q == FI) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        }
+        if (q == TURN) {                 // (all but the weights of the stage after the next have arrived)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(T::LOADS_W) : "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
         }
     };
-    static_assert(TURN + (T::LOADS - 1) * GAP - Q < TURN, "all loads of a stage before its barrier");
-    constexpr int SOONER = (Q - TURN + GAP - 1) / GAP < T::LOADS ? (Q - TURN + GAP - 1) / GAP : T::LOADS;     // of them, those before the stage ends
+    auto issue_at = [&](int s, int q) {
+#pragma unroll
+        for (int i = 0; i < T::LOADS_W; ++i)
+            if (q == FI + i * GAP) issue_w(s + 2, i);
+#pragma unroll
+        for (int i = 0; i < T::LOADS_T; ++i)
+            if (q == TURN + i) issue_t(s + 2, i);
+    };
     if (from < upto) {
         issue_window(from);
-        issue(from, 0, T::LOADS);
-        arrived();
-        issue(from + 1, 0, SOONER);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < T::LOADS_W; ++i) issue_w(from + s, i);
+#pragma unroll
+            for (int i = 0; i < T::LOADS_T; ++i) issue_t(from + s, i);
+            if (s == 0) arrived();
+        }
     }
     const lds_ptr tokens = lds + (T::ROWS + wt) * BLOCK, rows = lds + wr * BLOCK;
     if constexpr (FP8) {
@@ -422,7 +431,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 const int i = q % FI, j = q / FI;
-                if (q == TURN) arrived();
+                barriers(q);
                 if (i == 0) {
                     f_last = f;
                     f = raw * by;
@@ -430,7 +439,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
                     read(tokens + slot + 16 * ((j + 1) % FT) * BLOCK, t[(j + 1) & 1]);
                     raw = read_scale(j + 1 < FT ? scales : scales_next, (j + 1) % FT);
                 }
-                if (q >= TURN && (q - TURN) % 2 == 0) read(rows + next + 16 * ((q - TURN) / 2) * BLOCK, w[1 - ODD][(q - TURN) / 2]);
+                if (q >= TURN && q < TURN + FI) read(rows + next + 16 * (q - TURN) * BLOCK, w[1 - ODD][q - TURN]);
                 __builtin_amdgcn_sched_barrier(0);
                 p[q % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     join(w[ODD][i][0], w[ODD][i][1]), join(t[j & 1][0], t[j & 1][1]), v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
@@ -456,7 +465,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         auto wide = [&](const v4u (&x)[2], int e) { return eight_bf16(x[e >> 1][2 * (e & 1)], x[e >> 1][2 * (e & 1) + 1]); };
         v8bf w[FI][4], t[2][4];
         v4u wn[FI][2], tn[2][2];
-        v4f last = {0.f, 0.f, 0.f, 0.f};
+        v4f last[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         float raw[2], f = 0.f, f_last = 0.f;
         if (from < upto) {
 #pragma unroll
@@ -478,33 +487,43 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
             const int scales = scales_of(s), scales_next = scales_of(min(s + 1, upto - 1));
             if (((s + 2 - from) & 3) == 0) issue_window(s + 2);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
+            for (int q = 0; q < Q; q += 2) {                             // two products at once: neither waits for its own sum
                 const int i = q % FI, j = q / FI;
+                barriers(q);
                 if (i == 0) {
-                    if (q == TURN) arrived();
                     f_last = f;
                     f = raw[j & 1] * by;
                     const int slot = j + 2 < FT ? here : next;
                     read(tokens + slot + 16 * ((j + 2) % FT) * BLOCK, tn[j & 1]);
                     raw[j & 1] = read_scale(j + 2 < FT ? scales : scales_next, (j + 2) % FT);
                 }
-                if (q >= Q - 2 * FI && q < Q - FI) read(rows + next + 16 * i * BLOCK, wn[i]);
+                if (q >= Q - 2 * FI && q < Q - FI) {
+                    read(rows + next + 16 * i * BLOCK, wn[i]);
+                    read(rows + next + 16 * (i + 1) * BLOCK, wn[i + 1]);
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                v4f x = {0.f, 0.f, 0.f, 0.f};
+                v4f x[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i][e], t[j & 1][e], x, 0, 0, 0);
-                    if (j + 1 == FT) w[i][e] = wide(wn[i], e);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        x[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i + h][e], t[j & 1][e], x[h], 0, 0, 0);
+                        if (j + 1 == FT) w[i + h][e] = wide(wn[i + h], e);
+                    }
                 }
-                t[(j + 1) & 1][i] = wide(tn[(j + 1) & 1], i);
-                const int e = (q + Q - 1) % Q;
-                rescale(acc[e % FI][e / FI], last, i < 1 ? f_last : f);
-                last = x;
-                issue_at(s, q);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    t[(j + 1) & 1][i + h] = wide(tn[(j + 1) & 1], i + h);
+                    const int e = (q + Q - 2 + h) % Q;
+                    rescale(acc[e % FI][e / FI], last[h], i == 0 ? f_last : f);
+                    last[h] = x[h];
+                    issue_at(s, q + h);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        rescale(acc[FI - 1][FT - 1], last, f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rescale(acc[FI - 2 + h][FT - 1], last[h], f);
     }
     // A lane's outputs lie a token apart: through LDS they become pieces of whole
     // cache lines.  Each wave has a place of its own there, once all have read
@@ -593,13 +612,13 @@ struct Plan {
 // .. 17408), times the rounds in which its workgroups fill the CUs.  Measured
 // against each other (us):
 //                             FEW 16   32    64   SMALL (splits)    MID    BIG
-//   256 x 1024 x 2048          5.0   5.7   7.8   14.8              18.5   28.1
-//   96 x 7168 x 5120          29.1  19.7  16.0   41.3, 19.8 (4)    52.1   62.9
-//   512 x 5120 x 17408         234   140   111    138, 78 (3)       182    224
-//   4800 x 600 x 2896         62.0  40.5  31.7   25.4              32.1   42.0
-//   1024 x 7168 x 5120         206   127    95   57.8              57.7   70.3
-//   2048 x 7168 x 5120         414   251    186   107               114   75.9
-//   512 x 5120 x 5120, FP32   74.9  49.5  43.1   47.6, 41.7 (3)
+//   256 x 1024 x 2048          5.1   5.8   7.8   13.6              17.0   26.9
+//   96 x 7168 x 5120          29.1  19.8  16.1   31.2, 17.6 (4)    41.4   57.9
+//   512 x 5120 x 17408         233   140   111    104, 68 (3)       133    186
+//   4800 x 600 x 2896         61.4  40.4  31.6   20.6              26.2   37.8
+//   1024 x 7168 x 5120         205   127    94   48.7              45.9   62.6
+//   2048 x 7168 x 5120         414   251   185   93.1              91.3   70.9
+//   512 x 5120 x 5120, FP32   76.3  49.1  42.8   45.7, 39.8 (3)
 Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus) {
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t groups = up(k, BLOCK);
@@ -609,17 +628,17 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus) {
     auto consider = [&](const Plan& p, int64_t ns) {
         if (ns < least) least = ns, best = p;
     };
-    const int64_t few[3] = {150, 245, 360};
+    const int64_t few[3] = {150, 245, 380};
     for (int i = 0; i < 3; ++i) consider({Plan::FEW, 1 << i, 1}, groups * few[i] * up(up(n, 16 << i) * up(m, 64), cus));
     if (groups < 4) return best;         // (the tiles' windows of scales need four)
     const int64_t tiles = up(n, 128) * up(m, 128);
     for (int64_t z = 1; z <= 8 && (z == 1 || 4 * z <= groups); ++z) {
-        const int64_t one = bf16_out ? 1050 : 1100, two = bf16_out ? 1350 : 1950;           // workgroups on a CU
-        const int64_t join = z == 1 ? 0 : 2300 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
+        const int64_t one = bf16_out ? 900 : 1150, two = bf16_out ? 1450 : 2100;           // workgroups on a CU
+        const int64_t join = z == 1 ? 0 : 2500 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
         consider({Plan::SMALL, 0, (int)z}, up(groups, z) * (tiles * z <= cus ? one : two * up(tiles * z, 2 * cus)) + join);
     }
     if (bf16_out) {
-        consider({Plan::MID, 0, 1}, groups * 1400 * up(up(n, 256) * up(m, 128), cus));
+        consider({Plan::MID, 0, 1}, groups * 1300 * up(up(n, 256) * up(m, 128), cus));
         consider({Plan::BIG, 0, 1}, groups * 2000 * up(up(n, 256) * up(m, 256), cus));
     }
     return best;
