@@ -646,7 +646,9 @@ nq_status nq_rmsnorm(int act_fmt, const uint16_t* x, int64_t x_stride, const uin
                      void* stream) {
     if (act_fmt != NQ_ACT_BF16 && act_fmt != NQ_ACT_INT8_G64 && act_fmt != NQ_ACT_E4M3_B128) return NQ_ERR_FORMAT;
     const int64_t unit = act_fmt == NQ_ACT_BF16 ? 8 : act_fmt == NQ_ACT_INT8_G64 ? 64 : 16;
-    if (T < 0 || T >= MOST_BLOCKS || K < 0 || K > 32768 || K % unit != 0 || !stride_ok(x_stride, 1, K)) return NQ_ERR_SHAPE;
+    // (long rows take workgroups of up to 1024 threads)
+    if (T < 0 || T >= (K > 6144 ? MOST_BLOCKS / 4 : MOST_BLOCKS) || K < 0 || K > 32768 || K % unit != 0 || !stride_ok(x_stride, 1, K))
+        return NQ_ERR_SHAPE;
     if (!scale_ok(eps)) return NQ_ERR_RANGE;
     if (T == 0 || K == 0) return NQ_OK;
     NQ_TRY(all_at<16>(x, y));

@@ -190,16 +190,15 @@ hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
 
 template <int FMT>
 hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
-    const int pieces = (a.k + 7) / 8;
-    if (pieces <= 64) return go_norm<FMT, 256, 4, 1>(a, stream);
-    if (pieces <= 128) return go_norm<FMT, 256, 4, 2>(a, stream);
-    if (pieces <= 256) return go_norm<FMT, 256, 1, 1>(a, stream);
-    if (pieces <= 512) return go_norm<FMT, 256, 1, 2>(a, stream);
-    if (pieces <= 768) return go_norm<FMT, 256, 1, 3>(a, stream);
-    if (pieces <= 1024) return go_norm<FMT, 512, 1, 2>(a, stream);
-    if (pieces <= 1536) return go_norm<FMT, 512, 1, 3>(a, stream);
-    if (pieces <= 2048) return go_norm<FMT, 1024, 1, 2>(a, stream);
-    if (pieces <= 3072) return go_norm<FMT, 1024, 1, 3>(a, stream);
+    if (a.k <= 64 * 8) return go_norm<FMT, 256, 4, 1>(a, stream);
+    if (a.k <= 64 * 16) return go_norm<FMT, 256, 4, 2>(a, stream);
+    if (a.k <= 256 * 8) return go_norm<FMT, 256, 1, 1>(a, stream);
+    if (a.k <= 256 * 16) return go_norm<FMT, 256, 1, 2>(a, stream);
+    if (a.k <= 256 * 24) return go_norm<FMT, 256, 1, 3>(a, stream);
+    if (a.k <= 512 * 16) return go_norm<FMT, 512, 1, 2>(a, stream);
+    if (a.k <= 512 * 24) return go_norm<FMT, 512, 1, 3>(a, stream);
+    if (a.k <= 1024 * 16) return go_norm<FMT, 1024, 1, 2>(a, stream);
+    if (a.k <= 1024 * 24) return go_norm<FMT, 1024, 1, 3>(a, stream);
     return go_norm<FMT, 1024, 1, 4>(a, stream);
 }
 

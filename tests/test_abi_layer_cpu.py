@@ -34,6 +34,8 @@ def test_norm_refusals(L):
                       ("eps", math.inf, R), ("x", None, N), ("y", None, N), ("scale", None, N), ("res_out", None, N), ("x", MIS, AL),
                       ("res", MIS, AL), ("res_out", MIS, AL), ("w", MIS, AL), ("y", MIS, AL), ("scale", MIS, AL), ("y", A + 8, AL)])
     assert f(*dict(NORM, fmt=1, K=5104, xs=5104).values()) == S       # groups of 64
+    for fmt in (0, 1, 2):                                             # more threads than a launch has
+        assert f(*dict(NORM, fmt=fmt, T=1 << 22, K=6208, xs=6208).values()) == S
     assert f(*dict(NORM, fmt=0, K=5116, xs=5120).values()) == S       # 16-byte pieces
     assert f(*dict(NORM, T=0, x=None, y=None).values()) == nq.NQ_OK
     assert f(*dict(NORM, K=0, x=None, y=None).values()) == nq.NQ_OK

@@ -145,6 +145,16 @@ def test_norm_is_the_norm_of_what_is_kept():
         assert s is None or torch.equal(s, s2)
 
 
+def test_norm_of_more_values_than_31_bits_count():
+    t, k = 530000, 4096
+    x, w = rand(gen(9), 4000, k), rand(gen(10), k)
+    x = x[torch.arange(t, device=DEV) % 4000]
+    want, scale, _ = run_norm(nq.NQ_ACT_E4M3_B128, x[:4000], w)
+    got, scales, _ = run_norm(nq.NQ_ACT_E4M3_B128, x, w)
+    same_bits(got[-4000:], want[torch.arange(t - 4000, t, device=DEV) % 4000])
+    same_bits(scales[-4000:], scale[torch.arange(t - 4000, t, device=DEV) % 4000])
+
+
 def test_norm_repeats_its_bits():
     g = gen(9)
     x, w = rand(g, 300, 5120), rand(g, 5120)
@@ -183,6 +193,12 @@ def test_quantizer_not_finite():
     assert bool(scale[0, 0].isnan()) and bool(v[0, :128].isnan().all()) and bool((v[0, 128:] == 448).all())
     assert float(scale[1, 1]) == math.inf and bool((v[1, :128] == 448).all())
     assert bool(scale[2, 1].isnan()) and not bool(scale[2, 0].isnan())
+
+
+# An FP8 instruction adds its products in groups of eight and cuts each of them at 2^-13 of 2^e, e the largest sum of two
+# exponents in its group: up to seven cuts of the largest product a group, which is at most `size` over all groups.
+# (Codes below the smallest normal count with its exponent; in these tests none of them is a group's largest product.)
+CUT = 7 * 2.0 ** -13
 
 
 # ---- product --------------------------------------------------------------------------------------------------------
@@ -230,8 +246,10 @@ def check_product(a, a_s, w, w_s, out, **more):
     if out == torch.float32:
         within(y, ref, steps * size)
         assert float((y.double() - ref).norm()) <= 1e-5 * float(ref.norm())
-    else:           # an FP8 instruction keeps 2^-15 of its products' sizes (measured: 1.7e-5 of 3.05e-5)
-        within(y, ref, U16 * ref.abs() + (2.0 ** -15 + steps) * size * (1 + U16))
+    else:
+        within(y, ref, U16 * ref.abs() + (CUT + steps) * size * (1 + U16))
+        if y.numel() >= 1000:       # evenly spread between two BF16 values: at most half a step over sqrt(3); and the units' 1.8e-5
+            assert float((y.double() - ref).norm()) <= (U16 * 3 ** -0.5 + 3e-5) * float(ref.norm())
     return y
 
 
@@ -301,6 +319,44 @@ def test_product_scales_and_outputs_inside_larger_tensors():
     a2.copy_(a_s), w2.copy_(w_s)
     for m in (1, 40, 200):
         same_bits(run_product(a[:m], a_s[:m], w, w_s, BF), run_product(a[:m], a2[:m], w, w2, BF))
+
+
+@pytest.mark.parametrize("out", [BF, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(1000, 8200, 528), (990, 8203, 1168), (1000, 7100, 656), (777, 7001, 912), (2100, 4500, 1040), (1025, 1025, 4112)])
+def test_product_of_large_tiles(m, n, k, out):
+    """Tiles of 256 rows whose last ones are partly outside, blocks in odd and even numbers."""
+    check_product(*product_inputs(m, n, k, m + n + k), out)
+
+
+@pytest.mark.parametrize("m,n,k", [(70000, 32768, 16), (70000, 32768, 528), (64, 33600000, 16)])
+def test_product_of_more_outputs_than_31_bits_count(m, n, k):
+    a, a_s, w, w_s = product_inputs(m, min(n, 32768), k, 6)
+    if n > w.shape[0]:                                      # the same rows again and again
+        at = torch.arange(n, device=DEV) % 4096
+        w, w_s = w.view(torch.uint8)[at].view(F8), w_s[torch.arange(-(-n // 128), device=DEV) % 32].contiguous()
+    y = run_product(a, a_s, w, w_s, BF)
+    rows, cols = slice(m - 40, m), slice(n - 4000, n)
+    within(y[rows, cols], product64(a[rows], a_s[rows], w[n - 4096:], w_s[-32:])[:, -4000:],
+           U16 * y[rows, cols].double().abs() * (1 + U16) + (1 + U16) * CUT * product64(a[rows], a_s[rows], w[n - 4096:], w_s[-32:], absolute=True)[:, -4000:])
+
+
+def test_products_on_two_streams_at_once():
+    """Each stream with a workspace of its own."""
+    sets = [product_inputs(m, n, k, 8 + m) for m, n, k in ((200, 300, 4096), (33, 2000, 2048), (600, 4000, 1024), (300, 512, 5120))]
+    want = [run_product(*x, BF) for x in sets]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for x, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                m, n, k = x[0].shape[0], x[2].shape[0], x[0].shape[1]
+                ws, y = nq.alloc_gemm_fp8_b128_workspace(m, n, k, DEV), torch.empty((m, n), dtype=BF, device=DEV)
+                nq.nq_gemm_fp8_b128(x[0].view(torch.uint8), x[1], x[2].view(torch.uint8), x[3], m, n, k, y, ws)
+                got.append((y, ws))
+        torch.cuda.synchronize()
+        for a, (b, _) in zip(want, got):
+            same_bits(a, b)
 
 
 # ---- rotated append -------------------------------------------------------------------------------------------------
@@ -642,6 +698,34 @@ def test_attend_token_scales_hidden_rows_hold_anything():
         assert not bool(res[0][0][2].isfinite().any())
 
 
+@pytest.mark.parametrize("new", [1, 9])
+def test_append_and_attend_in_pages_past_32_bits(new):
+    """The last pages of a pool of more than 2^32 bytes a plane give the bits that the first pages of a small one give."""
+    hq, hkv, d, page, pages, total = 16, 4, 256, 64, 70000, 500
+    g = gen(77)
+    q, k, v = rand(g, total, hq, d), rand(g, total, hkv, d), rand(g, total, hkv, d)
+    pos, freq = torch.arange(total, device=DEV, dtype=torch.int32), (1e4 ** (-torch.arange(0, 64, 2, device=DEV, dtype=torch.float64) / 64)).float()
+    mask = torch.tensor([(2 << i) - 1 for i in range(new)], dtype=torch.int64, device=DEV)
+    got = []
+    for n, base in ((8, 0), (pages, pages - 8)):
+        planes = [torch.empty((n, hkv, page, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        scales = [torch.empty((n, hkv, page), device=DEV) for _ in range(2)]
+        table = torch.arange(base, base + 8, device=DEV, dtype=torch.int32).flip(0).view(1, -1).contiguous()
+        q_out, o = torch.empty_like(q), torch.empty((new, hq, d), dtype=BF, device=DEV)
+        nq.nq_kv_append_rope(nq.NQ_KV_E4M3_TOKEN, q, k, v, pos, freq, nq.NQ_ROPE_HALVES, *scales, table, i32([0]), i32([0, total]), q_out, *planes)
+        nq.nq_attn_tree(nq.NQ_KV_E4M3_TOKEN, q_out[-new:], *planes, *scales, table, i32([total - new]), i32([0, new]), mask, new, total, d ** -0.5, o,
+                        workspace=nq.alloc_attn_tree_workspace(1, new, hq, hkv, d, total, DEV))
+        got.append((q_out, o, *(x[base:base + 8].clone() for x in (*planes, *scales))))
+        del planes, scales
+    filled = torch.zeros((8, page), dtype=torch.bool, device=DEV)
+    at = torch.arange(total, device=DEV)
+    filled[7 - at // page, at % page] = True
+    for a, b in zip(got[0], got[1]):
+        if a.shape[:1] == (8,):
+            a, b = (x.transpose(1, 2)[filled] for x in (a, b))
+        same_bits(a, b)
+
+
 def test_attend_token_scales_empty_rows():
     d, hq, hkv = 64, 4, 2
     cache = Cache(nq.NQ_KV_E4M3_TOKEN, hkv, d, 16, 4)
@@ -759,7 +843,7 @@ def test_layer_step_against_64_bits():
         within(deq, y, y.abs() * U8 * 1.001 + L.scales[0].double().repeat_interleave(128, 1) * 2.0 ** -10)
         a = (L.codes[0].view(F8), L.scales[0])
         ref, size = product64(*a, *L.weights[0]), product64(*a, *L.weights[0], absolute=True)
-        within(L.qkv, ref, U16 * ref.abs() + 2.0 ** -14 * size)
+        within(L.qkv, ref, U16 * ref.abs() + CUT * size)
         rows = L.qkv.view(L.t, -1, L.D)
         q = turned64(rows[:, :L.HQ], L.qw, 1.0, 1e-6, pos, L.freq, False)
         within(L.q_out, q, U16 * q.abs() + 1e-5)
@@ -767,7 +851,7 @@ def test_layer_step_against_64_bits():
         within(L.o, o, U16 * o.abs() + (U16 + 1e-4) * size)
         out = product64(L.codes[1].view(F8), L.scales[1], *L.weights[1])
         size = product64(L.codes[1].view(F8), L.scales[1], *L.weights[1], absolute=True)
-        within(L.out, out, U16 * out.abs() + 2.0 ** -14 * size)
+        within(L.out, out, U16 * out.abs() + CUT * size)
         same_bits(L.res, (h.float() + L.out.float()).to(BF))
 
 
