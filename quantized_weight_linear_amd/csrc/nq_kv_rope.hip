@@ -8,8 +8,9 @@
 // workgroup has one token (or some heads of it): its angles' cosines and sines are worked
 // out once, in FP64 up to the fraction of a turn, since an FP32 angle of a far
 // position is off by more than a thousandth, and all heads read them from LDS.
-//   Each element is read once and written once; bound by HBM for prompts and
-// by latency for steps.
+//   Each element is read once and written once; bound by HBM for prompts (12800
+// tokens of 32 / 8 heads of 128 in BF16: 64.5 us, 4.9 TB/s) and by latency for
+// steps (one token: 4.0 us).
 #include <hip/hip_runtime.h>
 
 #include "nq.h"
@@ -149,10 +150,14 @@ __global__ __launch_bounds__(256) void kv_append_rope_kernel(RopeArgs a) {
     }
 }
 
+// Few tokens: a workgroup for each round of heads; many: one for all heads of a
+// token, which works its angles out once.  24 / 4 heads of 256, normalised, into
+// E4M3 rows with a scale each (us): 1 token 4.0 / 7.0, 64 4.4 / 7.5, 512 9.0 /
+// 9.7, 4096 44 / 37.5.
 template <int FMT>
 hipError_t go_rope(const RopeArgs& a, hipStream_t stream) {
     const int at_once = 256 * 8 / a.d, rounds = (a.hq + 2 * a.hkv + at_once - 1) / at_once;
-    const dim3 grid((unsigned)a.t, (unsigned)(a.t <= 256 ? rounds : 1));
+    const dim3 grid((unsigned)a.t, (unsigned)(a.t <= 512 ? rounds : 1));
     if (a.d == 64) kv_append_rope_kernel<FMT, 64><<<grid, 256, 0, stream>>>(a);
     else if (a.d == 128) kv_append_rope_kernel<FMT, 128><<<grid, 256, 0, stream>>>(a);
     else kv_append_rope_kernel<FMT, 256><<<grid, 256, 0, stream>>>(a);

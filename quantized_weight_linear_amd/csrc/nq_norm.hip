@@ -5,7 +5,8 @@
 //
 // A row stays in registers between its two passes (the sum of squares, then
 // the output), so every byte is read and written once.  Bound by HBM where
-// rows are many, by latency where they are few.
+// rows are many (16383 x 5120 in BF16: 69.7 us, 4.8 TB/s; 1792 with the residual
+// and E4M3 out: 15.6 us, 4.1 TB/s), by latency where they are few (one row: 3.8 us).
 //   h is rounded to BF16 before it is normalised: it is what the next layer
 // adds to, so the norm is that of the stored residual, fused or not.  Squares
 // are summed in FP64, which costs nothing beside the loads and neither
@@ -83,23 +84,20 @@ __device__ __forceinline__ v2u codes_i8(const float (&f)[8], float s) {
     return v2u{w[0], w[1]};
 }
 
-// ROWS rows a workgroup of THREADS, THREADS / ROWS threads a row, PIECES
-// pieces of 8 columns a thread, piece i of thread n at 8 (i threads + n): a
-// scale's columns lie in 8 or 16 neighbouring lanes.
-template <int FMT, int THREADS, int ROWS, int PIECES, bool RESIDUAL>
+// A row a workgroup of THREADS, PIECES pieces of 8 columns a thread, piece i of
+// thread n at 8 (i THREADS + n): a scale's columns lie in 8 or 16 neighbouring
+// lanes.
+template <int FMT, int THREADS, int PIECES, bool RESIDUAL>
 __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a) {
-    constexpr int PER = THREADS / ROWS, WAVES = PER / 64;
-    static_assert(PER % 64 == 0, "whole waves a row");
-    __shared__ double part[ROWS][WAVES > 1 ? WAVES : 1];
-    const int mine = threadIdx.x % PER, sub = threadIdx.x / PER;
-    const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
-    const bool live = t < a.t;
-    const uint16_t* x = a.x + (live ? t : 0) * a.xs;
-    const int64_t row = (live ? t : 0) * (int64_t)a.k;
+    constexpr int WAVES = THREADS / 64;
+    __shared__ double part[WAVES];
+    const int mine = threadIdx.x;
+    const int64_t t = blockIdx.x, row = t * a.k;
+    const uint16_t* x = a.x + t * a.xs;
     v4u h[PIECES], w[PIECES], r[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int col = (i * PER + mine) * 8;
+        const int col = (i * THREADS + mine) * 8;
         h[i] = r[i] = w[i] = v4u{0u, 0u, 0u, 0u};
         if (col < a.k) {
             h[i] = *reinterpret_cast<const v4u*>(x + col);
@@ -110,7 +108,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a) {
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int col = (i * PER + mine) * 8;
+        const int col = (i * THREADS + mine) * 8;
         float f[8];
         unpack8(h[i], f);
         if (RESIDUAL) {
@@ -118,7 +116,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a) {
             unpack8(r[i], g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[i][j] = f32_to_bf16_rne(f[2 * j] + g[2 * j]) | f32_to_bf16_rne(f[2 * j + 1] + g[2 * j + 1]) << 16;
-            if (live && col < a.k) *reinterpret_cast<v4u*>(a.residual_out + row + col) = h[i];
+            if (col < a.k) *reinterpret_cast<v4u*>(a.residual_out + row + col) = h[i];
             unpack8(h[i], f);
         }
 #pragma unroll
@@ -127,22 +125,22 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
     if constexpr (WAVES > 1) {
-        if ((threadIdx.x & 63) == 0) part[sub][mine / 64] = sum;
+        if ((threadIdx.x & 63) == 0) part[mine / 64] = sum;
         __syncthreads();
         sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) sum += part[sub][i];
+        for (int i = 0; i < WAVES; ++i) sum += part[i];
     }
     const double rstd = 1.0 / __builtin_sqrt(sum / (double)a.k + a.eps);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int col = (i * PER + mine) * 8;
+        const int col = (i * THREADS + mine) * 8;
         float f[8], g[8];
         unpack8(h[i], f);
         unpack8(w[i], g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = (float)((double)f[j] * rstd) * (g[j] + a.bias);
-        const bool store = live && col < a.k;
+        const bool store = col < a.k;
         if constexpr (FMT == NQ_ACT_BF16) {
             v4u o;
 #pragma unroll
@@ -180,26 +178,42 @@ __global__ __launch_bounds__(256) void quantize_fp8_b128_kernel(const uint16_t* 
     if (threadIdx.x % 16 == 0) scale[g] = s;
 }
 
-template <int FMT, int THREADS, int ROWS, int PIECES>
+template <int FMT, int THREADS, int PIECES>
 hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
-    const unsigned blocks = (unsigned)((a.t + ROWS - 1) / ROWS);
-    if (a.residual) rmsnorm_kernel<FMT, THREADS, ROWS, PIECES, true><<<blocks, THREADS, 0, stream>>>(a);
-    else rmsnorm_kernel<FMT, THREADS, ROWS, PIECES, false><<<blocks, THREADS, 0, stream>>>(a);
+    const unsigned blocks = (unsigned)a.t;
+    if (a.residual) rmsnorm_kernel<FMT, THREADS, PIECES, true><<<blocks, THREADS, 0, stream>>>(a);
+    else rmsnorm_kernel<FMT, THREADS, PIECES, false><<<blocks, THREADS, 0, stream>>>(a);
     return hipGetLastError();
 }
 
+// As few pieces a thread as there are, since a row waits for its sum and its
+// pieces come one after another; with many rows, more of them on a CU count for
+// more.  Microseconds, residual and E4M3 output:
+//                       1 row            1792            16384
+//   512:    64 x 1   2.3            3.5              13.0
+//          256 x 1/4 2.4 (4 rows)   3.5              14.3
+//   1024:  128 x 1   2.5            5.0              23.7
+//          256 x 2/4 3.2 (4 rows)   5.3              25.9
+//   4096:  512 x 1   2.9           12.8              85.7
+//          256 x 2   3.4           13.6              74.8
+//   5120:  512 x 2   3.8           17.4             129
+//          256 x 3   4.3           17.4             112
+//   8192:  512 x 2   4.1           22.8             167
+//         1024 x 1   4.1           22.9             178
+//   12288: 512 x 3   5.2           36.0
+//         1024 x 2   5.6           44.3
 template <int FMT>
 hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
-    if (a.k <= 64 * 8) return go_norm<FMT, 256, 4, 1>(a, stream);
-    if (a.k <= 64 * 16) return go_norm<FMT, 256, 4, 2>(a, stream);
-    if (a.k <= 256 * 8) return go_norm<FMT, 256, 1, 1>(a, stream);
-    if (a.k <= 256 * 16) return go_norm<FMT, 256, 1, 2>(a, stream);
-    if (a.k <= 256 * 24) return go_norm<FMT, 256, 1, 3>(a, stream);
-    if (a.k <= 512 * 16) return go_norm<FMT, 512, 1, 2>(a, stream);
-    if (a.k <= 512 * 24) return go_norm<FMT, 512, 1, 3>(a, stream);
-    if (a.k <= 1024 * 16) return go_norm<FMT, 1024, 1, 2>(a, stream);
-    if (a.k <= 1024 * 24) return go_norm<FMT, 1024, 1, 3>(a, stream);
-    return go_norm<FMT, 1024, 1, 4>(a, stream);
+    if (a.k <= 64 * 8) return go_norm<FMT, 64, 1>(a, stream);
+    if (a.k <= 128 * 8) return go_norm<FMT, 128, 1>(a, stream);
+    if (a.k <= 256 * 8) return go_norm<FMT, 256, 1>(a, stream);
+    if (a.k <= 512 * 8) return a.t <= 1024 ? go_norm<FMT, 512, 1>(a, stream) : go_norm<FMT, 256, 2>(a, stream);
+    if (a.k <= 256 * 24) return a.t <= 1024 ? go_norm<FMT, 512, 2>(a, stream) : go_norm<FMT, 256, 3>(a, stream);
+    if (a.k <= 512 * 16) return go_norm<FMT, 512, 2>(a, stream);
+    if (a.k <= 512 * 24) return go_norm<FMT, 512, 3>(a, stream);
+    if (a.k <= 1024 * 16) return go_norm<FMT, 1024, 2>(a, stream);
+    if (a.k <= 1024 * 24) return go_norm<FMT, 1024, 3>(a, stream);
+    return go_norm<FMT, 1024, 4>(a, stream);
 }
 
 }  // namespace
