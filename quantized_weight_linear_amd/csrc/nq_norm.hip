@@ -186,28 +186,31 @@ hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// As few pieces a thread as there are, since a row waits for its sum and its
-// pieces come one after another; with many rows, more of them on a CU count for
-// more.  Microseconds, residual and E4M3 output:
-//                       1 row            1792            16384
-//   512:    64 x 1   2.3            3.5              13.0
-//          256 x 1/4 2.4 (4 rows)   3.5              14.3
-//   1024:  128 x 1   2.5            5.0              23.7
-//          256 x 2/4 3.2 (4 rows)   5.3              25.9
-//   4096:  512 x 1   2.9           12.8              85.7
-//          256 x 2   3.4           13.6              74.8
-//   5120:  512 x 2   3.8           17.4             129
-//          256 x 3   4.3           17.4             112
-//   8192:  512 x 2   4.1           22.8             167
-//         1024 x 1   4.1           22.9             178
-//   12288: 512 x 3   5.2           36.0
-//         1024 x 2   5.6           44.3
+// Few rows: as few pieces a thread as there are, since a row waits for its sum
+// and its pieces come one after another.  Many: workgroups half as large, of
+// which a CU holds more rows.  Microseconds, E4M3 output (the residual but for *):
+//                     1 row    1792   16384   65536 *
+//   512:   64 x 1      2.3      3.5    13.0    31
+//          64 x 2      2.8      4.3    17.3    42
+//   1024: 128 x 1      2.5      5.0    23.7    63
+//          64 x 2      3.1      5.2    23.6    52
+//   2048: 256 x 1      2.6      8.1    43.7    64 (32768)
+//         128 x 2      3.3      8.8    40.4    59
+//   4096: 512 x 1      2.9     12.8    85.7
+//         256 x 2      3.4     13.6    74.8
+//   5120: 512 x 2      3.8     17.4   129
+//         256 x 3      4.3     16.6   112
+//   8192: 512 x 2      4.1     22.8   167
+//         256 x 4      5.4     26.6   189
+//   12288: 512 x 3     5.2     36.0
+//         1024 x 2     5.6     44.3
 template <int FMT>
 hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
+    const bool few = a.t <= 2048;
     if (a.k <= 64 * 8) return go_norm<FMT, 64, 1>(a, stream);
-    if (a.k <= 128 * 8) return go_norm<FMT, 128, 1>(a, stream);
-    if (a.k <= 256 * 8) return go_norm<FMT, 256, 1>(a, stream);
-    if (a.k <= 512 * 8) return a.t <= 1024 ? go_norm<FMT, 512, 1>(a, stream) : go_norm<FMT, 256, 2>(a, stream);
+    if (a.k <= 128 * 8) return few ? go_norm<FMT, 128, 1>(a, stream) : go_norm<FMT, 64, 2>(a, stream);
+    if (a.k <= 256 * 8) return few ? go_norm<FMT, 256, 1>(a, stream) : go_norm<FMT, 128, 2>(a, stream);
+    if (a.k <= 512 * 8) return few ? go_norm<FMT, 512, 1>(a, stream) : go_norm<FMT, 256, 2>(a, stream);
     if (a.k <= 256 * 24) return a.t <= 1024 ? go_norm<FMT, 512, 2>(a, stream) : go_norm<FMT, 256, 3>(a, stream);
     if (a.k <= 512 * 16) return go_norm<FMT, 512, 2>(a, stream);
     if (a.k <= 512 * 24) return go_norm<FMT, 512, 3>(a, stream);

@@ -83,7 +83,8 @@ def check_norm(fmt, x, weight, residual=None, bias=0.0, eps=1e-6, in_place=False
 
 
 SHAPES = [(1, 64), (1, 128), (3, 192), (5, 448), (4, 512), (9, 576), (2, 1024), (7, 1088), (1, 2048), (3, 2112), (33, 5120), (1, 4160),
-          (2, 6144), (2, 8256), (3, 12288), (2, 12352), (2, 16384), (3, 17408), (1, 24640), (2, 32768), (1000, 256)]
+          (2, 6144), (2, 8256), (3, 12288), (2, 12352), (2, 16384), (3, 17408), (1, 24640), (2, 32768), (1000, 256), (2100, 704), (2100, 1088),
+          (2049, 4096), (1025, 5120)]
 
 
 @pytest.mark.parametrize("fmt", [nq.NQ_ACT_BF16, nq.NQ_ACT_INT8_G64, nq.NQ_ACT_E4M3_B128])
