@@ -103,8 +103,9 @@ struct Place {
 
 // ---- few tokens: every wave streams its own blocks ------------------------------------------------------------------
 
-// A workgroup has 16 RF weight rows and up to 8 TL tokens; its waves split the
-// blocks of 128 columns between them and join in LDS, in the order of the waves.
+// A workgroup has 16 RF weight rows and up to 8 TL tokens, and all blocks of 128
+// columns or a run of them; its waves split these between them and join in LDS, in
+// the order of the waves.
 // Each wave streams its blocks (weights, tokens and the tokens' scales) through a ring of RING
 // slots of its own in LDS, without barriers: from memory straight into LDS, since
 // there eight neighbouring lanes read a row's 128 bytes, where operand order
@@ -130,7 +131,7 @@ struct Few {
     static_assert(TL <= 8 && LOADS * (RING - 1) + 1 < 64 && RING <= 4, "");
 };
 
-template <int TL, int RF, int WAVES, int RING, bool ONCE, bool BF16OUT>
+template <int TL, int RF, int WAVES, int RING, bool ONCE, bool FP8, bool BF16OUT>
 __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
     using L = Few<TL, RF, WAVES, RING>;
     constexpr int NT = L::NT;
@@ -142,7 +143,8 @@ __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
     const int rows_w = min(a.n - n0, 16 * RF), rows_a = min(a.m - m0, 8 * TL);
     const v4i buf_w = buffer(a.w + (int64_t)n0 * a.k, (int64_t)rows_w * a.k), buf_a = buffer(a.a + (int64_t)m0 * a.k, (int64_t)rows_a * a.k);
     const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, (int64_t)rows_a * a.groups * 4);
-    const int per = (a.groups + WAVES - 1) / WAVES, from = wave * per, upto = min(from + per, a.groups);
+    const int first_block = blockIdx.y * a.per, blocks = max(0, min(a.per, a.groups - first_block));    // this workgroup's blocks
+    const int per = (blocks + WAVES - 1) / WAVES, from = first_block + min(wave * per, blocks), upto = first_block + min((wave + 1) * per, blocks);
     // Load i: rows 8 i .. 8 i + 7 of a panel.
     int col[2], off[2];                  // the lane's piece, and its place, for even and odd i
 #pragma unroll
@@ -203,8 +205,8 @@ __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");               // the slot is read
         issue(s + RING, slot, (V + RING) % 4);
         slot = slot + 1 == RING ? 0 : slot + 1;
-        v8bf wide[RF][BF16OUT ? 1 : 4];
-        if constexpr (!BF16OUT) {
+        v8bf wide[RF][FP8 ? 1 : 4];
+        if constexpr (!FP8) {
 #pragma unroll
             for (int i = 0; i < RF; ++i)
 #pragma unroll
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
             v4f p[RF];
 #pragma unroll
             for (int i = 0; i < RF; ++i) p[i] = v4f{0.f, 0.f, 0.f, 0.f};
-            if constexpr (BF16OUT) {
+            if constexpr (FP8) {
 #pragma unroll
                 for (int i = 0; i < RF; ++i)
                     p[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w[i][0], w[i][1]), join(x[t][0], x[t][1]), p[i], 0, 0, 0,
@@ -243,6 +245,7 @@ __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");                     // nothing is on its way into LDS any more
     __syncthreads();
+    char* const y = (char*)a.y + (int64_t)blockIdx.y * a.m * a.n * 4;    // (several workgroups an output: FP32 parts, one after another)
     auto* part = (__attribute__((address_space(3))) v4f*)smem;           // [WAVES][RF NT][64]
 #pragma unroll
     for (int i = 0; i < RF; ++i)
@@ -262,24 +265,24 @@ __global__ __launch_bounds__(WAVES * 64) void b128_few_kernel(B128Args a) {
         const int64_t to = (int64_t)(m0 + t) * a.n + row;
         if (a.n % 4 == 0) {
             if (row >= a.n) continue;
-            if constexpr (BF16OUT) *reinterpret_cast<v2u*>((uint16_t*)a.y + to) = v2u{bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
-            else *reinterpret_cast<v4f*>((float*)a.y + to) = sum;
+            if constexpr (BF16OUT) *reinterpret_cast<v2u*>((uint16_t*)y + to) = v2u{bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+            else *reinterpret_cast<v4f*>((float*)y + to) = sum;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (row + e < a.n) store<BF16OUT>(a.y, to + e, sum[e]);
+                if (row + e < a.n) store<BF16OUT>(y, to + e, sum[e]);
         }
     }
 }
 
-template <int TL, int RF, int WAVES, int RING, bool ONCE, bool BF16OUT>
-hipError_t go_few(const B128Args& a, hipStream_t stream) {
+template <int TL, int RF, int WAVES, int RING, bool ONCE, bool FP8, bool BF16OUT>
+hipError_t go_few(const B128Args& a, int splits, hipStream_t stream) {
     using L = Few<TL, RF, WAVES, RING>;
-    auto kernel = b128_few_kernel<TL, RF, WAVES, RING, ONCE, BF16OUT>;
+    auto kernel = b128_few_kernel<TL, RF, WAVES, RING, ONCE, FP8, BF16OUT>;
     static LdsLimit limit;
     if (hipError_t e = limit.raise((const void*)kernel, L::LDS); e != hipSuccess) return e;
     const int64_t tiles = ((int64_t)(a.n + 16 * RF - 1) / (16 * RF)) * ((a.m + 8 * TL - 1) / (8 * TL));
-    kernel<<<(unsigned)tiles, WAVES * 64, L::LDS, stream>>>(a);
+    kernel<<<dim3((unsigned)tiles, (unsigned)splits), WAVES * 64, L::LDS, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -601,14 +604,19 @@ hipError_t go_tile(const B128Args& a, int splits, hipStream_t stream) {
 struct Plan {
     enum { FEW, SMALL, MID, BIG } form;
     int rows;                            // FEW: blocks of 16 weight rows a workgroup
-    int splits;                          // SMALL: workgroups a tile
+    int splits;                          // FEW, SMALL: workgroups an output
 };
 
 // Up to 64 tokens: FEW, with 16 rows a workgroup while that gives no more
 // workgroups than CUs (or for up to 4 tokens, where the tokens' bytes do not
-// count), else 32.  Microseconds with 16 / 32 rows, K = 5120: 33 tokens, N = 1024
-// 5.9 / 7.2, 2048 6.3 / 7.6, 7168 14.2 / 11.4, 17408 31.8 / 27.7; one token, N =
-// 17408 16.8 / 17.9.
+// count), else 32; or K split over the CUs that this leaves idle, with 16 or 64
+// rows, where the blocks that a wave saves (nanoseconds each, by rows and tokens)
+// are worth the join.  Microseconds unsplit with 16 / 32 rows, FP32, K = 5120: 33
+// tokens, N = 2048 7.5 / 9.0, 7168 13.4 / 11.1, 17408 33.0 / 28.4; one token, N =
+// 17408 17.0 / 18.2.  Split / not: 5120 x 17408, 64 rows three times, 16 tokens
+// 20.4 / 22.1, 33 23.8 / 29.4, 64 28.4 / 39.4; 5120 x 6144, 33 tokens 12.0 / 11.0;
+// 256 x 7168, 16 rows four times, 16 tokens 5.8 / 6.1, 64 7.9 / 10.8; 2048 x 5120,
+// 16 rows twice, 33 tokens 7.8 / 7.5.
 //   More tokens: the form with the least time by what a block of 128 columns
 // takes each (nanoseconds, measured over 65 .. 8192 tokens, N 100 .. 17408, K 512
 // .. 17408), times the rounds in which its workgroups fill the CUs.  Measured
@@ -624,12 +632,21 @@ struct Plan {
 Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t most_splits = 8) {
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t groups = up(k, BLOCK);
-    if (m <= 64) return {Plan::FEW, up(n, 16) <= cus || m <= 4 ? 1 : 2, 1};
     Plan best{Plan::FEW, 1, 1};
     int64_t least = INT64_MAX;
     auto consider = [&](const Plan& p, int64_t ns) {
         if (ns < least) least = ns, best = p;
     };
+    if (m <= 64) {
+        const bool small = up(n, 16) <= cus;
+        const int64_t tl = m <= 48 ? up(m, 8) : 8;                       // (eights of tokens: the kernel's TL)
+        if (small || m <= 4) consider({Plan::FEW, 1, 1}, up(groups, 4) * (150 + 55 * tl));
+        else consider({Plan::FEW, 2, 1}, up(groups, 4) * (400 + 85 * tl));
+        const int rows = small ? 1 : 4;
+        for (int64_t z = 2; z <= most_splits && 4 * z <= groups && up(n, 16 * rows) * z <= cus && (small || m > 4); ++z)
+            consider({Plan::FEW, rows, (int)z}, up(up(groups, z), 4) * (small ? 150 + 55 * tl : 1000 + 110 * tl) + 2200 + 400 * z + z * m * n / 1000);
+        return best;
+    }
     const int64_t few[3] = {150, 245, 380};
     for (int i = 0; i < 3; ++i) {
         const int64_t blocks = up(n, 16 << i) * up(m, 64);
@@ -649,38 +666,46 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t m
     return best;
 }
 
-template <int TL, bool BF16OUT>
-hipError_t go_few(const B128Args& a, int rows, hipStream_t stream) {
+template <int TL, bool FP8, bool BF16OUT>
+hipError_t go_few(const B128Args& a, const Plan& p, hipStream_t stream) {
     // Weights that are read once, and fill a good part of the caches, go past them (one token, 17408 x 5120: 19.9 -> 18.1 us with 32
     // rows; 5120 x 6144, which stays in the last cache from call to call, 7.0 -> 8.0).
     const bool once = a.m <= 8 * TL && (int64_t)a.n * a.k >= (64 << 20);
-    if constexpr (TL == 8) {
-        if (rows == 4) return go_few<TL, 4, 4, 2, false, BF16OUT>(a, stream);
+    constexpr bool PARTS = FP8 && !BF16OUT;                              // never with 32 rows, or so many weights
+    if constexpr (!BF16OUT || TL == 8) {
+        if (p.rows == 4) return go_few<TL, 4, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
     }
-    if (rows == 2) return once ? go_few<TL, 2, 4, 2, true, BF16OUT>(a, stream) : go_few<TL, 2, 4, 2, false, BF16OUT>(a, stream);
-    return once ? go_few<TL, 1, 4, 2, true, BF16OUT>(a, stream) : go_few<TL, 1, 4, 2, false, BF16OUT>(a, stream);
+    if constexpr (!PARTS) {
+        if (p.rows == 2)
+            return once ? go_few<TL, 2, 4, 2, true, FP8, BF16OUT>(a, p.splits, stream) : go_few<TL, 2, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
+        if (once) return go_few<TL, 1, 4, 2, true, FP8, BF16OUT>(a, p.splits, stream);
+    }
+    return go_few<TL, 1, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
+}
+
+template <bool FP8, bool BF16OUT>
+hipError_t go_few(const B128Args& a, const Plan& p, hipStream_t stream) {
+    if (a.m <= 8) return go_few<1, FP8, BF16OUT>(a, p, stream);
+    if (a.m <= 16) return go_few<2, FP8, BF16OUT>(a, p, stream);
+    if (a.m <= 24) return go_few<3, FP8, BF16OUT>(a, p, stream);
+    if (a.m <= 32) return go_few<4, FP8, BF16OUT>(a, p, stream);
+    if (a.m <= 40) return go_few<5, FP8, BF16OUT>(a, p, stream);
+    if (a.m <= 48) return go_few<6, FP8, BF16OUT>(a, p, stream);
+    return go_few<8, FP8, BF16OUT>(a, p, stream);
 }
 
 template <bool BF16OUT>
 hipError_t go(B128Args a, const Plan& p, float* parts, hipStream_t stream) {
-    if (p.form == Plan::FEW) {
-        if (a.m <= 8) return go_few<1, BF16OUT>(a, p.rows, stream);
-        if (a.m <= 16) return go_few<2, BF16OUT>(a, p.rows, stream);
-        if (a.m <= 24) return go_few<3, BF16OUT>(a, p.rows, stream);
-        if (a.m <= 32) return go_few<4, BF16OUT>(a, p.rows, stream);
-        if (a.m <= 40) return go_few<5, BF16OUT>(a, p.rows, stream);
-        if (a.m <= 48) return go_few<6, BF16OUT>(a, p.rows, stream);
-        return go_few<8, BF16OUT>(a, p.rows, stream);
-    }
     if constexpr (BF16OUT) {
         if (p.form == Plan::BIG) return go_tile<4, 2, 4, 8, true, true>(a, 1, stream);
         if (p.form == Plan::MID) return go_tile<4, 2, 4, 4, true, true>(a, 1, stream);
     }
-    if (p.splits == 1) return go_tile<2, 2, 4, 4, BF16OUT, BF16OUT>(a, 1, stream);
+    const bool few = p.form == Plan::FEW;
+    if (p.splits == 1) return few ? go_few<BF16OUT, BF16OUT>(a, p, stream) : go_tile<2, 2, 4, 4, BF16OUT, BF16OUT>(a, 1, stream);
     void* y = a.y;
     a.y = parts;
     a.per = (a.groups + p.splits - 1) / p.splits;
-    if (hipError_t e = go_tile<2, 2, 4, 4, BF16OUT, false>(a, p.splits, stream); e != hipSuccess) return e;
+    if (hipError_t e = few ? go_few<BF16OUT, false>(a, p, stream) : go_tile<2, 2, 4, 4, BF16OUT, false>(a, p.splits, stream); e != hipSuccess) return e;
     const int64_t outputs = (int64_t)a.m * a.n;
     b128_join_kernel<BF16OUT><<<(unsigned)((outputs + 1023) / 1024), 256, 0, stream>>>(parts, p.splits, outputs, y);
     return hipGetLastError();

@@ -257,7 +257,8 @@ def check_product(a, a_s, w, w_s, out, **more):
 MNK = [(1, 1, 16), (1, 16, 128), (1, 17, 144), (2, 128, 256), (3, 129, 400), (15, 300, 1040), (16, 64, 2048), (17, 257, 384), (31, 48, 640),
        (33, 513, 1152), (48, 130, 272), (49, 40, 5136), (64, 256, 512), (65, 100, 256), (100, 300, 784), (128, 384, 128), (129, 257, 272),
        (130, 1, 128), (200, 500, 1040), (256, 256, 640), (257, 255, 2064), (300, 700, 400), (511, 130, 16), (640, 1024, 512), (1, 1000, 17408),
-       (40, 33, 17408), (300, 64, 5120), (129, 128, 17408)]
+       (40, 33, 17408), (300, 64, 5120), (129, 128, 17408),
+       (12, 4500, 17408), (33, 5120, 8208), (64, 4099, 10000), (50, 700, 4112)]
 
 
 @pytest.mark.parametrize("out", [BF, torch.float32])
@@ -275,7 +276,7 @@ def test_product_of_whole_numbers_is_exact(m, n, k):
     assert torch.equal(run_product(*x, BF), ref.to(BF))
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 300, 2048), (33, 200, 5120), (200, 300, 4096), (600, 260, 1024)])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 2048), (33, 200, 5120), (200, 300, 4096), (600, 260, 1024), (33, 5120, 17408), (64, 256, 7168)])
 def test_product_with_and_without_workspace(m, n, k):
     """No workspace, a smaller one and one with anything in it; and the same bits each time."""
     x = product_inputs(m, n, k, 3)
