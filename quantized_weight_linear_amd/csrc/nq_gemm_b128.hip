@@ -314,7 +314,7 @@ struct Output {
 
 // The products run some steps ahead of the rescales, so that no rescale waits for
 // its product.  Operands are read a column of products ahead, also across stages.
-template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT>
+template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT, bool NARROW>
 __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) {
     using T = Tile<WR, WT, FI, FT>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -327,13 +327,19 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
 
     const v4i buf_w = buffer(a.w + (int64_t)n0 * a.k, (int64_t)rows_w * a.k), buf_a = buffer(a.a + (int64_t)m0 * a.k, (int64_t)rows_a * a.k);
     const v4i buf_s = buffer(a.as + (int64_t)m0 * a.groups, (int64_t)rows_a * a.groups * 4);
-    // A window never reaches past its row: the last one starts earlier.
+    // A window never reaches past its row: the last one starts earlier.  NARROW: rows
+    // of fewer than four scales come at once, 4 bytes a token and block.
     auto window = [&](int s) { return min(s - ((s - from) & 3), a.groups - 4); };
     auto issue_window = [&](int s) {     // that of blocks s .. s + 3
-        if (wave < T::TOKENS / 64 && s < upto)
-            lds_load16(buf_s, ((64 * wave + lane) * a.groups + window(s)) * 4, lds + T::WINDOWS + ((s - from) / 4 & 1) * T::WINDOW + wave * 1024);
+        if (wave >= T::TOKENS / 64 || s >= upto) return;
+        const int row = (64 * wave + lane) * a.groups;
+        if constexpr (NARROW)
+            for (int g = 0; g < a.groups; ++g) lds_load4(buf_s, (row + g) * 4, lds + T::WINDOWS + g * T::TOKENS * 4 + wave * 256);
+        else lds_load16(buf_s, (row + window(s)) * 4, lds + T::WINDOWS + ((s - from) / 4 & 1) * T::WINDOW + wave * 1024);
     };
-    auto scales_of = [&](int s) { return T::WINDOWS + ((s - from) / 4 & 1) * T::WINDOW + (s - window(s)) * 4; };
+    auto scales_of = [&](int s) {
+        return T::WINDOWS + (NARROW ? s * T::TOKENS * 4 : ((s - from) / 4 & 1) * T::WINDOW + (s - window(s)) * 4);
+    };
 
     // Load i of this wave: rows 8 q .. 8 q + 7 of a panel, q = i WAVES + wave.  No
     // branches: past the last block, and of what lies past the last column, nothing
@@ -353,7 +359,7 @@ __global__ __launch_bounds__(WR * WT * 64, 2) void b128_tile_kernel(B128Args a) 
         x[0] = *(__attribute__((address_space(3))) const v4u*)(row + first);
         x[1] = *(__attribute__((address_space(3))) const v4u*)(row + (first ^ 64));
     };
-    auto read_scale = [&](int at, int j) { return *(__attribute__((address_space(3))) const float*)(lds + at + (wt + 16 * j + n) * 16); };
+    auto read_scale = [&](int at, int j) { return *(__attribute__((address_space(3))) const float*)(lds + at + (wt + 16 * j + n) * (NARROW ? 4 : 16)); };
     auto arrived = [&] {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
@@ -588,12 +594,12 @@ __global__ __launch_bounds__(256) void b128_join_kernel(const float* parts, int 
     }
 }
 
-template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT>
+template <int WR, int WT, int FI, int FT, bool FP8, bool BF16OUT, bool NARROW = false>
 hipError_t go_tile(const B128Args& a, int splits, hipStream_t stream) {
     using T = Tile<WR, WT, FI, FT>;
     constexpr int OUT = T::WAVES * Output<FI, FT, BF16OUT>::BYTES, LDS = OUT > T::LDS ? OUT : T::LDS;
     static_assert(LDS <= 160 * 1024, "");
-    auto kernel = b128_tile_kernel<WR, WT, FI, FT, FP8, BF16OUT>;
+    auto kernel = b128_tile_kernel<WR, WT, FI, FT, FP8, BF16OUT, NARROW>;
     static LdsLimit limit;
     if (hipError_t e = limit.raise((const void*)kernel, LDS); e != hipSuccess) return e;
     const int64_t tiles = ((int64_t)(a.m + T::TOKENS - 1) / T::TOKENS) * ((a.n + T::ROWS - 1) / T::ROWS);
@@ -618,9 +624,10 @@ struct Plan {
 // 256 x 7168, 16 rows four times, 16 tokens 5.8 / 6.1, 64 7.9 / 10.8; 2048 x 5120,
 // 16 rows twice, 33 tokens 7.8 / 7.5.
 //   More tokens: the form with the least time by what a block of 128 columns
-// takes each (nanoseconds, measured over 65 .. 8192 tokens, N 100 .. 17408, K 512
-// .. 17408), times the rounds in which its workgroups fill the CUs.  Measured
-// against each other (us):
+// takes each and what a workgroup takes beside them (nanoseconds, fitted to 120
+// sizes of 65 .. 16384 tokens, N 100 .. 17408, K 128 .. 17408, none of which loses
+// more than 6 % to its best form), times the rounds in which its workgroups fill
+// the CUs.  Measured against each other (us):
 //                             FEW 16   32    64   SMALL (splits)    MID    BIG
 //   256 x 1024 x 2048          5.1   5.8   7.8   13.6              17.0   26.9
 //   96 x 7168 x 5120          29.1  19.8  16.1   31.2, 17.6 (4)    41.4   57.9
@@ -628,6 +635,7 @@ struct Plan {
 //   4800 x 600 x 2896         61.4  40.4  31.6   20.6              26.2   37.8
 //   1024 x 7168 x 5120         205   127    94   48.7              45.9   62.6
 //   2048 x 7168 x 5120         414   251   185   93.1              91.3   70.9
+//   1792 x 5120 x 128, FP32   77.3  51.4  38.3   14.1
 //   512 x 5120 x 5120, FP32   76.3  49.1  42.8   45.7, 39.8 (3)
 Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t most_splits = 8) {
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
@@ -647,21 +655,21 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t m
             consider({Plan::FEW, rows, (int)z}, up(up(groups, z), 4) * (small ? 150 + 55 * tl : 1000 + 110 * tl) + 2200 + 400 * z + z * m * n / 1000);
         return best;
     }
-    const int64_t few[3] = {150, 245, 380};
+    const int64_t few[3] = {170, 230, 360}, start[3] = {550, 750, 1550};
     for (int i = 0; i < 3; ++i) {
         const int64_t blocks = up(n, 16 << i) * up(m, 64);
-        if (i == 2 || blocks < MOST_BLOCKS) consider({Plan::FEW, 1 << i, 1}, groups * few[i] * up(blocks, cus));
+        if (i == 2 || blocks < MOST_BLOCKS) consider({Plan::FEW, 1 << i, 1}, (groups * few[i] + start[i]) * up(blocks, cus));
     }
-    if (groups < 4) return best;         // (the tiles' windows of scales need four)
     const int64_t tiles = up(n, 128) * up(m, 128);
     for (int64_t z = 1; z <= most_splits && (z == 1 || 4 * z <= groups); ++z) {
-        const int64_t one = bf16_out ? 900 : 1150, two = bf16_out ? 1450 : 2100;           // workgroups on a CU
+        const int64_t one = bf16_out ? 900 : 1100, two = bf16_out ? 1450 : 1900;           // workgroups on a CU
         const int64_t join = z == 1 ? 0 : 2500 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
-        consider({Plan::SMALL, 0, (int)z}, up(groups, z) * (tiles * z <= cus ? one : two * up(tiles * z, 2 * cus)) + join);
+        const int64_t per = up(groups, z);
+        consider({Plan::SMALL, 0, (int)z}, (tiles * z <= cus ? per * one + 1500 : (per * two + 2250) * up(tiles * z, 2 * cus)) + join);
     }
-    if (bf16_out) {
-        consider({Plan::MID, 0, 1}, groups * 1300 * up(up(n, 256) * up(m, 128), cus));
-        consider({Plan::BIG, 0, 1}, groups * 2000 * up(up(n, 256) * up(m, 256), cus));
+    if (bf16_out && groups >= 4) {       // (fewer scales a row: SMALL alone has that form)
+        consider({Plan::MID, 0, 1}, (groups * 1400 + 1700) * up(up(n, 256) * up(m, 128), cus));
+        consider({Plan::BIG, 0, 1}, (groups * 2300 + 3400) * up(up(n, 256) * up(m, 256), cus));
     }
     return best;
 }
@@ -701,6 +709,7 @@ hipError_t go(B128Args a, const Plan& p, float* parts, hipStream_t stream) {
         if (p.form == Plan::MID) return go_tile<4, 2, 4, 4, true, true>(a, 1, stream);
     }
     const bool few = p.form == Plan::FEW;
+    if (!few && a.groups < 4) return go_tile<2, 2, 4, 4, BF16OUT, BF16OUT, true>(a, 1, stream);
     if (p.splits == 1) return few ? go_few<BF16OUT, BF16OUT>(a, p, stream) : go_tile<2, 2, 4, 4, BF16OUT, BF16OUT>(a, 1, stream);
     void* y = a.y;
     a.y = parts;

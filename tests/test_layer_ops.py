@@ -311,6 +311,10 @@ def test_product_of_nothing():
     y = torch.full((3, 5), 9.0, device=DEV)
     nq.nq_gemm_fp8_b128(z, torch.empty((3, 0), device=DEV), z, torch.empty((1, 0), device=DEV), 3, 5, 0, y)
     assert bool((y == 0).all())
+    for out in (BF, torch.float32):
+        y = torch.full((2000, 3000), 9.0, device=DEV, dtype=out)
+        nq.nq_gemm_fp8_b128(z, torch.empty((2000, 0), device=DEV), z, torch.empty((24, 0), device=DEV), 2000, 3000, 0, y)
+        assert bool((y == 0).all())
 
 
 def test_product_scales_and_outputs_inside_larger_tensors():
@@ -324,7 +328,8 @@ def test_product_scales_and_outputs_inside_larger_tensors():
 
 
 @pytest.mark.parametrize("out", [BF, torch.float32])
-@pytest.mark.parametrize("m,n,k", [(1000, 8200, 528), (990, 8203, 1168), (1000, 7100, 656), (777, 7001, 912), (2100, 4500, 1040), (1025, 1025, 4112)])
+@pytest.mark.parametrize("m,n,k", [(1000, 8200, 528), (990, 8203, 1168), (1000, 7100, 656), (777, 7001, 912), (2100, 4500, 1040), (1025, 1025, 4112),
+                                   (1000, 8200, 272), (1729, 12406, 384), (1000, 7100, 112), (1025, 8203, 16), (600, 5000, 144)])
 def test_product_of_large_tiles(m, n, k, out):
     """Tiles of 256 rows whose last ones are partly outside, blocks in odd and even numbers."""
     check_product(*product_inputs(m, n, k, m + n + k), out)
