@@ -364,10 +364,12 @@ nq_status nq_gemm_fp8row(const uint16_t* x, const uint8_t* w, const uint16_t* w_
  *           P the sum over block g's columns of a[m][k] * w[n][k]; the product of
  *           the two scales is formed in FP32, and the blocks are summed in FP32
  *   workspace, workspace_bytes   optional device scratch
- *           (nq_gemm_fp8_b128_workspace_bytes): lets K be split over workgroups
- *           where M and N give too few.  It needs no preparation and holds nothing
- *           between calls; calls that share it must be ordered (the same stream).
- *           A smaller one than asked for is not used.
+ *           (nq_gemm_fp8_b128_workspace_bytes, enough for every M up to the one
+ *           given and both output types): lets K be split over workgroups where M
+ *           and N give too few.  It needs no preparation and holds nothing between
+ *           calls; calls that share it must be ordered (the same stream).  Of a
+ *           smaller one a call uses what there is: K is split into no more than
+ *           workspace_bytes / (4 M N) parts.
  * FP32 outputs: both operands are decoded exactly to BF16 and P is summed in FP32
  * on the BF16 matrix units, within this library's 1e-5.  BF16 outputs: P comes
  * from the FP8 matrix units, which add products in groups of eight and cut each

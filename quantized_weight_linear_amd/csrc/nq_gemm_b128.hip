@@ -16,6 +16,7 @@
 // and go through the BF16 instructions at half the rate.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "nq_attn_launch.h"
@@ -637,7 +638,8 @@ struct Plan {
 //   2048 x 7168 x 5120         414   251   185   93.1              91.3   70.9
 //   1792 x 5120 x 128, FP32   77.3  51.4  38.3   14.1
 //   512 x 5120 x 5120, FP32   76.3  49.1  42.8   45.7, 39.8 (3)
-Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t most_splits = 8) {
+constexpr int64_t MOST_SPLITS = 8, JOIN = 2500, JOIN_RATE = 625, TWO_F32 = 1900;
+Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t most_splits = MOST_SPLITS) {
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t groups = up(k, BLOCK);
     Plan best{Plan::FEW, 1, 1};
@@ -652,7 +654,7 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t m
         else consider({Plan::FEW, 2, 1}, up(groups, 4) * (400 + 85 * tl));
         const int rows = small ? 1 : 4;
         for (int64_t z = 2; z <= most_splits && 4 * z <= groups && up(n, 16 * rows) * z <= cus && (small || m > 4); ++z)
-            consider({Plan::FEW, rows, (int)z}, up(up(groups, z), 4) * (small ? 150 + 55 * tl : 1000 + 110 * tl) + 2200 + 400 * z + z * m * n / 1000);
+            consider({Plan::FEW, rows, (int)z}, up(up(groups, z), 4) * (small ? 150 + 55 * tl : 1000 + 110 * tl) + 2200 + 400 * z + z * (m * n / 1000));
         return best;
     }
     const int64_t few[3] = {170, 230, 360}, start[3] = {550, 750, 1550};
@@ -662,8 +664,8 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t m
     }
     const int64_t tiles = up(n, 128) * up(m, 128);
     for (int64_t z = 1; z <= most_splits && (z == 1 || 4 * z <= groups); ++z) {
-        const int64_t one = bf16_out ? 900 : 1100, two = bf16_out ? 1450 : 1900;           // workgroups on a CU
-        const int64_t join = z == 1 ? 0 : 2500 + z * m * n / 625;                           // its launch, and the parts at 5 TB/s
+        const int64_t one = bf16_out ? 900 : 1100, two = bf16_out ? 1450 : TWO_F32;         // workgroups on a CU
+        const int64_t join = z == 1 ? 0 : JOIN + z * (m * n / JOIN_RATE);                    // its launch, and the parts at 5 TB/s
         const int64_t per = up(groups, z);
         consider({Plan::SMALL, 0, (int)z}, (tiles * z <= cus ? per * one + 1500 : (per * two + 2250) * up(tiles * z, 2 * cus)) + join);
     }
@@ -722,10 +724,24 @@ hipError_t go(B128Args a, const Plan& p, float* parts, hipStream_t stream) {
 
 }  // namespace
 
+// The most bytes of parts that any size up to m takes.  From one of the sizes
+// below to the next all costs but the join's stay as they are, and that grows with
+// m and the splits: the first of them has the most splits.  Above 64 tokens a split
+// saves less than a round of two workgroups a CU, so no size splits once two
+// parts cost as much, and no parts cost more; that stands for what is not searched
+// of few rows with more than half a million tokens.
 int64_t gemm_fp8_b128_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    const int64_t cus = device_cu_count();
-    const int splits = max(plan(m, n, k, true, cus).splits, plan(m, n, k, false, cus).splits);
-    return splits > 1 ? splits * m * n * 4 : 0;
+    const int64_t cus = device_cu_count(), groups = (k + BLOCK - 1) / BLOCK, round = TWO_F32 * groups;
+    if (groups < 8) return 0;
+    int64_t most = 0, from = 1;
+    for (int i = 0; from <= m && (from <= 64 || 2 * (from * n / JOIN_RATE) < round); ++i) {
+        if (i == 8192) return std::max(most, 4 * std::min(MOST_SPLITS * m * n, JOIN_RATE * (round + MOST_SPLITS)));
+        const int64_t upto = from < 5 ? 4 : from < 49 ? (from + 7) / 8 * 8 : (from + 63) / 64 * 64;
+        const int splits = std::max(plan(from, n, k, true, cus).splits, plan(from, n, k, false, cus).splits);
+        if (splits > 1) most = std::max(most, splits * std::min(upto, m) * n * 4);
+        from = upto + 1;
+    }
+    return most;
 }
 
 hipError_t launch_gemm_fp8_b128(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int64_t m,
@@ -733,8 +749,8 @@ hipError_t launch_gemm_fp8_b128(const uint8_t* a, const float* a_scale, const ui
                                 hipStream_t stream) {
     const int groups = (int)((k + BLOCK - 1) / BLOCK);
     const B128Args args{a, a_scale, w, w_scale, (int)m, (int)n, (int)k, groups, groups, y};
-    Plan p = plan(m, n, k, bf16_out, device_cu_count());
-    if (p.splits > 1 && workspace_bytes < p.splits * m * n * 4) p = plan(m, n, k, bf16_out, device_cu_count(), 1);
+    const int64_t fit = workspace_bytes / (m * n * 4);                   // parts
+    const Plan p = plan(m, n, k, bf16_out, device_cu_count(), std::clamp(fit, (int64_t)1, MOST_SPLITS));
     return bf16_out ? go<true>(args, p, (float*)workspace, stream) : go<false>(args, p, (float*)workspace, stream);
 }
 

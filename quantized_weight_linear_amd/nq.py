@@ -285,7 +285,7 @@ def nq_gemm_fp8_b128_workspace_bytes(M, N, K):
 
 
 def alloc_gemm_fp8_b128_workspace(M, N, K, device):
-    """A workspace for nq_gemm_fp8_b128 at these sizes, or None where it needs none."""
+    """A workspace for nq_gemm_fp8_b128 of up to M tokens, or None where none of them needs any."""
     n = nq_gemm_fp8_b128_workspace_bytes(M, N, K)
     return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
 

@@ -69,6 +69,17 @@ def test_product_refusals(L):
         assert L.nq_gemm_fp8_b128_workspace_bytes(m, n, k) == 0
 
 
+@pytest.mark.parametrize("n,k", [(5120, 5120), (5120, 17408), (17408, 5120), (256, 7168), (1024, 5136), (1, 20000), (100, 1040), (300, 900)])
+def test_product_workspace_serves_smaller_products(L, n, k):
+    """What is asked for at M is enough for every smaller M."""
+    f, most = L.nq_gemm_fp8_b128_workspace_bytes, 0
+    for m in [*range(1, 1200), *range(1200, 9000, 61), 20000, 70001, 1 << 20]:
+        need = f(m, n, k)
+        assert need >= most, (m, n, k)
+        most = need
+    assert most == 0 or k > 7 * 128             # fewer than eight blocks of K are never split
+
+
 ROPE = dict(fmt=3, q=A, qs=1536, k=A, ks=256, v=A, vs=256, qw=A, kw=A, bias=0.0, eps=1e-6, pos=A, freq=A, rot=64, rope=0, ksc=A, vsc=A,
             table=A, width=8, lens=A, cu=A, B=2, T=5, Hq=6, Hkv=1, D=256, page=64, pages=9, qo=A, qos=1536, ko=None, kos=0, kp=A, vp=A,
             stream=None)

@@ -292,6 +292,31 @@ def test_product_with_and_without_workspace(m, n, k):
             check_product(*x, out, workspace=small)
 
 
+@pytest.mark.parametrize("m,most,n,k", [(512, 4096, 5120, 5120), (65, 2000, 5120, 17408), (33, 1792, 5120, 17408), (110, 20000, 5120, 8192)])
+def test_product_on_the_workspace_of_a_larger_one(m, most, n, k):
+    """A workspace for the most tokens of a step serves a step of fewer: the same bits as on one made for it, behind which nothing is written."""
+    x = product_inputs(m, n, k, 12)
+    own, large = (nq.nq_gemm_fp8_b128_workspace_bytes(i, n, k) for i in (m, most))
+    assert large >= own > 0
+    for out in (BF, torch.float32):
+        first = check_product(*x, out, workspace=torch.empty(own, dtype=torch.uint8, device=DEV))
+        ws = torch.full((large + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        same_bits(first, run_product(*x, out, workspace=ws[:large]))
+        assert bool((ws[large:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 5120, 8192), (64, 256, 7168), (256, 5120, 17408)])
+def test_product_uses_what_there_is_of_a_workspace(m, n, k):
+    """Two parts fit, and half of a third: two are written, nothing behind them."""
+    x, part = product_inputs(m, n, k, 13), m * n * 4
+    assert nq.nq_gemm_fp8_b128_workspace_bytes(m, n, k) >= 2 * part
+    for out in (BF, torch.float32):
+        ws = torch.full((2 * part + part // 2 // 16 * 16,), 0xFF, dtype=torch.uint8, device=DEV)
+        check_product(*x, out, workspace=ws)
+        parts = ws[:2 * part].view(torch.float32)           # (0xFF..: NaN)
+        assert not bool(parts.isnan().any()) and bool((ws[2 * part:] == 0xFF).all())
+
+
 @pytest.mark.parametrize("m", [1, 20, 64, 100, 200, 300])
 @pytest.mark.parametrize("out", [BF, torch.float32])
 def test_product_not_finite_stays_in_its_row_and_column(m, out):
