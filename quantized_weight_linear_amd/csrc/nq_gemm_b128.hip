@@ -678,21 +678,19 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t m
 
 template <int TL, bool FP8, bool BF16OUT>
 hipError_t go_few(const B128Args& a, const Plan& p, hipStream_t stream) {
-    // Weights that are read once, and fill a good part of the caches, go past them (us through them / past them: one token, 17408 x
-    // 5120, 16 rows 18.6 / 17.1; 33 tokens, 5120 x 17408, 64 rows three times 23.3 / 22.6, 16 tokens 20.4 / 19.0; 33 tokens, 2048 x
-    // 65536, 16 rows twice, FP8 units 41.9 / 39.4; 5120 x 6144, which stays in the last cache from call to call, 7.7 / 8.2).
+    // Weights that are read once, and fill a good part of the caches, go past them (one token, 17408 x 5120: 19.9 -> 18.1 us with 32
+    // rows; 5120 x 6144, which stays in the last cache from call to call, 7.0 -> 8.0).
     const bool once = a.m <= 8 * TL && (int64_t)a.n * a.k >= (64 << 20);
-    if constexpr (!BF16OUT) {            // (64 rows: up to 64 tokens always in parts)
-        if (p.rows == 4 && once) return go_few<TL, 4, 4, 2, true, FP8, BF16OUT>(a, p.splits, stream);
-    }
+    constexpr bool PARTS = FP8 && !BF16OUT;                              // never with 32 rows, or so many weights
     if constexpr (!BF16OUT || TL == 8) {
         if (p.rows == 4) return go_few<TL, 4, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
     }
-    if constexpr (BF16OUT || !FP8) {     // (parts from the FP8 units: 16 or 64 rows)
+    if constexpr (!PARTS) {
         if (p.rows == 2)
             return once ? go_few<TL, 2, 4, 2, true, FP8, BF16OUT>(a, p.splits, stream) : go_few<TL, 2, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
+        if (once) return go_few<TL, 1, 4, 2, true, FP8, BF16OUT>(a, p.splits, stream);
     }
-    return once ? go_few<TL, 1, 4, 2, true, FP8, BF16OUT>(a, p.splits, stream) : go_few<TL, 1, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
+    return go_few<TL, 1, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
 }
 
 template <bool FP8, bool BF16OUT>
