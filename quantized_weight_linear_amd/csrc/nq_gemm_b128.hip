@@ -678,10 +678,12 @@ Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t m
 
 template <int TL, bool FP8, bool BF16OUT>
 hipError_t go_few(const B128Args& a, const Plan& p, hipStream_t stream) {
-    // Weights that are read once, and fill a good part of the caches, go past them (one token, 17408 x 5120: 19.9 -> 18.1 us with 32
-    // rows; 5120 x 6144, which stays in the last cache from call to call, 7.0 -> 8.0).
+    // Weights that are read once, and fill a good part of the caches, go past them (us through them / past them: one token, 17408 x
+    // 5120 18.6 / 17.1; 5120 x 6144, which stays in the last cache from call to call, 7.7 / 8.2).  Not so in the split forms of 64 rows
+    // and of the FP8 units: 33 tokens, 5120 x 17408, 64 rows three times 21.2 / 22.3 where three such weights take turns (267 MB, about
+    // the last cache's size), 23.3 / 22.6 where seven do.
     const bool once = a.m <= 8 * TL && (int64_t)a.n * a.k >= (64 << 20);
-    constexpr bool PARTS = FP8 && !BF16OUT;                              // never with 32 rows, or so many weights
+    constexpr bool PARTS = FP8 && !BF16OUT;                              // of K split: 16 or 64 rows, through the caches
     if constexpr (!BF16OUT || TL == 8) {
         if (p.rows == 4) return go_few<TL, 4, 4, 2, false, FP8, BF16OUT>(a, p.splits, stream);
     }

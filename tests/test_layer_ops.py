@@ -317,6 +317,14 @@ def test_product_uses_what_there_is_of_a_workspace(m, n, k):
         assert not bool(parts.isnan().any()) and bool((ws[2 * part:] == 0xFF).all())
 
 
+@pytest.mark.parametrize("out", [BF, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(1, 2048, 32784), (4, 1030, 70000), (33, 2048, 40000), (64, 4100, 16400), (20, 5121, 13312)])
+def test_product_in_parts_of_many_weights(m, n, k, out):
+    """Weights of more than 64 MiB whose columns are shared out."""
+    assert n * k >= 64 << 20 and nq.nq_gemm_fp8_b128_workspace_bytes(m, n, k) > 0
+    check_product(*product_inputs(m, n, k, m + 14), out)
+
+
 @pytest.mark.parametrize("m", [1, 20, 64, 100, 200, 300])
 @pytest.mark.parametrize("out", [BF, torch.float32])
 def test_product_not_finite_stays_in_its_row_and_column(m, out):
