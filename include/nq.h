@@ -184,7 +184,7 @@ nq_status nq_quantize_act_fp8_row(const uint16_t* x, int64_t M, int64_t K, uint8
  * and keeps its signed zeros; a block holding a NaN gets s = NaN and NaN codes,
  * one holding an infinity (but no NaN) s = infinity, and reads as NaN.
  *   x [T][K] BF16 bits;  codes [T][K];  scale [T][ceil(K/128)] FP32 (4-byte aligned)
- * Errors: K % 16 != 0, more than 2^28 blocks -> NQ_ERR_SHAPE.
+ * Errors: K % 16 != 0, T or K of 2^31 or more, 2^28 or more blocks -> NQ_ERR_SHAPE.
  */
 nq_status nq_quantize_act_fp8_b128(const uint16_t* x, int64_t T, int64_t K, uint8_t* codes, float* scale,
                                    void* stream);
@@ -379,7 +379,7 @@ nq_status nq_gemm_fp8row(const uint16_t* x, const uint8_t* w, const uint16_t* w_
  * absolute sum at most (codes below the smallest normal one counting as that).
  * The result does not depend on timing.  a_scale, wsi: 4-byte aligned.
  * Errors: K % 16 != 0, K of 2^20 or more, gr / gc mismatch, 2^24 or more tiles of
- * 64 x 64 (up to 64 tokens: N of 2^28 or more) -> NQ_ERR_SHAPE.
+ * 64 x 64 (up to 64 tokens: N above 2^28 - 16) -> NQ_ERR_SHAPE.
  */
 int64_t nq_gemm_fp8_b128_workspace_bytes(int64_t M, int64_t N, int64_t K);
 nq_status nq_gemm_fp8_b128(const uint8_t* a_codes, const float* a_scale, const uint8_t* w, const float* wsi,

@@ -80,6 +80,17 @@ def test_product_workspace_serves_smaller_products(L, n, k):
     assert most == 0 or k > 7 * 128             # fewer than eight blocks of K are never split
 
 
+@no_gpu
+def test_limits_of_quantizer_and_product(L):
+    """The largest sizes that the header allows reach the launch, the next ones are refused."""
+    for t, k, status in (((1 << 28) - 1, 16, HIP), (1 << 28, 16, S), (1, (1 << 31) - 16, HIP), (1 << 24, 2048, S), ((1 << 24) - 1, 2048, HIP)):
+        assert L.nq_quantize_act_fp8_b128(*dict(QUANT, T=t, K=k).values()) == status, (t, k)
+    top = (1 << 31) - 1024
+    for m, n, status in ((top, 1, S), (1 << 30, 1, S), ((1 << 30) - 64, 1, HIP), (1, (1 << 28) - 16, HIP), (1, (1 << 28) - 15, S), (65, (1 << 29) - 64, HIP),
+                         (65, 1 << 29, S), (64, (1 << 28) - 16, HIP), (2, top + 1, S)):
+        assert L.nq_gemm_fp8_b128(*dict(PRODUCT, M=m, N=n, gr=-(-n // 128)).values()) == status, (m, n)
+
+
 ROPE = dict(fmt=3, q=A, qs=1536, k=A, ks=256, v=A, vs=256, qw=A, kw=A, bias=0.0, eps=1e-6, pos=A, freq=A, rot=64, rope=0, ksc=A, vsc=A,
             table=A, width=8, lens=A, cu=A, B=2, T=5, Hq=6, Hkv=1, D=256, page=64, pages=9, qo=A, qos=1536, ko=None, kos=0, kp=A, vp=A,
             stream=None)
