@@ -94,6 +94,11 @@ __device__ __forceinline__ uint32_t f32_to_e4m3_sat(float f) {
 // boundary, while the FP64 product lies within 2^-52 of it, so both round to
 // the same FP32 value.  The IEEE special cases carry over: x * inf = x / 0,
 // 0 * inf = NaN = 0 / 0, x * 0 = x / inf, NaN stays NaN.
+//   Two FP32 values (48 bits) as well, where the quotient is a normal number: a
+// boundary m has 25 bits and is no quotient of theirs, so x and m s, integers of
+// the same unit and up to 49 bits, differ by one of it at least, 2^-49 of them.
+// A quotient below 2^-126 may lie on a boundary and come out one step (2^-149)
+// off, which the 8-bit codes made of it do not see.
 __device__ __forceinline__ float div_via_recip64(float x, double r) { return (float)((double)x * r); }
 
 // Four FP32 values -> four E4M3 codes (bytes 0..3), round to nearest even, by

@@ -619,25 +619,27 @@ struct Plan {
 // count), else 32; or K split over the CUs that this leaves idle, with 16 or 64
 // rows, where the blocks that a wave saves (nanoseconds each, by rows and tokens)
 // are worth the join.  Microseconds unsplit with 16 / 32 rows, FP32, K = 5120: 33
-// tokens, N = 2048 7.5 / 9.0, 7168 13.4 / 11.1, 17408 33.0 / 28.4; one token, N =
+// tokens, N = 2048 7.5 / 8.8, 7168 13.4 / 10.8, 17408 32.7 / 28.3; one token, N =
 // 17408 17.0 / 18.2.  Split / not: 5120 x 17408, 64 rows three times, 16 tokens
-// 20.4 / 22.1, 33 23.8 / 29.4, 64 28.4 / 39.4; 5120 x 6144, 33 tokens 12.0 / 11.0;
-// 256 x 7168, 16 rows four times, 16 tokens 5.8 / 6.1, 64 7.9 / 10.8; 2048 x 5120,
-// 16 rows twice, 33 tokens 7.8 / 7.5.
+// 20.4 / 22.4, 33 23.4 / 29.6, 64 27.8 / 39.7; 5120 x 6144, 33 tokens 11.9 / 10.4;
+// 256 x 7168, 16 rows four times, 16 tokens 5.7 / 6.0, 64 7.9 / 10.9; 2048 x 5120,
+// 16 rows twice, 33 tokens 7.7 / 7.5.
 //   More tokens: the form with the least time by what a block of 128 columns
-// takes each and what a workgroup takes beside them (nanoseconds, fitted to 120
-// sizes of 65 .. 16384 tokens, N 100 .. 17408, K 128 .. 17408, none of which loses
-// more than 6 % to its best form), times the rounds in which its workgroups fill
-// the CUs.  Measured against each other (us):
+// takes each and what a workgroup takes beside them (nanoseconds, fitted), times
+// the rounds in which its workgroups fill the CUs.  Over 125 sizes of 65 .. 16384
+// tokens, N 100 .. 17408, K 128 .. 17408, both outputs, it takes a form within 2 % of
+// the best one in 230 of 250 cases, and one more than 10 % behind in 10 (200 x 5120 x
+// 512 BF16 9.7 for 7.0, 512 x 17408 x 5120 FP32 143 for 111, 1792 x 5120 x 5120 FP32
+// 129 for 108).  Measured against each other (us):
 //                             FEW 16   32    64   SMALL (splits)    MID    BIG
-//   256 x 1024 x 2048          5.1   5.8   7.8   13.6              17.0   26.9
-//   96 x 7168 x 5120          29.1  19.8  16.1   31.2, 17.6 (4)    41.4   57.9
-//   512 x 5120 x 17408         233   140   111    104, 68 (3)       133    186
-//   4800 x 600 x 2896         61.4  40.4  31.6   20.6              26.2   37.8
-//   1024 x 7168 x 5120         205   127    94   48.7              45.9   62.6
-//   2048 x 7168 x 5120         414   251   185   93.1              91.3   70.9
-//   1792 x 5120 x 128, FP32   77.3  51.4  38.3   14.1
-//   512 x 5120 x 5120, FP32   76.3  49.1  42.8   45.7, 39.8 (3)
+//   300 x 1024 x 2048          8.1   5.8   7.9   13.5, 11.5 (4)    16.9   27.1
+//   96 x 7168 x 5120          28.3  19.3  15.8   30.2, 17.2 (4)    42.5   58.1
+//   512 x 5120 x 17408         230   138   110    103, 67 (3)       132    187
+//   4800 x 600 x 2896         61.4  40.6  31.6   20.1              25.8   37.9
+//   1024 x 7168 x 5120         208   128    95   48.3              45.6   62.8
+//   2048 x 7168 x 5120         414   252   185   92.2              91.8   69.3
+//   1792 x 5120 x 128, FP32   77.5  51.7  38.3   13.9
+//   512 x 5120 x 5120, FP32   75.4  48.5  42.3   45.1, 39.4 (3)
 constexpr int64_t MOST_SPLITS = 8, JOIN = 2500, JOIN_RATE = 625, TWO_F32 = 1900;
 Plan plan(int64_t m, int64_t n, int64_t k, bool bf16_out, int64_t cus, int64_t most_splits = MOST_SPLITS) {
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };

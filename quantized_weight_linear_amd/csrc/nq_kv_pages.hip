@@ -304,7 +304,8 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(char* pool, int64_t plane_
 // read before any is written, since a row may be both.  Later batches never
 // read what an earlier one wrote: accepted tokens ascend, so the place that
 // row i moves to lies below every row read after it.  100 sequences of up to 64
-// drafts, 32 planes of 4 heads of 256 in BF16: 19 us; one 5 us.
+// drafts, 32 planes of 4 heads of 256 in BF16: 19 us; one 5 us.  Rows of 4 bytes, the
+// scales of an E4M3 cache: 4.9 us; one 3.6.
 constexpr int MOVE_ROWS = 64, MOVE_PLANES = 4, MOVE_BATCH = 4;
 template <class Piece>               // 16 bytes, or the 4 of a scale's row
 __global__ __launch_bounds__(256) void kv_compact_kernel(char* pool, int64_t plane_bytes, int planes, int hkv, int shift,

@@ -5,8 +5,10 @@
 //
 // A row stays in registers between its two passes (the sum of squares, then
 // the output), so every byte is read and written once.  Bound by HBM where
-// rows are many (16383 x 5120 in BF16: 69.7 us, 4.8 TB/s; 1792 with the residual
-// and E4M3 out: 15.6 us, 4.1 TB/s), by latency where they are few (one row: 3.8 us).
+// rows are many (16383 x 5120 in BF16: 66.2 us, 5.1 TB/s; 1792 with the residual
+// and E4M3 out: 15.9 us, 4.1 TB/s), by latency where they are few (one row: 3.9 us),
+// and by the FP64 arithmetic beside the loads where 8-bit outputs come without a
+// residual (16383 x 5120 to E4M3 83 us, to int8 86, for 50 of bytes).
 //   h is rounded to BF16 before it is normalised: it is what the next layer
 // adds to, so the norm is that of the stored residual, fused or not.  Squares
 // are summed in FP64, which costs nothing beside the loads and neither
@@ -162,7 +164,8 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a) {
 }
 
 // Eight columns a thread, sixteen lanes a scale.  s = fp32(amax / 448), codes
-// e4m3_rne_sat(fp32(x / s)): exact, see div_via_recip64.
+// e4m3_rne_sat(fp32(x / s)): exact, see div_via_recip64.  Bound by HBM (1792 x 17408
+// 23.1 us, 4.1 TB/s; 16384 x 5120 57, 4.4), by latency for few rows (33 x 17408 2.6 us).
 __global__ __launch_bounds__(256) void quantize_fp8_b128_kernel(const uint16_t* x, int64_t t, int k, int groups, uint8_t* codes,
                                                                 float* scale) {
     const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16, row = g / groups;
@@ -188,22 +191,31 @@ hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
 
 // Few rows: as few pieces a thread as there are, since a row waits for its sum
 // and its pieces come one after another.  Many: workgroups half as large, of
-// which a CU holds more rows.  Microseconds, E4M3 output (the residual but for *):
-//                     1 row    1792   16384   65536 *
-//   512:   64 x 1      2.3      3.5    13.0    31
-//          64 x 2      2.8      4.3    17.3    42
-//   1024: 128 x 1      2.5      5.0    23.7    63
-//          64 x 2      3.1      5.2    23.6    52
-//   2048: 256 x 1      2.6      8.1    43.7    64 (32768)
-//         128 x 2      3.3      8.8    40.4    59
-//   4096: 512 x 1      2.9     12.8    85.7
-//         256 x 2      3.4     13.6    74.8
-//   5120: 512 x 2      3.8     17.4   129
-//         256 x 3      4.3     16.6   112
-//   8192: 512 x 2      4.1     22.8   167
-//         256 x 4      5.4     26.6   189
-//   12288: 512 x 3     5.2     36.0
-//         1024 x 2     5.6     44.3
+// which a CU holds more rows.  Microseconds with the residual, E4M3 output, three
+// sets of inputs in turn; (int8) where that output's order is another:
+//                     1 row    1792    3000    4096   16384   65536
+//   512:   64 x 1      2.5      3.7     4.5     5.1    13.1    45.8
+//   1024: 128 x 1      2.7      4.9     7.0     9.2    21.3    85.3 (93.3)
+//          64 x 2      3.2      5.0     7.3     9.3    22.5    86.9 (87.9)
+//   2048: 256 x 1      2.8      8.1    11.0    13.2    47.0 (51.0)   166 (176)
+//         128 x 2      3.4      8.8    12.1    14.2    47.0 (48.6)   165 (166)
+//   4096: 512 x 1      3.2     12.3    17.4    21.9    86.7
+//         256 x 2      3.6     13.3    18.2    22.7    86.0
+//   5120: 512 x 2      4.0     17.3    25.6    35.4   127
+//         256 x 3      4.5     16.4    23.4    31.3   108
+//   8192: 512 x 2      4.2     20.7    35.0    47.6   165
+//         256 x 4      5.5     23.5    41.4    54.7   185
+//        1024 x 1      4.2     21.8    36.2    48.5   182
+//   12288: 512 x 3     5.4     31.7    54.1    69.8
+//         1024 x 2     5.8     42.8    69.3    89.9
+//   16384: 1024 x 2    6.0     52.1    82.4   106
+//          512 x 4     6.4     45.5    71.1    91.7
+//   24576: 1024 x 3    7.6     79.1   121     162
+//   32768: 1024 x 4    9.2    106     166     217
+// Between 2049 and some 10000 rows of 1024 to 4096 the larger workgroups are up to
+// 11 % faster; without a residual the smaller ones gain most (65536 x 1024 E4M3
+// 55.7 / 47.2).  BF16 outputs are within 8 % either way, also at 16384 columns
+// (1024 x 2 47.2, 512 x 4 48.4 for 1792 rows), whose form was chosen for few rows.
 template <int FMT>
 hipError_t go_norm(const NormArgs& a, hipStream_t stream) {
     const bool few = a.t <= 2048;
